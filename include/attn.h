@@ -48,7 +48,7 @@
  *   Values      only metadata is validated, never values (scope notes: wrappers
  *               validate metadata but do not scan values); inputs must be
  *               finite. Every tensor's element count must fit a signed 32-bit
- *               index (same notes).
+ *               index (same notes); a 4-bit cache's pools may be larger.
  *   Errors      a negative attn_status_t; nothing is thrown across the ABI.
  *               On a validation error no kernel has been launched.
  */
@@ -83,7 +83,9 @@ typedef enum {
     ATTN_ERR_WORKSPACE = -8, /* workspace NULL or smaller than the size query returns */
     ATTN_ERR_CUDA = -9,      /* a CUDA runtime/driver call failed (launch, copy, ...) */
     ATTN_ERR_TIMEOUT = -10,  /* a kernel gave up on a bounded wait (see attn_last_device_status) */
-    ATTN_ERR_PATH = -11      /* the requested path cannot run this problem */
+    ATTN_ERR_PATH = -11,     /* the requested path cannot run this problem */
+    ATTN_ERR_SCALE = -12,    /* a factor of a 4-bit cache is not a positive power of two */
+    ATTN_ERR_ALIAS = -13     /* an output overlaps an input or another output */
 } attn_status_t;
 
 /* Kernel paths. AUTO picks: split-KV decode when (Hq/Hkv)*M <= 16 and the
@@ -383,6 +385,113 @@ ATTN_API int attn_decode_paged_fp8(const void* q, const void* k_pages, const voi
                                    float q_descale, float k_descale, float v_descale, attn_dtype_t out_dtype,
                                    void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- The 4-bit paged KV cache -------------------------------------------
+ *
+ * A cache that is 3.8 times smaller than a BF16 one (68 bytes instead of 256 a
+ * key or value at D = 128), for decode steps whose time is the reading of the
+ * cache: the tables that place requests in it (attn_page_plan, for every paged
+ * call), the write into it (attn_kv4_append), decode over it
+ * (attn_decode_paged_kv4) and its read back into 16 bits (attn_kv4_gather), with
+ * which the forward pass runs on it. An extension: the pages use 16-bit inputs.
+ *
+ * Format. Four pools, each laid out as attn_decode_paged's are:
+ *   k_codes, v_codes    bytes [num_pages, Hkv, page_size, D / 2]
+ *   k_scales, v_scales  E4M3 bytes [num_pages, Hkv, page_size, D / 32]
+ * all 16-byte aligned, D = 32, 64 or 128. A row is D / 32 groups of 32 elements,
+ * each with 32 codes n in 0..15 and a scale s; an element stands for
+ *   descale * s * (n - 8),
+ * exact in FP16 and BF16 times descale. k_descale and v_descale are one factor
+ * for a whole cache, positive powers of two (else ATTN_ERR_SCALE), to be given
+ * with the same value to every call; they move the range of the scales
+ * (2^-9 .. 448) to that of the data (1 suits magnitudes from 0.1 to a few
+ * hundred). Codes lie in a row in units of consecutive elements, 8 in a key row
+ * (one little-endian 32-bit word) and 4 in a value row (16 bits), the lowest
+ * element in the lowest bits; unit u of group i is unit u * (D / 32) + i of the
+ * row. A zeroed pool holds zeros.
+ * Pools may hold more bytes than 32 bits count; num_pages * page_size (the
+ * number of slots) must fit a signed 32-bit index, else ATTN_ERR_OVERFLOW.
+ * page_size is 16, 32, 64 or a multiple of 128. */
+
+/* Block tables and slots of one step of a serving loop, built on the device.
+ * Request b has cached_lens[b] keys in the cache (pages block_table[b, 0 ..
+ * ceil(cached / page_size)) hold them) and brings new_lens[b] more; the step's
+ * rows are those of request 0, then 1, and so on (negative lengths count as 0).
+ *   seq_lens[b] = cached_lens[b] + new_lens[b]
+ *   row_starts[b] = rows of the requests before b; row_starts[B] = all rows
+ *   block_table: the pages that request b needs and does not have are taken
+ *     from free_pages in order, requests in order, pages of a request in order;
+ *     only those entries are written.
+ *   slot_map[r], r < num_rows: page * page_size + offset of row r's key; -1 for
+ *     r >= row_starts[B] (a padded batch) and for a row without a page.
+ *   stats[3]: rows of the step; pages taken from free_pages; rows without a
+ *     slot: their page is behind max_pages or behind the end of free_pages (its
+ *     table entry is then -1), or the row is behind num_rows. Callers that can
+ *     run out check stats[2]; seq_lens counts such rows all the same.
+ * Sums that pass 2^31 - 1 are written as 2^31 - 1.
+ *   cached_lens, new_lens, seq_lens [B], free_pages [num_free], block_table
+ *   [B, max_pages], row_starts [B + 1], slot_map [num_rows], stats [3]: device
+ *   int32, 4-byte aligned. No output may overlap an input or another output
+ *   (ATTN_ERR_ALIAS): blocks read the ones while others write the others.
+ * Any page_size >= 1. One launch, no workspace. */
+ATTN_API int attn_page_plan(const int* cached_lens, const int* new_lens, const int* free_pages, int* block_table,
+                            int* seq_lens, int* row_starts, int* slot_map, int* stats, int B, int page_size,
+                            int max_pages, int num_free, int num_rows, void* stream);
+
+/* Quantizes T new key and value rows into the cache: row t of every KV head to
+ * slot slot_map[t] = page * page_size + offset; a slot outside [0, num_pages *
+ * page_size) skips the row (padding). A slot may be named once: with two rows
+ * for one slot its content is a mixture of theirs. Per group of 32 elements, with
+ * x the elements over descale:
+ *   s = E4M3(max|x| / 7.5), to nearest even, at most 448
+ *   n = 8 + clamp(round(x / s), -8, 7), halves away from zero; 8 where s = 0
+ * both exactly as written, for finite inputs, whatever their order of magnitude.
+ *   k, v: device [T, Hkv, D] of dtype (ATTN_BF16 / ATTN_FP16), 16-byte aligned,
+ *   the D elements of a head and the heads of a row contiguous; k_stride and
+ *   v_stride elements from one row to the next (at least Hkv * D, a multiple of
+ *   8), so that both may be parts of a wider projection's output.
+ *   slot_map: device int32 [T]. */
+ATTN_API int attn_kv4_append(const void* k, const void* v, const int* slot_map, void* k_codes, void* k_scales,
+                             void* v_codes, void* v_scales, int T, int Hkv, int D, long long k_stride,
+                             long long v_stride, int num_pages, int page_size, float k_descale, float v_descale,
+                             attn_dtype_t dtype, void* stream);
+
+/* Reads sequences back: k, v [B, Hkv, N, D] of dtype (device, 16-byte aligned)
+ * receive the first N rows of each sequence as the values they stand for, in the
+ * layout that attn_fwd takes; rows from min(seq_lens[b], max_pages * page_size)
+ * on, and rows of pages outside the pool, are zeros. Values beyond FP16's
+ * range (descale large) become infinite.
+ *   block_table, seq_lens: as attn_decode_paged. B and Hkv at most 65535. */
+ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                             const int* block_table, const int* seq_lens, void* k, void* v, int B, int Hkv, int N,
+                             int D, int num_pages, int page_size, int max_pages, float k_descale, float v_descale,
+                             attn_dtype_t dtype, void* stream);
+
+/* attn_decode_paged on a 4-bit cache, with attention sinks: q and o [B, Hq, M,
+ * D] of dtype, every other argument as attn_decode_paged, and
+ *   sinks: the first `sinks` keys of a sequence stay visible behind a sliding
+ *   window: row i sees the keys j <= p_i (causal) with j > p_i - window or
+ *   j < sinks. <= 0: none; without a window it changes nothing.
+ * The values of the cache enter the products exactly; the query is rounded to
+ * FP16 relative to its row's largest element and the probabilities to FP16, all
+ * sums are FP32. Pages need not be clean: rows behind a sequence's end may hold
+ * anything. A table entry outside [0, num_pages) reads a page of zeros.
+ * D is 32, 64 or 128 (else ATTN_ERR_HEADDIM); B * Hkv <= 65535 and at most
+ * 16 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
+ * to 8 grouped rows read the cache once, more in blocks of 16 rows; for many
+ * rows (a prefill over a cached context) attn_kv4_gather and attn_fwd are the
+ * faster way.
+ *   workspace: device memory of attn_decode_paged_kv4_workspace_bytes(...)
+ *   bytes, 16-byte aligned; NULL makes the call allocate it stream-ordered. */
+ATTN_API size_t attn_decode_paged_kv4_workspace_bytes(int B, int Hq, int Hkv, int M, int D, int page_size,
+                                                      int max_pages, int max_seq_len, int causal, int window,
+                                                      int sinks);
+ATTN_API int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                                   const void* v_scales, const int* block_table, const int* seq_lens, void* o,
+                                   int B, int Hq, int Hkv, int M, int D, int num_pages, int page_size,
+                                   int max_pages, int max_seq_len, int causal, int window, int sinks, float scale,
+                                   float k_descale, float v_descale, attn_dtype_t dtype, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
 /* Wide-row split softmax, the course's workshop A2 ("Intermediate and advanced
  * kernel workshops": three ordered kernels with per-call scratch; answer key,
  * A2 row and worked answer): y[i,:] = softmax(x[i,:]) for each row of a
@@ -439,7 +548,7 @@ ATTN_API int attn_selftest_prefill_abort(const void* q, const void* k, const voi
                                          int B, int Hq, int Hkv, int M, int N, int D, attn_dtype_t dtype,
                                          long long withhold_at, void* stream);
 
-/* Library ABI version (major*100 + minor). 200: attn_workspace_bytes takes the
+/* Library ABI version (major*100 + minor). 201 added the 4-bit paged cache. 200: attn_workspace_bytes takes the
  * seven size arguments of attn_fwd_ws (the former nine-argument query is now
  * attn_workspace_bytes_ex), attn_fwd_ws is added, and dtype arguments are
  * typed attn_dtype_t (same size and values as before). 101 added the E4M3

@@ -84,6 +84,17 @@ def lib() -> ctypes.CDLL:
             L.attn_bwd_workspace_bytes.restype = sz
             L.attn_bwd.argtypes = [vp] * 9 + [ci] * 8 + [cf, ci, vp, sz, vp]
             L.attn_bwd.restype = ci
+            L.attn_page_plan.argtypes = [vp] * 8 + [ci] * 5 + [vp]
+            L.attn_page_plan.restype = ci
+            cl = ctypes.c_longlong
+            L.attn_kv4_append.argtypes = [vp] * 7 + [ci] * 3 + [cl] * 2 + [ci] * 2 + [cf] * 2 + [ci, vp]
+            L.attn_kv4_append.restype = ci
+            L.attn_kv4_gather.argtypes = [vp] * 8 + [ci] * 7 + [cf] * 2 + [ci, vp]
+            L.attn_kv4_gather.restype = ci
+            L.attn_decode_paged_kv4_workspace_bytes.argtypes = [ci] * 11
+            L.attn_decode_paged_kv4_workspace_bytes.restype = sz
+            L.attn_decode_paged_kv4.argtypes = [vp] * 8 + [ci] * 12 + [cf] * 3 + [ci, vp, sz, vp]
+            L.attn_decode_paged_kv4.restype = ci
             L.attn_split_softmax_workspace_bytes.argtypes = [ci, ci, ci]
             L.attn_split_softmax_workspace_bytes.restype = sz
             L.attn_split_softmax.argtypes = [vp, vp, ci, ci, ci, ci, vp, sz, vp]
@@ -374,6 +385,154 @@ def attn_decode_paged_fp8(q, k_pages, v_pages, block_table, seq_lens, o, max_seq
                                      float(k_descale), float(v_descale), _DTYPES[o.dtype], _ptr(workspace),
                                      ws_bytes, _stream(stream))
     _check(st, "attn_decode_paged_fp8")
+
+
+# ---------------------------------------------------------------------------
+# The 4-bit paged KV cache
+# ---------------------------------------------------------------------------
+def kv4_cache(num_pages, Hkv, page_size, D, device="cuda"):
+    """Zeroed pools of a 4-bit cache: (k_codes, k_scales, v_codes, v_scales), codes uint8
+    [num_pages, Hkv, page_size, D/2], scales float8_e4m3fn [num_pages, Hkv, page_size, D/32]."""
+    def pools():
+        codes = torch.zeros((num_pages, Hkv, page_size, D // 2), dtype=torch.uint8, device=device)
+        scales = torch.zeros((num_pages, Hkv, page_size, D // 32), dtype=torch.uint8, device=device)
+        return codes, scales.view(torch.float8_e4m3fn)
+
+    return pools() + pools()
+
+
+def _on_current_device(*tensors) -> None:
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"tensors are on {dev} and {t.device}: one device is wanted")
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}: they must be on the current CUDA device")
+
+
+def _int32(**tensors) -> None:
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+
+
+def _kv4_dims(k_codes, k_scales, v_codes, v_scales):
+    if k_codes.dim() != 4 or k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
+        raise ValueError("codes are uint8 [num_pages, Hkv, page_size, D/2]")
+    num_pages, Hkv, page_size, half = k_codes.shape
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes must have one shape")
+    want = (num_pages, Hkv, page_size, half // 16)
+    for t in (k_scales, v_scales):
+        if tuple(t.shape) != want or t.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"scales are float8_e4m3fn [num_pages, Hkv, page_size, D/32] = {want}")
+    for t in (k_codes, k_scales, v_codes, v_scales):
+        if not t.is_contiguous():
+            raise ValueError("the cache's tensors must be contiguous")
+    return num_pages, Hkv, page_size, 2 * half
+
+
+def attn_page_plan(cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats, page_size,
+                   stream=None) -> None:
+    """C-ABI ``attn_page_plan``: takes pages for the new keys of every request (``block_table``, updated in
+    place) and writes ``seq_lens`` [B], ``row_starts`` [B+1], ``slot_map`` [rows, padding included] and
+    ``stats`` [3]: rows, pages taken, rows without a slot. All int32 device tensors."""
+    _int32(cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages, block_table=block_table,
+           seq_lens=seq_lens, row_starts=row_starts, slot_map=slot_map, stats=stats)
+    B = cached_lens.numel()
+    if cached_lens.dim() != 1 or new_lens.shape != (B,) or seq_lens.shape != (B,) or row_starts.shape != (B + 1,):
+        raise ValueError("cached_lens, new_lens and seq_lens are [B], row_starts is [B+1]")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages]")
+    if free_pages.dim() != 1 or slot_map.dim() != 1 or stats.shape != (3,):
+        raise ValueError("free_pages and slot_map are one-dimensional, stats is [3]")
+    _on_current_device(stats, cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map)
+    st = lib().attn_page_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_pages), _ptr(block_table), _ptr(seq_lens),
+                              _ptr(row_starts), _ptr(slot_map), _ptr(stats), B, int(page_size), block_table.shape[1],
+                              free_pages.numel(), slot_map.numel(), _stream(stream))
+    _check(st, "attn_page_plan")
+
+
+def attn_kv4_append(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, k_descale=1.0, v_descale=1.0,
+                    stream=None) -> None:
+    """C-ABI ``attn_kv4_append``: quantizes the rows of ``k`` and ``v`` [T, Hkv, D] (BF16 or FP16; heads
+    contiguous, rows any distance apart) into the cache at ``slot_map`` [T] (-1 skips a row)."""
+    num_pages, Hkv, page_size, D = _kv4_dims(k_codes, k_scales, v_codes, v_scales)
+    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, D) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [T, {Hkv}, {D}]")
+    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
+        raise ValueError("k and v must share one dtype, bfloat16 or float16")
+    for t in (k, v):
+        if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D)):
+            raise ValueError("the elements of a head and the heads of a row must be contiguous")
+    T = k.shape[0]
+    _int32(slot_map=slot_map)
+    if slot_map.shape != (T,):
+        raise ValueError("slot_map must be [T]")
+    _on_current_device(k, v, slot_map, k_codes, k_scales, v_codes, v_scales)
+    st = lib().attn_kv4_append(_ptr(k), _ptr(v), _ptr(slot_map), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
+                               _ptr(v_scales), T, Hkv, D, k.stride(0), v.stride(0), num_pages, page_size,
+                               float(k_descale), float(v_descale), _DTYPES[k.dtype], _stream(stream))
+    _check(st, "attn_kv4_append")
+
+
+def attn_kv4_gather(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, k, v, k_descale=1.0, v_descale=1.0,
+                    stream=None) -> None:
+    """C-ABI ``attn_kv4_gather``: writes the first N rows of every sequence into ``k`` and ``v``
+    [B, Hkv, N, D] (BF16 or FP16) as the values the cache stands for; zeros behind a sequence's end."""
+    num_pages, Hkv, page_size, D = _kv4_dims(k_codes, k_scales, v_codes, v_scales)
+    if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != D or v.shape != k.shape:
+        raise ValueError(f"k and v must be [B, {Hkv}, N, {D}]")
+    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
+        raise ValueError("k and v must share one dtype, bfloat16 or float16")
+    if not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("k and v must be contiguous")
+    B, _, N, _ = k.shape
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    _on_current_device(k, v, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
+    st = lib().attn_kv4_gather(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(block_table),
+                               _ptr(seq_lens), _ptr(k), _ptr(v), B, Hkv, N, D, num_pages, page_size,
+                               block_table.shape[1], float(k_descale), float(v_descale), _DTYPES[k.dtype],
+                               _stream(stream))
+    _check(st, "attn_kv4_gather")
+
+
+def attn_decode_paged_kv4_workspace_bytes(B, Hq, Hkv, M, D, page_size, max_pages, max_seq_len, causal=True, window=0,
+                                          sinks=0) -> int:
+    return int(lib().attn_decode_paged_kv4_workspace_bytes(B, Hq, Hkv, M, D, page_size, max_pages, max_seq_len,
+                                                           int(bool(causal)), int(window), int(sinks)))
+
+
+def attn_decode_paged_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, o, max_seq_len, causal=True,
+                          window=0, sinks=0, scale=0.0, k_descale=1.0, v_descale=1.0, workspace=None,
+                          stream=None) -> None:
+    """C-ABI ``attn_decode_paged_kv4``: decode over a 4-bit paged cache; writes ``o`` in place. With a
+    sliding ``window``, the first ``sinks`` keys of a sequence stay visible. ``workspace`` None lets the
+    library allocate it stream-ordered."""
+    num_pages, Hkv, page_size, D = _kv4_dims(k_codes, k_scales, v_codes, v_scales)
+    if q.dim() != 4 or q.shape[3] != D or o.shape != q.shape:
+        raise ValueError(f"q and o must be [B, Hq, M, {D}]")
+    if q.dtype not in (torch.bfloat16, torch.float16) or o.dtype != q.dtype:
+        raise ValueError("q and o must share one dtype, bfloat16 or float16")
+    if not q.is_contiguous() or not o.is_contiguous():
+        raise ValueError("q and o must be contiguous")
+    B, Hq, M, _ = q.shape
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    _on_current_device(q, o, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
+    ws_bytes = 0
+    if workspace is not None:
+        _on_current_device(q, workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = lib().attn_decode_paged_kv4(_ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+                                     _ptr(block_table), _ptr(seq_lens), _ptr(o), B, Hq, Hkv, M, D, num_pages,
+                                     page_size, block_table.shape[1], int(max_seq_len), int(bool(causal)),
+                                     int(window), int(sinks), float(scale or 0.0), float(k_descale), float(v_descale),
+                                     _DTYPES[q.dtype], _ptr(workspace), ws_bytes, _stream(stream))
+    _check(st, "attn_decode_paged_kv4")
 
 
 def attn_split_softmax_workspace_bytes(M, N, chunk=1024) -> int:

@@ -408,6 +408,8 @@ const char* attn_strerror(int status) {
         case ATTN_ERR_CUDA: return "CUDA call failed";
         case ATTN_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
         case ATTN_ERR_PATH: return "the requested path cannot run this problem";
+        case ATTN_ERR_SCALE: return "a 4-bit cache's factor is not a positive power of two";
+        case ATTN_ERR_ALIAS: return "an output overlaps an input or another output";
         default: return "unknown status";
     }
 }
@@ -421,7 +423,7 @@ int attn_last_device_status(void* stream) {
     return word ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }
 
-int attn_version(void) { return 200; }
+int attn_version(void) { return 201; }
 
 }  // extern "C"
 

@@ -1,0 +1,292 @@
+// The 4-bit paged KV cache: the write of new rows into it and its read back into
+// 16 bits (its format is in attn_kv4.h; the attention that reads it in
+// attn_kv4_decode.cu).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn.h"
+#include "attn_internal.h"
+#include "attn_kv4.h"
+
+namespace attn {
+namespace {
+
+constexpr int64_t kI32Max = 2147483647LL;
+constexpr int kThreads = 256;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+template <typename T>
+__device__ __forceinline__ float2 to_float2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 to_float2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 to_float2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t from_float2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t from_float2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+template <>
+__device__ __forceinline__ uint32_t from_float2<__half>(float lo, float hi) {
+    const __half2 t = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+}
+
+// ---------------------------------------------------------------------------
+// append: one thread takes 8 elements of a key row and the same 8 of the value
+// row; the 4 threads of a group share its maximum.
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+    const void* k;
+    const void* v;
+    const int* slots;
+    Kv4Cache c;
+    long long k_stride, v_stride;  // elements from one row of the batch to the next
+    int T, Hkv;
+    float k_inv, v_inv;  // 1 / descale (a power of two)
+};
+
+// 8 elements -> 8 codes in one word (lowest element in the lowest bits) and the
+// group's scale byte. Exact with respect to the format's definition: the quotient
+// x / s is taken as x * r with r = (1 / s)(1 + 2^-16). A tie between two codes is
+// pushed to the larger magnitude (r exceeds 1 / s by 2^-16 and rounding errs by
+// less than 2^-22), and nothing else crosses a border: x has 11 significant bits
+// and s times a border 8, so a quotient that is not on a border is at least 2^-11
+// of it away.
+template <typename T>
+__device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_t* scale) {
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    float x[8];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = to_float2<T>(words[i]);
+        x[2 * i] = t.x * inv;
+        x[2 * i + 1] = t.y * inv;
+        top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // division rounds correctly, so a maximum that lies on a border between two scales is seen there
+    const uint32_t s = __nv_cvt_float_to_fp8(__fdiv_rn(top, 7.5f), __NV_SATFINITE, __NV_E4M3);
+    const float sf = e4m3_value(s);
+    const float r = sf > 0.f ? __fdiv_rn(1.0f, sf) * (1.0f + 0x1p-16f) : 0.f;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = fminf(fmaxf(x[i] * r, -8.0f), 7.0f);
+        // 1.5 * 2^23 + 8: the integer part of the sum sits in its low bits
+        codes |= (__float_as_uint(t + 12582920.0f) & 15u) << (4 * i);
+    }
+    *scale = s;
+    return codes;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
+    constexpr int NG = D / kKv4Group;
+    constexpr int U = D / 8;  // threads of a row
+    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long row = idx / U;  // row of the batch times Hkv plus the head
+    const int u = (int)(idx % U);
+    const long long rows = (long long)a.T * a.Hkv;
+    const bool in = row < rows;
+    const int t = in ? (int)(row / a.Hkv) : 0, h = in ? (int)(row % a.Hkv) : 0;
+    const int slot = in ? __ldg(a.slots + t) : -1;
+    const bool live = slot >= 0 && slot < (long long)a.c.num_pages * a.c.page_size;
+    uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
+    if (live) {
+        wk = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + h * D + u * 8));
+        wv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + h * D + u * 8));
+    }
+    uint32_t sk, sv;
+    const uint32_t ck = quantize8<T>(wk, a.k_inv, &sk);
+    const uint32_t cv = quantize8<T>(wv, a.v_inv, &sv);
+    const int i = u / 4, c = u % 4;  // group, and which 8 of its 32 elements
+    // value units of 4 elements: two groups' units at one position make a word, so
+    // the threads of groups i and i ^ 1 trade one unit each
+    int vword;
+    uint32_t vbits;
+    if (NG > 1) {
+        const bool odd = i & 1;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? (cv & 0xFFFFu) : (cv >> 16), 4);
+        vbits = odd ? (got | (cv & 0xFFFF0000u)) : ((cv & 0xFFFFu) | (got << 16));
+        vword = ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2;
+    } else {
+        vbits = cv;
+        vword = c;
+    }
+    if (!live) return;
+    const int ps = a.c.page_size;
+    const size_t at = ((size_t)(slot / ps) * a.Hkv + h) * ps + slot % ps;
+    reinterpret_cast<uint32_t*>(a.c.k_codes + at * (D / 2))[c * NG + i] = ck;
+    reinterpret_cast<uint32_t*>(a.c.v_codes + at * (D / 2))[vword] = vbits;
+    if (c == 0) {
+        a.c.k_scales[at * NG + i] = (uint8_t)sk;
+        a.c.v_scales[at * NG + i] = (uint8_t)sv;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// gather: one thread writes 8 elements of a key row and the same 8 of the value row
+// ---------------------------------------------------------------------------
+struct GatherArgs {
+    Kv4Cache c;
+    const int* table;
+    const int* lens;
+    void* k;
+    void* v;
+    int Hkv, N, max_pages;
+    float k_scale, v_scale;
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 expand8(uint32_t codes, float s) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float lo = (float)(int)((codes >> (8 * i)) & 15u) - 8.0f;
+        const float hi = (float)(int)((codes >> (8 * i + 4)) & 15u) - 8.0f;
+        w[i] = from_float2<T>(lo * s, hi * s);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a) {
+    constexpr int NG = D / kKv4Group;
+    constexpr int U = D / 8;
+    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const int j = (int)(idx / U), u = (int)(idx % U);
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int i = u / 4, c = u % 4;
+    const bool odd = i & 1;
+    const bool in = idx < (long long)a.N * U;
+    uint32_t ck = 0, cv = 0;
+    float sk = 0.f, sv = 0.f;  // a row behind the sequence, or on a page outside the pool, is zeros
+    const int ps = a.c.page_size;
+    if (in && j < __ldg(a.lens + b) && j / ps < a.max_pages) {
+        const int page = __ldg(a.table + (size_t)b * a.max_pages + j / ps);
+        if (page >= 0 && page < a.c.num_pages) {
+            const size_t at = ((size_t)page * a.Hkv + h) * ps + j % ps;
+            ck = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_codes + at * (D / 2)) + c * NG + i);
+            const int vword = NG > 1 ? ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2 : c;
+            cv = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_codes + at * (D / 2)) + vword);
+            sk = e4m3_value(__ldg(a.c.k_scales + at * NG + i)) * a.k_scale;
+            sv = e4m3_value(__ldg(a.c.v_scales + at * NG + i)) * a.v_scale;
+        }
+    }
+    if (NG > 1) {  // the inverse of the append kernel's trade
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? (cv & 0xFFFFu) : (cv >> 16), 4);
+        cv = odd ? (got | (cv & 0xFFFF0000u)) : ((cv & 0xFFFFu) | (got << 16));
+    }
+    if (!in) return;
+    const size_t out = (((size_t)b * a.Hkv + h) * a.N + j) * U + u;
+    reinterpret_cast<uint4*>(a.k)[out] = expand8<T>(ck, sk);
+    reinterpret_cast<uint4*>(a.v)[out] = expand8<T>(cv, sv);
+}
+
+template <typename T>
+cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
+    const long long n = (long long)a.T * a.Hkv * (D / 8);
+    const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
+    switch (D) {
+        case 32: kv4_append_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
+        case 64: kv4_append_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;
+        default: kv4_append_kernel<T, 128><<<grid, kThreads, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_gather(const GatherArgs& a, int B, int D, cudaStream_t s) {
+    const long long n = (long long)a.N * (D / 8);
+    const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), (unsigned)a.Hkv, (unsigned)B);
+    switch (D) {
+        case 32: kv4_gather_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
+        case 64: kv4_gather_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;
+        default: kv4_gather_kernel<T, 128><<<grid, kThreads, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// The pools hold 64-bit many bytes; their slots are numbered in 32 bits.
+int kv4_validate_cache(const Kv4Cache& c, int Hkv, int D) {
+    if (c.num_pages < 0 || Hkv < 0 || D <= 0) return ATTN_ERR_SHAPE;
+    if (!kv4_page_size(c.page_size)) return ATTN_ERR_SHAPE;
+    if (!kv4_head_dim(D)) return ATTN_ERR_HEADDIM;
+    if ((int64_t)c.num_pages * c.page_size > kI32Max) return ATTN_ERR_OVERFLOW;
+    if (c.num_pages > 0 && Hkv > 0 && (!c.k_codes || !c.k_scales || !c.v_codes || !c.v_scales)) return ATTN_ERR_NULL;
+    if (!aligned(c.k_codes, 16) || !aligned(c.k_scales, 16) || !aligned(c.v_codes, 16) || !aligned(c.v_scales, 16))
+        return ATTN_ERR_ALIGN;
+    return ATTN_OK;
+}
+
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+int attn_kv4_append(const void* k, const void* v, const int* slot_map, void* k_codes, void* k_scales, void* v_codes,
+                    void* v_scales, int T, int Hkv, int D, long long k_stride, long long v_stride, int num_pages,
+                    int page_size, float k_descale, float v_descale, attn_dtype_t dtype, void* stream) {
+    if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;
+    if (T < 0) return ATTN_ERR_SHAPE;
+    const Kv4Cache c{static_cast<uint8_t*>(k_codes), static_cast<uint8_t*>(k_scales), static_cast<uint8_t*>(v_codes),
+                     static_cast<uint8_t*>(v_scales), num_pages, page_size};
+    const int rc = kv4_validate_cache(c, Hkv, D);
+    if (rc != ATTN_OK) return rc;
+    const int64_t row = (int64_t)Hkv * D;
+    if ((int64_t)T * row > kI32Max) return ATTN_ERR_OVERFLOW;
+    if (T > 1 && (k_stride < row || v_stride < row)) return ATTN_ERR_SHAPE;
+    if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
+    if (T == 0 || Hkv == 0 || num_pages == 0) return ATTN_OK;
+    if (!k || !v || !slot_map) return ATTN_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4) || (T > 1 && (k_stride % 8 || v_stride % 8)))
+        return ATTN_ERR_ALIGN;
+    const AppendArgs a{k, v, slot_map, c, k_stride, v_stride, T, Hkv, 1.0f / k_descale, 1.0f / v_descale};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == ATTN_BF16 ? launch_append<__nv_bfloat16>(a, D, s) : launch_append<__half>(a, D, s));
+}
+
+int attn_kv4_gather(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                    const int* block_table, const int* seq_lens, void* k, void* v, int B, int Hkv, int N, int D,
+                    int num_pages, int page_size, int max_pages, float k_descale, float v_descale, attn_dtype_t dtype,
+                    void* stream) {
+    if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_DTYPE;
+    if (B < 0 || N < 0 || max_pages < 0) return ATTN_ERR_SHAPE;
+    const auto mut = [](const void* p) { return static_cast<uint8_t*>(const_cast<void*>(p)); };
+    const Kv4Cache c{mut(k_codes), mut(k_scales), mut(v_codes), mut(v_scales), num_pages, page_size};
+    const int rc = kv4_validate_cache(c, Hkv, D);
+    if (rc != ATTN_OK) return rc;
+    // the grid holds a KV head per y and a sequence per z index
+    if ((int64_t)B * Hkv * N * D > kI32Max || (int64_t)B * max_pages > kI32Max || B > 65535 || Hkv > 65535)
+        return ATTN_ERR_OVERFLOW;
+    if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
+    if ((int64_t)B * Hkv * N == 0) return ATTN_OK;
+    if (!k || !v || !seq_lens || (max_pages > 0 && !block_table)) return ATTN_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq_lens, 4) || !aligned(block_table, 4)) return ATTN_ERR_ALIGN;
+    const GatherArgs a{c, block_table, seq_lens, k, v, Hkv, N, max_pages, k_descale, v_descale};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == ATTN_BF16 ? launch_gather<__nv_bfloat16>(a, B, D, s)
+                                          : launch_gather<__half>(a, B, D, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,569 @@
+"""The 4-bit paged cache on the GPU against its definition in 64 bits: the write
+into it (exact), the read back (exact), the tables of a step (exact), decode
+attention over it (within a bound derived per element in kv4_reference), and a
+serving loop of them together."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_reference as ref
+import streaming_attention_gb300 as sa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def model_rows(rng, shape, which):
+    """Keys with a few strong channels, values around half a unit."""
+    x = rng.normal(size=shape)
+    return x * (0.7 + 2.0 * (np.arange(shape[-1]) % 19 == 3)) if which == "k" else x * 0.5
+
+
+def make_cache(rng, pages, Hkv, ps, D, kd=1.0, vd=0.125):
+    """Pools filled with quantized rows (by the reference): device tensors and numpy."""
+    dev, host = [], []
+    for which, d in (("k", kd), ("v", vd)):
+        codes, byte, _ = ref.quantize(model_rows(rng, (pages, Hkv, ps, D), which), d)
+        packed = ref.pack(codes, which)
+        host += [packed, byte]
+        dev += [torch.from_numpy(packed).to(DEV), torch.from_numpy(byte).to(DEV).view(torch.float8_e4m3fn)]
+    return dev, host
+
+
+def make_table(rng, lens, ps, pages, width=None):
+    need = [-(-n // ps) for n in lens]
+    width = width or max(max(need), 1)
+    ids = rng.permutation(pages)
+    table, at = np.zeros((len(lens), width), np.int32), 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    return table
+
+
+def run_decode(q, dev, table, lens, cap, causal=True, window=0, sinks=0, scale=0.0, kd=1.0, vd=0.125, ws=True):
+    B, Hq, M, D = q.shape
+    o = torch.full_like(q, float("nan"))
+    work = None
+    if ws:
+        n = sa.attn_decode_paged_kv4_workspace_bytes(B, Hq, dev[0].shape[1], M, D, dev[0].shape[2], table.shape[1], cap,
+                                                     causal, window, sinks)
+        work = torch.full((max(n, 1),), 255, dtype=torch.uint8, device=DEV)
+    sa.attn_decode_paged_kv4(q, *dev, i32(table), i32(lens), o, cap, causal, window, sinks, scale, kd, vd, work)
+    torch.cuda.synchronize()
+    return o
+
+
+def check_decode(o, q, host, table, lens, cap, causal=True, window=0, sinks=0, scale=0.0, kd=1.0, vd=0.125):
+    ps = host[0].shape[2]
+    ks = ref.sequences(table, lens, host[0], host[1], "k", kd, ps, cap)
+    vs = ref.sequences(table, lens, host[2], host[3], "v", vd, ps, cap)
+    got, qq = ref.f64(o), ref.f64(q)
+    for b in range(len(lens)):
+        want, bound = ref.attention(qq[b], ks[b], vs[b], causal, window, sinks, scale, q.dtype)
+        err = np.abs(got[b] - want)
+        worst = (err / np.maximum(bound, 1e-300)).max() if err.size else 0
+        assert np.isfinite(got[b]).all() and (err <= bound).all(), f"sequence {b}: {worst:.3g} of the bound"
+
+
+def case(seed, lens, Hq, Hkv, M, D, ps, dtype, spare=3, width=None):
+    rng = np.random.default_rng(seed)
+    pages = sum(-(-n // ps) for n in lens) + spare
+    dev, host = make_cache(rng, pages, Hkv, ps, D)
+    table = make_table(rng, lens, ps, pages, width)
+    q = torch.from_numpy(rng.normal(size=(len(lens), Hq, M, D))).to(dtype).to(DEV)
+    return q, dev, host, table
+
+
+# ---------------------------------------------------------------------------
+# append and gather
+# ---------------------------------------------------------------------------
+def border_rows(D, dtype, descale):
+    """Rows whose elements lie on and next to the borders between codes and whose maxima lie on and
+    next to the borders between scales."""
+    rows = []
+    for s in (1.0, 1.125, 0.8125, 2.0 ** -9, 3 * 2.0 ** -9, 448.0, 7 * 2.0 ** -7):
+        x = np.zeros(D)
+        ties = np.array([(n + 0.5) * s for n in range(-8, 8)])
+        t = torch.from_numpy(ties * descale).to(dtype)
+        up = (t.view(torch.int16) + 1).view(dtype)
+        down = (t.view(torch.int16) - 1).view(dtype)
+        x[:16] = t.double().numpy()
+        x[16:32] = np.where(np.arange(16) % 2 == 0, up.double().numpy(), down.double().numpy())
+        rows.append(x)
+    for k in range(9):  # maxima 7.5 times a border between two scales, and its neighbours
+        top = torch.tensor(7.5 * (1 + (2 * k + 1) / 16) * 2.0 ** -3 * descale).to(dtype)
+        for step in (-1, 0, 1):
+            x = np.full(D, 0.01 * descale)
+            x[D - 1] = float((top.view(torch.int16) + step).view(dtype))
+            rows.append(x)
+    rows.append(np.zeros(D))
+    rows.append(np.full(D, 2.0 ** -12 * descale))  # its scale rounds to zero
+    rows.append(np.full(D, -6000.0 * descale))     # behind the largest scale: saturates
+    return np.stack(rows)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("kd,vd", [(1.0, 0.125), (0.0625, 4.0)])
+def test_append_and_gather_are_exact(D, dtype, kd, vd):
+    rng = np.random.default_rng(D)
+    Hkv, ps, pages, T = 3, 16, 9, 83
+    k = model_rows(rng, (T, Hkv, D), "k")
+    v = model_rows(rng, (T, Hkv, D), "v")
+    bk, bv = border_rows(D, dtype, kd), border_rows(D, dtype, vd)
+    k[:len(bk), 1], v[:len(bv), 2] = bk, bv
+    # K and V as parts of a wider projection's output
+    qkv = torch.zeros(T, 5 + 2 * Hkv, D, dtype=dtype, device=DEV)
+    qkv[:, 5:5 + Hkv] = torch.from_numpy(k)
+    qkv[:, 5 + Hkv:] = torch.from_numpy(v)
+    kk, vv = qkv[:, 5:5 + Hkv], qkv[:, 5 + Hkv:]
+    slots = rng.permutation(pages * ps)[:T].astype(np.int32)
+    slots[70], slots[71], slots[72] = -1, pages * ps, 2 ** 31 - 1  # skipped rows
+    dev, host = make_cache(rng, pages, Hkv, ps, D)
+    sa.attn_kv4_append(kk, vv, torch.from_numpy(slots).to(DEV), *dev, kd, vd)
+    torch.cuda.synchronize()
+    for x, which, d, n in ((ref.f64(kk), "k", kd, 0), (ref.f64(vv), "v", vd, 2)):
+        codes, byte, val = ref.quantize(x, d)
+        packed, scales = host[n].copy(), host[n + 1].copy()
+        for t, slot in enumerate(slots):
+            if 0 <= slot < pages * ps:
+                packed[slot // ps, :, slot % ps] = ref.pack(codes[t], which)
+                scales[slot // ps, :, slot % ps] = byte[t]
+        assert np.array_equal(bytes_np(dev[n]), packed), which
+        assert np.array_equal(bytes_np(dev[n + 1]), scales), which
+    # read back: sequences over shuffled pages, one with a page outside the pool, one empty
+    table = np.array([[4, 1, 8], [7, -1, 0], [2, pages, 3], [5, 6, 6]], np.int32)
+    lens = [41, 48, 30, 0]
+    out_k = torch.full((4, Hkv, 50, D), float("nan"), dtype=dtype, device=DEV)
+    out_v = out_k.clone()
+    sa.attn_kv4_gather(*dev, i32(table), i32(lens), out_k, out_v, kd, vd)
+    torch.cuda.synchronize()
+    for out, which, d, n in ((out_k, "k", kd, 0), (out_v, "v", vd, 2)):
+        seqs = ref.sequences(table, lens, bytes_np(dev[n]), bytes_np(dev[n + 1]), which, d, ps)
+        for b, L in enumerate(lens):
+            want = np.zeros((Hkv, 50, D))
+            want[:, :L] = seqs[b]
+            assert np.array_equal(ref.f64(out[b]), want), (which, b)
+
+
+def bytes_np(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def test_gather_lengths_past_the_table_and_short_outputs():
+    rng = np.random.default_rng(8)
+    dev, host = make_cache(rng, 6, 2, 32, 64)
+    table = np.array([[3, 1], [5, 0]], np.int32)
+    for N, lens in ((100, [1000, -4]), (17, [64, 20]), (1, [1, 64])):
+        k = torch.full((2, 2, N, 64), float("nan"), dtype=BF16, device=DEV)
+        v = k.clone()
+        sa.attn_kv4_gather(*dev, i32(table), i32(lens), k, v, 1.0, 0.125)
+        torch.cuda.synchronize()
+        ks = ref.sequences(table, lens, host[0], host[1], "k", 1.0, 32)
+        for b in range(2):
+            want = np.zeros((2, N, 64))
+            n = min(N, ks[b].shape[1])
+            want[:, :n] = ks[b][:, :n]
+            assert np.array_equal(ref.f64(k[b]), want)
+
+
+def test_append_one_row_of_one_head_any_stride():
+    """A single row's stride is not read; a single head's neither."""
+    rng = np.random.default_rng(9)
+    dev, _ = make_cache(rng, 2, 1, 16, 32)
+    x = torch.from_numpy(rng.normal(size=(1, 1, 32))).to(FP16).to(DEV)
+    k = torch.as_strided(x, (1, 1, 32), (3, 5, 1))
+    sa.attn_kv4_append(k, x, i32([17]), *dev)
+    torch.cuda.synchronize()
+    codes, byte, _ = ref.quantize(ref.f64(x), 1.0)
+    assert np.array_equal(bytes_np(dev[0])[1, 0, 1], ref.pack(codes, "k")[0, 0])
+    assert np.array_equal(bytes_np(dev[3])[1, 0, 1], byte[0, 0])
+
+
+# ---------------------------------------------------------------------------
+# tables of a step
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,ps,most,pad,short", [
+    (1, 16, 40, 0, 0), (7, 16, 100, 5, 0), (64, 32, 2, 0, 0), (1000, 16, 60, 33, 0), (1024, 64, 9, 1, 0),
+    (1025, 16, 3, 0, 0), (3000, 128, 300, 64, 0), (20, 16, 200, 0, 30), (20, 7, 50, -90, 4), (5, 1, 9, 2, 0)])
+def test_page_plan(B, ps, most, pad, short):
+    """pad < 0: slot_map too short for the step; short: pages missing from the free list."""
+    rng = np.random.default_rng(B)
+    cached = rng.integers(0, 5 * ps, B)
+    cached[rng.random(B) < 0.3] = 0
+    new = rng.integers(0, most + 1, B)
+    cached[0], new[0] = ps, 1  # a full page, then one key more
+    if B > 2:
+        cached[1], new[1], cached[2], new[2] = -3, -1, 0, ps
+    width = int(max(-(-(cached + new) // ps)))
+    if short:
+        width = max(width - 2, 1)  # some requests outgrow the table
+    have = np.minimum(-(-np.maximum(cached, 0) // ps), width)
+    need = int((np.minimum(-(-(np.maximum(cached, 0) + np.maximum(new, 0)) // ps), width) - have).sum())
+    ids = rng.permutation(int(have.sum()) + need + 7)
+    table, at = np.full((B, width), -7), 0
+    for b in range(B):
+        table[b, :have[b]] = ids[at:at + have[b]]
+        at += have[b]
+    free = ids[at:at + max(need - short, 0)]
+    T = max(int(np.maximum(new, 0).sum()) + pad, 0)
+    want = ref.plan(cached.tolist(), new.tolist(), free.tolist(), table, ps, T)
+    d_table = i32(table)
+    out = [torch.full((n,), -9, dtype=torch.int32, device=DEV) for n in (B, B + 1, T, 3)]
+    sa.attn_page_plan(i32(cached), i32(new), i32(free), d_table, *out, ps)
+    torch.cuda.synchronize()
+    assert d_table.tolist() == want[0]
+    for got, w in zip(out, want[1:]):
+        assert got.tolist() == w
+
+
+def test_page_plan_of_nothing_and_of_huge_lengths():
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    starts, slots, stats = i32([-9]), i32([5, 5]), i32([9, 9, 9])
+    sa.attn_page_plan(e, e.clone(), e.clone(), torch.empty((0, 4), dtype=torch.int32, device=DEV), e.clone(), starts,
+                      slots, stats, 16)
+    torch.cuda.synchronize()
+    assert starts.tolist() == [0] and slots.tolist() == [-1, -1] and stats.tolist() == [0, 0, 0]
+    big = 2 ** 31 - 1  # sums of lengths pass 32 bits: saturated, nothing out of range is touched
+    table, lens, starts = i32([[-7, -7]] * 3), i32([0] * 3), i32([0] * 4)
+    sa.attn_page_plan(i32([big, 5, 0]), i32([big, 3, big]), i32([4, 2]), table, lens, starts, slots, stats, 16)
+    torch.cuda.synchronize()
+    assert lens.tolist() == [big, 8, big] and starts.tolist() == [0, big, big, big]
+    assert slots.tolist() == [-1, -1] and stats.tolist() == [big, 2, big]
+    assert table.tolist() == [[-7, -7], [-7, -7], [4, 2]]
+
+
+# ---------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("ps", [16, 32, 64, 128, 384])
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (True, 300, 0), (True, 130, 5), (False, 0, 0),
+                                                 (False, 200, 70)])
+def test_decode_ragged(D, ps, causal, window, sinks):
+    lens = [1000, 1, 0, 1024, 517, 15, 16, 17]
+    dtype = FP16 if ps in (32, 128) else BF16
+    q, dev, host, table = case(D + ps, lens, 8, 2, 1, D, ps, dtype)
+    o = run_decode(q, dev, table, lens, 1024, causal, window, sinks)
+    check_decode(o, q, host, table, lens, 1024, causal, window, sinks)
+    assert torch.all(o[2] == 0)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,M", [(128, 3, 3, 1), (128, 8, 1, 1), (64, 9, 1, 1), (128, 16, 2, 2), (32, 4, 4, 8),
+                                        (128, 4, 2, 9), (128, 40, 1, 1), (64, 6, 2, 7), (128, 14, 2, 5)])
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (True, 40, 3), (False, 0, 0)])
+def test_decode_grouped_and_speculative_rows(D, Hq, Hkv, M, causal, window, sinks):
+    """Rows per KV head from 1 to 40; sequences shorter than M leave rows with no visible key."""
+    lens = [301, 3, 640, 70, 0]
+    q, dev, host, table = case(Hq * M, lens, Hq, Hkv, M, D, 32, FP16 if M % 2 else BF16)
+    o = run_decode(q, dev, table, lens, 640, causal, window, sinks)
+    check_decode(o, q, host, table, lens, 640, causal, window, sinks)
+    if causal and M > 3:
+        assert torch.all(o[1, :, :M - 3] == 0)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 200), (63, 64), (64, 65), (200, 16), (5000, 9), (17, 900),
+                                          (2 ** 31 - 1, 2 ** 31 - 1), (40, -3), (-1, 5)])
+def test_decode_windows_and_sinks(window, sinks):
+    """Windows that start inside, at and behind the sinks; sinks and windows longer than the sequence."""
+    lens = [900, 64, 65, 128, 1, 333]
+    q, dev, host, table = case(77, lens, 4, 2, 2, 64, 16, BF16)
+    o = run_decode(q, dev, table, lens, 900, True, window, sinks)
+    check_decode(o, q, host, table, lens, 900, True, window, max(sinks, 0))
+
+
+def test_decode_long_context_splits_and_one_split():
+    for lens, Hq, Hkv, M, window in (([20000], 4, 1, 1, 0), ([9000, 4097], 16, 8, 1, 0), ([300] * 90, 8, 8, 1, 0),
+                                     ([7001], 32, 2, 1, 2222)):
+        q, dev, host, table = case(len(lens), lens, Hq, Hkv, M, 128, 16, BF16)
+        o = run_decode(q, dev, table, lens, max(lens), True, window, 4)
+        check_decode(o, q, host, table, lens, max(lens), True, window, 4)
+
+
+@pytest.mark.parametrize("scale", [0.3, -0.05, 2.0])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_decode_scales_and_workspace_of_the_library(scale, dtype):
+    lens = [500, 7, 333]
+    q, dev, host, table = case(5, lens, 8, 2, 2, 128, 64, dtype)
+    o = run_decode(q, dev, table, lens, 500, True, 100, 3, scale, ws=False)
+    check_decode(o, q, host, table, lens, 500, True, 100, 3, scale)
+
+
+def test_decode_query_magnitudes():
+    """Rows of very different size: the largest element of a row near 1e30, 1e-30 and 6e4, a zero row, and
+    a row whose small elements fall below FP16's range relative to its largest."""
+    lens = [200]
+    q, dev, host, table = case(6, lens, 6, 1, 1, 64, 16, BF16)
+    q[0, 0] *= 1e30
+    q[0, 1] *= 1e-30
+    q[0, 2] = 0
+    q[0, 3, 0, 1:] *= 1e-6
+    q[0, 4] *= 3e4
+    qs = q.clone()
+    # per-row scales that bring the logits back to order 1, one call each
+    for h, scale in ((0, 1e-31), (1, 1e29), (2, 0.1), (3, 0.1), (4, 1e-5), (5, 0.1)):
+        o = run_decode(qs, dev, table, lens, 200, True, 0, 0, scale)
+        ks = ref.sequences(table, lens, host[0], host[1], "k", 1.0, 16)
+        vs = ref.sequences(table, lens, host[2], host[3], "v", 0.125, 16)
+        want, bound = ref.attention(ref.f64(q)[0, h:h + 1], ks[0], vs[0], True, 0, 0, scale, BF16)
+        assert (np.abs(ref.f64(o)[0, h:h + 1] - want) <= bound).all(), h
+
+
+def test_decode_rising_and_constant_logits():
+    """A maximum that rises in every tile (each one rescales the state), and keys that are all equal."""
+    rng = np.random.default_rng(12)
+    L, D, ps = 1500, 64, 16
+    pages = -(-L // ps)
+    k = rng.normal(size=(pages, 1, ps, D)) * 0.1
+    k[..., 0] = (np.arange(pages * ps).reshape(pages, 1, ps) / L - 0.5) * 30
+    v = rng.normal(size=(pages, 1, ps, D))
+    dev, host = [], []
+    for x, which, d in ((k, "k", 1.0), (v, "v", 0.125)):
+        codes, byte, _ = ref.quantize(x, d)
+        host += [ref.pack(codes, which), byte]
+        dev += [torch.from_numpy(host[-2]).to(DEV), torch.from_numpy(byte).to(DEV).view(torch.float8_e4m3fn)]
+    table = np.arange(pages, dtype=np.int32)[None]
+    q = torch.zeros(1, 2, 1, D, dtype=BF16, device=DEV)
+    q[0, 0, 0, 0] = 16.0
+    q[0, 1, 0, 0] = -16.0
+    o = run_decode(q, dev, table, [L], L)
+    check_decode(o, q, host, table, [L], L)
+    q.zero_()  # equal logits: the mean of the values
+    o = run_decode(q, dev, table, [L], L)
+    check_decode(o, q, host, table, [L], L)
+
+
+def test_decode_cap_empty_problems_and_no_pages():
+    lens = [640, 640]
+    q, dev, host, table = case(17, lens, 4, 1, 2, 64, 32, BF16)
+    o = run_decode(q, dev, table, lens, 333)
+    check_decode(o, q, host, table, lens, 333)
+    assert torch.all(run_decode(q, dev, table, lens, 0) == 0)
+    assert torch.all(run_decode(q, dev, table, [0, -5], 640) == 0)
+    empty = sa.kv4_cache(0, 1, 32, 64)
+    assert torch.all(run_decode(q, empty, table, lens, 640) == 0)
+    assert run_decode(q[:0].contiguous(), dev, table[:0], [], 640).shape == (0, 4, 2, 64)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_decode_pages_outside_the_pool_read_zeros(D):
+    lens = [500, 512, 300]
+    q, dev, host, table = case(47, lens, 8, 2, 1, D, 32, BF16)
+    pages = host[0].shape[0]
+    table[0, 3], table[1, 0], table[2, 7], table[1, 15] = -1, pages, 2 ** 31 - 1, -2 ** 31
+    o = run_decode(q, dev, table, lens, 512)
+    check_decode(o, q, host, table, lens, 512)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_decode_rows_behind_the_end_may_hold_anything(D):
+    """NaN scales and every code in the rows behind a sequence's last key, on pages that it uses."""
+    lens = [500, 1, 300, 17]
+    q, dev, host, table = case(48, lens, 4, 2, 1, D, 64, FP16)
+    want = run_decode(q, dev, table, lens, 512, True, 250, 3)
+    used = np.zeros(host[1].shape[:3:2], bool)
+    for b, L in enumerate(lens):
+        for j in range(L):
+            used[table[b, j // 64], j % 64] = True
+    dead = torch.from_numpy(~used).to(DEV)
+    for n in (1, 3):
+        dev[n].view(torch.uint8).permute(0, 2, 1, 3)[dead] = 0x7F  # E4M3 NaN
+    for n in (0, 2):
+        dev[n].permute(0, 2, 1, 3)[dead] = 0xF0
+    assert torch.equal(run_decode(q, dev, table, lens, 512, True, 250, 3), want)
+
+
+def test_decode_same_result_every_time_and_for_shared_pages():
+    lens = [2000, 1500, 2000]
+    q, dev, host, table = case(49, lens, 8, 2, 1, 128, 16, BF16)
+    table[2] = table[0]  # two requests share a prefix's pages
+    first = run_decode(q, dev, table, lens, 2000)
+    check_decode(first, q, host, table, lens, 2000)
+    for _ in range(5):
+        assert torch.equal(run_decode(q, dev, table, lens, 2000), first)
+
+
+def test_pools_past_32_bits():
+    """Code pools of more than 2^31 bytes: rows at their end are written and read in the right place."""
+    Hkv, ps, D = 2, 16, 128
+    pages = (2 ** 31 + 2 ** 28) // (Hkv * ps * D // 2)
+    dev = sa.kv4_cache(pages, Hkv, ps, D)
+    assert dev[0].numel() > 2 ** 31
+    rng = np.random.default_rng(50)
+    L = 40
+    table = np.array([[pages - 1, 0, pages - 2]], np.int32)
+    x = {w: torch.from_numpy(model_rows(rng, (L, Hkv, D), w)).to(BF16).to(DEV) for w in "kv"}
+    slots = [int(table[0, j // ps]) * ps + j % ps for j in range(L)]
+    sa.attn_kv4_append(x["k"], x["v"], i32(slots), *dev, 1.0, 0.125)
+    k = torch.empty(1, Hkv, L, D, dtype=BF16, device=DEV)
+    v = torch.empty_like(k)
+    sa.attn_kv4_gather(*dev, i32(table), i32([L]), k, v, 1.0, 0.125)
+    q = torch.from_numpy(rng.normal(size=(1, 4, 1, D))).to(BF16).to(DEV)
+    o = run_decode(q, dev, table, [L], L)
+    val = [ref.quantize(ref.f64(x[w]).transpose(1, 0, 2), d)[2] for w, d in (("k", 1.0), ("v", 0.125))]
+    assert np.array_equal(ref.f64(k[0]), val[0]) and np.array_equal(ref.f64(v[0]), val[1])
+    want, bound = ref.attention(ref.f64(q)[0], val[0], val[1], True, 0, 0, 0.0, BF16)
+    assert (np.abs(ref.f64(o)[0] - want) <= bound).all()
+
+
+# ---------------------------------------------------------------------------
+# together, as a serving loop uses them
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D,ps,dtype", [(128, 16, BF16), (64, 32, FP16)])
+def test_serving_loop(D, ps, dtype):
+    """Prompts of different lengths are placed, written and attended to, then four decode steps (the third
+    with a finished request and a padded batch): tables, cache and outputs against the definition. The
+    prompt's attention reads the cache back and runs attn_fwd on it."""
+    rng = np.random.default_rng(D)
+    B, Hq, Hkv, pages, width = 3, 4, 2, 40, 12
+    kd, vd = 1.0, 0.125
+    dev = sa.kv4_cache(pages, Hkv, ps, D)
+    free = rng.permutation(pages).astype(np.int32)
+    d_free, taken = i32(free), 0
+    table = i32(np.full((B, width), -1))
+    lens = i32([0] * B)
+    told = [[np.zeros((0, Hkv, D)), np.zeros((0, Hkv, D))] for _ in range(B)]
+    for step, (news, pad) in enumerate((([70, 1, 33], 0), ([1, 1, 1], 2), ([1, 0, 1], 1), ([2, 2, 2], 0), ([1, 1, 1], 5))):
+        T = sum(news) + pad
+        k = torch.from_numpy(model_rows(rng, (T, Hkv, D), "k")).to(dtype).to(DEV)
+        v = torch.from_numpy(model_rows(rng, (T, Hkv, D), "v")).to(dtype).to(DEV)
+        seq, starts, slots, stats = (torch.empty(n, dtype=torch.int32, device=DEV) for n in (B, B + 1, T, 3))
+        sa.attn_page_plan(lens, i32(news), d_free[taken:].clone(), table, seq, starts, slots, stats, ps)
+        sa.attn_kv4_append(k, v, slots, *dev, kd, vd)
+        n_rows, used, lost = stats.tolist()
+        assert (n_rows, lost) == (sum(news), 0) and slots.tolist()[sum(news):] == [-1] * pad
+        taken += used
+        lens, at = seq, 0
+        for b, n in enumerate(news):
+            for which, x, d in ((0, k, kd), (1, v, vd)):
+                told[b][which] = np.concatenate([told[b][which], ref.quantize(ref.f64(x[at:at + n]), d)[2]])
+            at += n
+        M = 2 if step == 3 else 1
+        q = torch.from_numpy(rng.normal(size=(B, Hq, M, D))).to(dtype).to(DEV)
+        o = torch.full_like(q, float("nan"))
+        sa.attn_decode_paged_kv4(q, *dev, table, lens, o, width * ps, True, 50, 4, 0.0, kd, vd)
+        torch.cuda.synchronize()
+        for b in range(B):
+            kk, vv = (x.transpose(1, 0, 2) for x in told[b])
+            want, bound = ref.attention(ref.f64(q)[b], kk, vv, True, 50, 4, 0.0, dtype)
+            assert (np.abs(ref.f64(o)[b] - want) <= bound).all(), (step, b)
+        if step == 0:  # the prompt of request 0: its chunk of 33 rows over the cached context
+            N, M = 70, 33
+            ck, cv = (torch.empty(1, Hkv, N, D, dtype=dtype, device=DEV) for _ in range(2))
+            sa.attn_kv4_gather(*dev, table[:1], lens[:1], ck, cv, kd, vd)
+            qc = torch.from_numpy(rng.normal(size=(1, Hq, M, D))).to(dtype).to(DEV)
+            oc = sa.attention(qc, ck, cv, causal=True)
+            kk, vv = (x.transpose(1, 0, 2) for x in told[0])
+            want, _ = ref.attention(ref.f64(qc)[0], kk, vv, True, 0, 0, 0.0, dtype)
+            assert np.abs(ref.f64(oc)[0] - want).max() <= (1e-2 if dtype == FP16 else 2e-2)
+
+
+def test_whole_step_in_a_graph():
+    """Plan, append and decode captured once and replayed over new lengths, rows and queries; two graphs
+    with workspaces of their own replayed one after the other, and an eager call between."""
+    rng = np.random.default_rng(60)
+    B, Hq, Hkv, D, ps, pages, width = 4, 8, 2, 128, 16, 300, 70
+    _, host = make_cache(rng, pages, Hkv, ps, D)
+
+    def world(seed):
+        r = np.random.default_rng(seed)
+        t = [torch.from_numpy(x.copy()).to(DEV) for x in host]
+        w = dict(dev=[t[0], t[1].view(torch.float8_e4m3fn), t[2], t[3].view(torch.float8_e4m3fn)])
+        w["cached"], w["new"] = i32(r.integers(0, 1000, B)), i32([1] * B)
+        w["table"] = i32(r.permutation(pages)[: B * width].reshape(B, width))
+        w["free"] = i32(r.permutation(pages)[:8])
+        w["lens"], w["starts"], w["slots"], w["stats"] = i32([0] * B), i32([0] * (B + 1)), i32([0] * (B + 1)), i32([0] * 3)
+        w["k"] = torch.from_numpy(r.normal(size=(B + 1, Hkv, D))).to(BF16).to(DEV)
+        w["v"] = torch.from_numpy(r.normal(size=(B + 1, Hkv, D))).to(BF16).to(DEV)
+        w["q"] = torch.from_numpy(r.normal(size=(B, Hq, 1, D))).to(BF16).to(DEV)
+        w["o"] = torch.zeros_like(w["q"])
+        return w
+
+    def step(w):
+        sa.attn_page_plan(w["cached"], w["new"], w["free"], w["table"], w["lens"], w["starts"], w["slots"], w["stats"], ps)
+        sa.attn_kv4_append(w["k"], w["v"], w["slots"], *w["dev"], 1.0, 0.125)
+        sa.attn_decode_paged_kv4(w["q"], *w["dev"], w["table"], w["lens"], w["o"], width * ps, True, 400, 4, 0.0, 1.0,
+                                 0.125)
+
+    def load(w, seed):
+        new = world(seed)
+        for name, x in new.items():
+            for a, b in zip(w[name], x) if name == "dev" else [(w[name], x)]:
+                a.view(torch.uint8).copy_(b.view(torch.uint8))
+
+    graphs = []
+    for seed in (1, 2):
+        w = world(seed)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(w)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(w)
+        graphs.append((g, w))
+    for seed in (3, 4, 5):
+        for n, (g, w) in enumerate(graphs):
+            load(w, seed + 10 * n)
+        eager = world(seed)
+        for g, w in graphs:
+            g.replay()
+        step(eager)
+        torch.cuda.synchronize()
+        other = world(seed + 10)
+        step(other)
+        torch.cuda.synchronize()
+        for want, (g, w) in zip((eager, other), graphs):
+            for name in ("o", "table", "lens", "slots", "stats", "starts"):
+                assert torch.equal(w[name], want[name]), name
+            for a, b in zip(w["dev"], want["dev"]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_calls_on_two_streams_and_two_threads():
+    """Calls that overlap, each with its own workspace, from streams and from host threads."""
+    jobs = []
+    for seed, lens, M in ((70, [3000, 100], 1), (71, [2500], 4), (72, [40] * 60, 1)):
+        q, dev, host, table = case(seed, lens, 8, 2, M, 128, 16, BF16)
+        jobs.append((q, dev, i32(table), i32(lens), max(lens), run_decode(q, dev, table, lens, max(lens))))
+    outs = [torch.zeros_like(j[0]) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for j, o, s in zip(jobs, outs, streams):
+            sa.attn_decode_paged_kv4(j[0], *j[1], j[2], j[3], o, j[4], k_descale=1.0, v_descale=0.125, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, j[5]) for o, j in zip(outs, jobs))
+    errors = []
+
+    def work(j, o, s):
+        try:
+            for _ in range(5):
+                sa.attn_decode_paged_kv4(j[0], *j[1], j[2], j[3], o, j[4], k_descale=1.0, v_descale=0.125, stream=s)
+        except Exception as e:  # reported below
+            errors.append(e)
+
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=x) for x in zip(jobs, outs, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and all(torch.equal(o, j[5]) for o, j in zip(outs, jobs))
+
+
+def test_status_word_stays_clear():
+    assert sa.last_device_status() == 0
