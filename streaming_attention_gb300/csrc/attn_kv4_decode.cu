@@ -1,9 +1,21 @@
 // Decode attention over the 4-bit paged KV cache (format: attn_kv4.h).
 //
-// One block owns one split of a sequence's visible key tiles for one KV head and
-// up to 8 * NT of its grouped query rows (query head h = g * G + r / M, row
-// i = r % M); its four warps take 16 keys each of a 64-key tile and keep their own
-// running (m, l, acc) per row, joined at the end by the common-maximum rule.
+// Work. A segment is the visible keys of one (sequence, KV head, block of 8 * NT
+// grouped query rows), in tiles of 64 keys; query head h = g * G + r / M, row
+// i = r % M. The tiles of all segments in a row are cut into equal ranges, one per
+// block of a grid that fills the GPU once, whatever the lengths are: each block
+// counts the tiles from seq_lens itself. A segment that lies inside a block's range
+// is written to o there; of one that is cut, each block leaves its part's
+// (m, l, acc) in the workspace (at most two parts a block: one begun before it, one
+// that goes on behind it), and a second kernel joins them by the common-maximum
+// rule.
+//
+// In a block, four warps take 16 keys each of a tile and keep their own running
+// (m, l, acc) per row, joined through shared memory at the end of a segment's part.
+// Each warp copies its keys' codes and scales into a ring of its own
+// (cp.async, kStages deep, no barrier between warps): the reading of the cache is
+// what bounds the kernel, and 16 warps with 4 stages in flight keep about 140 KB of
+// it outstanding per SM.
 //
 // A warp's products run transposed, on m16n8k16 matrix instructions with the
 // cache as the left operand, so that a row of the cache is expanded once for all
@@ -30,7 +42,10 @@ namespace attn {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;  // keys of a tile, 16 per warp
+constexpr int kStages = 5;          // tiles in a warp's ring
+constexpr int kMinTiles = 2;        // a block's range is at least this long while there are blocks to spare
 constexpr float kPShift = 6.0f;     // probabilities are kept times 2^6
 
 struct DecodeArgs {
@@ -39,14 +54,35 @@ struct DecodeArgs {
     const int* table;
     const int* lens;
     void* o;
-    float *ws_m, *ws_l, *ws_acc;
-    int Hq, Hkv, M, G;
+    float *ws_m, *ws_l, *ws_acc;  // [blocks][2][rows], the same, [blocks][2][rows][D]
+    int4* cut;                    // [blocks]: segment that a block leaves unfinished (b, head * Z + z), last block of it
+    int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
     int causal, window, sinks;
     float scale_log2;  // logit scale and K factor, times log2(e)
     float v_scale;
-    int per_split, S;  // tiles of a split, splits
 };
+
+// The tiles that any row of a sequence of L keys may see: those of the first `sinks` keys, then those of the
+// window's union. At least one, so that every segment belongs to a block.
+struct Tiles {
+    int sink, win, n;  // tiles of the sinks, first tile of the window, all
+    __device__ int at(int t) const { return t < sink ? t : t - sink + win; }
+};
+__device__ __forceinline__ Tiles tiles_of(const DecodeArgs& a, int L) {
+    int lo0, hi0, lo1, hi1;
+    key_range(L - a.M, L, a.causal, a.window, &lo0, &hi0);
+    key_range(L - 1, L, a.causal, a.window, &lo1, &hi1);
+    const int end = hi1 / kTile + (hi1 % kTile != 0);
+    Tiles t;
+    t.win = min(lo0 / kTile, end);
+    t.sink = min(a.sinks / kTile + (a.sinks % kTile != 0), t.win);
+    t.n = max(t.sink + end - t.win, 1);
+    return t;
+}
+__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
+    return min(max(__ldg(a.lens + b), 0), a.max_len);
+}
 
 template <int N>
 struct Bytes;
@@ -129,253 +165,468 @@ __device__ __forceinline__ void put<__half>(void* o, size_t i, float x) {
     reinterpret_cast<__half*>(o)[i] = __float2half_rn(x);
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One stage of a warp's ring: the codes and scales of 16 keys and values. Row `slot` of the S^T product's left
+// operand is key (slot / 2) % 4 + 4 (slot % 2) + 8 (slot / 8), so that the four keys that a lane needs of the
+// values (slots 2 cq, 2 cq + 1, 2 cq + 8, 2 cq + 9) are cq + 4 e. Key rows lie in the order of the slots and value
+// rows in that of the keys, at D = 128 with the 16-byte chunks of every other pair of rows exchanged: both are read
+// without bank conflicts.
+template <int D>
+struct Stage {
+    static constexpr int NG = D / kKv4Group;
+    static constexpr int kRow = D / 2;           // bytes of a row's codes
+    static constexpr int kCodes = 16 * kRow;     // 64 chunks of 16 bytes at D = 128, 32, 16
+    static constexpr int kScales = 16 * NG;
+    static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
+    static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+
+    // lane's part of the copy of rows at .. at + 15 of the pools
+    static __device__ __forceinline__ void load(uint32_t dst, const Kv4Cache& c, size_t at, int lane) {
+        constexpr int Q = kRow / 16;  // chunks of a row
+#pragma unroll
+        for (int i = 0; i < (kCodes + 511) / 512; ++i) {
+            const int x = lane + 32 * i;
+            if (kCodes >= 512 || x < kCodes / 16) {
+                const int r = x / Q, q = x % Q;
+                const int slot = (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1);
+                const int vq = D == 128 ? q ^ (r & 2) : q;
+                copy16(dst + kK + slot * kRow + q * 16, c.k_codes + at * kRow + x * 16);
+                copy16(dst + kV + r * kRow + vq * 16, c.v_codes + at * kRow + x * 16);
+            }
+        }
+        constexpr int S = kScales / 16;
+        if (lane < 2 * S) {
+            const bool v = lane >= S;
+            const int x = v ? lane - S : lane;
+            copy16(dst + (v ? kVs : kKs) + x * 16, (v ? c.v_scales : c.k_scales) + at * NG + x * 16);
+        }
+    }
+};
+
+// Exclusive sum over the block's threads, and the total.
+__device__ __forceinline__ long long block_sum(long long x, long long* part, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long s = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
+    }
+    __syncthreads();  // the last use of `part` is done
+    if (lane == 31) part[warp] = s;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += part[w];
+        all += part[w];
+    }
+    *total = all;
+    return s - x + before;
+}
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(const DecodeArgs a) {
+    using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
     constexpr int ROWS = 8 * NT;
     using KChunk = typename Bytes<4 * NG>::T;
     using VChunk = typename Bytes<2 * NG>::T;
     using Scales = typename Bytes<NG>::T;
+    extern __shared__ __align__(16) uint8_t smem[];
+    // the rings, and after them in the same place the warps' sums of a part
+    float* sm_acc = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D]
     __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-    __shared__ float sm_acc[kWarps][ROWS][D];
+    __shared__ long long part[kWarps], found_before;
+    __shared__ int found_b;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, cq = lane & 3;  // the lane's place in a matrix fragment
-    const int split = blockIdx.x;
-    const int b = blockIdx.y / a.Hkv, g = blockIdx.y % a.Hkv;
-    const int R = a.G * a.M, r0 = blockIdx.z * ROWS;
+    const int key_slot = (gq >> 1) + 4 * (gq & 1);  // the key of slot gq; slot gq + 8: 8 more
+    uint8_t* ring = smem + warp * (kStages * St::kBytes);
+    const uint32_t ring_at = ptx::smem_u32(ring);
+    const int H = a.Hkv * a.Z;
+    const int R = a.G * a.M;
     const int ps = a.c.page_size;
 
-    // keys of this sequence and the tiles any of its rows may see: those of the
-    // first `sinks` keys, then those of the window's union
-    const int L = min(max(__ldg(a.lens + b), 0), a.max_len);
-    int lo0, hi0, lo1, hi1;
-    key_range(L - a.M, L, a.causal, a.window, &lo0, &hi0);
-    key_range(L - 1, L, a.causal, a.window, &lo1, &hi1);
-    const int t_end = hi1 / kTile + (hi1 % kTile != 0);
-    const int t_win = min(lo0 / kTile, t_end);
-    const int n_sink = min(min(a.sinks / kTile + (a.sinks % kTile != 0), t_win), t_end);
-    const int tiles = n_sink + t_end - t_win;
-    const int first = split * a.per_split, last = min(first + a.per_split, tiles);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // Q^T fragments, each row scaled to maximum 1..2, and the visible range of the lane's own rows
-    uint32_t qf[NT][NG][2][2];
-    float sc[NT][2];
-    int vis_lo[NT][2], vis_hi[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + nt * 8 + gq;
-        float x[NG][8], top = 0.f;
-        const bool row = r < R;
-        const int h = g * a.G + (row ? r / a.M : 0), i = row ? r % a.M : 0;
-        const uint32_t* qrow =
-            reinterpret_cast<const uint32_t*>(a.q) + (((size_t)b * a.Hq + h) * a.M + i) * (D / 2) + cq * 4;
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            const uint4 w = row ? __ldg(reinterpret_cast<const uint4*>(qrow + n * 16)) : make_uint4(0, 0, 0, 0);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[n][2 * e] = lo_of<T>(ww[e]);
-                x[n][2 * e + 1] = lo_of<T>(ww[e] >> 16);
-                top = fmaxf(top, fmaxf(fabsf(x[n][2 * e]), fabsf(x[n][2 * e + 1])));
-            }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // biased exponent of the row's maximum, kept where 2^e and 2^-e are both normal
-        int e = (int)(__float_as_uint(top) >> 23);
-        e = top == 0.f ? 127 : min(max(e, 1), 253);
-        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-        const float up = __uint_as_float((uint32_t)e << 23) * a.scale_log2;
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    qf[nt][n][s][t] = ptx::pack_f16(x[n][2 * s + t] * down, x[n][4 + 2 * s + t] * down);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            sc[nt][t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
-            const int rt = r0 + nt * 8 + 2 * cq + t;
-            int p = rt < R ? rt % a.M + L - a.M : L - 1;
-            key_range(p, L, a.causal, a.window, &vis_lo[nt][t], &vis_hi[nt][t]);
-        }
+    // ---- this block's range of the tiles ----
+    long long total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        long long all;
+        block_sum(b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0, part, &all);
+        total += all;
     }
-
-    float m[NT][2], l[NT][2], acc[NT][2 * NG][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            m[nt][t] = -INFINITY;
-            l[nt][t] = 0.f;
+    const long long want = (total + kMinTiles - 1) / kMinTiles;
+    const long long blocks = want < gridDim.x ? want : gridDim.x;
+    if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (blockIdx.x >= blocks) return;
+    const long long u0 = total * blockIdx.x / blocks, u1 = total * (blockIdx.x + 1) / blocks;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        const long long n = b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0;
+        long long all;
+        const long long s = before + block_sum(n, part, &all);
+        if (s <= u0 && u0 < s + n) {
+            found_b = b;
+            found_before = s;
         }
-#pragma unroll
-        for (int n = 0; n < 2 * NG; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][n][e] = 0.f;
-    }
-
-    const int* trow = a.table + (size_t)b * a.max_pages;
-    for (int tile = first; tile < last; ++tile) {
-        const int j0 = (tile < n_sink ? tile : tile - n_sink + t_win) * kTile + warp * 16;
-        if (j0 >= L) continue;
-        const int page = __ldg(trow + j0 / ps);
-        const bool held = page >= 0 && page < a.c.num_pages;  // a page outside the pool reads as zeros
-        const size_t at = ((size_t)(held ? page : 0) * a.Hkv + g) * ps + j0 % ps;
-
-        // ---- S^T = K Q^T ----
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-        if (held) {
-            union {
-                KChunk v;
-                uint32_t w[NG];
-            } k0, k1;
-            k0.v = __ldg(reinterpret_cast<const KChunk*>(a.c.k_codes + (at + gq) * (D / 2)) + cq);
-            k1.v = __ldg(reinterpret_cast<const KChunk*>(a.c.k_codes + (at + gq + 8) * (D / 2)) + cq);
-            const uint32_t s0 = __ldg(reinterpret_cast<const Scales*>(a.c.k_scales + (at + gq) * NG));
-            const uint32_t s1 = __ldg(reinterpret_cast<const Scales*>(a.c.k_scales + (at + gq + 8) * NG));
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                // the scale in both halves
-                const uint32_t f0 = e4m3x2(((s0 >> (8 * n)) & 0xFFu) * 0x0101u);
-                const uint32_t f1 = e4m3x2(((s1 >> (8 * n)) & 0xFFu) * 0x0101u);
-                const uint32_t n0 = hmul2(f0, kMinus72), n1 = hmul2(f1, kMinus72);
-                const uint32_t x0[4] = {expand<0>(k0.w[n], f0, n0), expand<0>(k1.w[n], f1, n1),
-                                        expand<1>(k0.w[n], f0, n0), expand<1>(k1.w[n], f1, n1)};
-                const uint32_t x1[4] = {expand<2>(k0.w[n], f0, n0), expand<2>(k1.w[n], f1, n1),
-                                        expand<3>(k0.w[n], f0, n0), expand<3>(k1.w[n], f1, n1)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816(s[nt], x0, qf[nt][n][0][0], qf[nt][n][0][1]);
-                    mma_16816(s[nt], x1, qf[nt][n][1][0], qf[nt][n][1][1]);
-                }
-            }
-        }
-
-        // ---- softmax: s[0..1] is key gq of rows 2 cq, 2 cq + 1; s[2..3] key gq + 8 ----
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float x[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = j0 + gq + 8 * e;
-                    const bool see = j < vis_hi[nt][t] && (j >= vis_lo[nt][t] || j < a.sinks);
-                    x[e] = see ? s[nt][2 * e + t] * sc[nt][t] : -INFINITY;  // a masked key scores -inf
-                }
-                float mx = fmaxf(m[nt][t], fmaxf(x[0], x[1]));
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                // ghost-row pin: while every key so far is masked, 0 stands for the maximum
-                const float use = mx == -INFINITY ? 0.f : mx;
-                const float alpha = ptx::ex2(m[nt][t] - use);
-                m[nt][t] = mx;
-                p[t] = ptx::ex2(x[0] - use + kPShift);
-                p[2 + t] = ptx::ex2(x[1] - use + kPShift);
-                l[nt][t] = l[nt][t] * alpha + p[t] + p[2 + t];
-#pragma unroll
-                for (int n = 0; n < 2 * NG; ++n) {
-                    acc[nt][n][t] *= alpha;
-                    acc[nt][n][2 + t] *= alpha;
-                }
-            }
-            pb[nt][0] = transpose8(ptx::pack_f16(p[0], p[1]));
-            pb[nt][1] = transpose8(ptx::pack_f16(p[2], p[3]));
-        }
-
-        // ---- O^T += V^T P^T ----
-        if (held) {
-            union VWords {
-                VChunk v;
-                uint32_t w[(NG + 1) / 2];
-            } v[4];
-            uint32_t vs[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 2 * cq + (e & 1) + 8 * (e >> 1);
-                v[e].w[0] = 0;
-                v[e].v = __ldg(reinterpret_cast<const VChunk*>(a.c.v_codes + (at + k) * (D / 2)) + gq);
-                vs[e] = __ldg(reinterpret_cast<const Scales*>(a.c.v_scales + (at + k) * NG));
-                if (j0 + k >= L) vs[e] = 0;  // whatever stands behind the sequence counts as zero
-            }
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                const uint32_t pick = n & 1 ? 0x7632u : 0x5410u, byte = (uint32_t)(n | ((4 + n) << 4));
-                const uint32_t u0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], pick);
-                const uint32_t u1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], pick);
-                const uint32_t f0 = e4m3x2(__byte_perm(vs[0], vs[1], byte));
-                const uint32_t f1 = e4m3x2(__byte_perm(vs[2], vs[3], byte));
-                const uint32_t n0 = hmul2(f0, kMinus72), n1 = hmul2(f1, kMinus72);
-                const uint32_t x0[4] = {expand<0>(u0, f0, n0), expand<1>(u0, f0, n0), expand<0>(u1, f1, n1),
-                                        expand<1>(u1, f1, n1)};
-                const uint32_t x1[4] = {expand<2>(u0, f0, n0), expand<3>(u0, f0, n0), expand<2>(u1, f1, n1),
-                                        expand<3>(u1, f1, n1)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816(acc[nt][2 * n], x0, pb[nt][0], pb[nt][1]);
-                    mma_16816(acc[nt][2 * n + 1], x1, pb[nt][0], pb[nt][1]);
-                }
-            }
-        }
-    }
-
-    // ---- join the warps ----
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[nt][t] += __shfl_xor_sync(0xffffffffu, l[nt][t], d);
-            const int r = nt * 8 + 2 * cq + t;
-            if (gq == 0) {
-                sm_m[warp][r] = m[nt][t];
-                sm_l[warp][r] = l[nt][t];
-            }
-            // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even) or gq + 8
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-                *reinterpret_cast<float4*>(&sm_acc[warp][r][32 * n + 4 * gq]) =
-                    make_float4(acc[nt][2 * n][t], acc[nt][2 * n][2 + t], acc[nt][2 * n + 1][t],
-                                acc[nt][2 * n + 1][2 + t]);
-        }
+        before += all;
+        if (u0 < before) break;
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < ROWS * D; x += kWarps * 32) {
-        const int r = x / D, d = x % D;
-        if (r0 + r >= R) break;
-        float mx = -INFINITY;
+    int b = found_b;
+    long long rem = u0 - found_before;  // tiles of sequence b before this block's
+
+    for (long long u = u0; u < u1;) {
+        const int L = length_of(a, b);
+        const Tiles tl = tiles_of(a, L);
+        const int hz = (int)(rem / tl.n), t0 = (int)(rem % tl.n);
+        const int t1 = (int)min((long long)tl.n, t0 + (u1 - u));
+        const int g = hz / a.Z, r0 = (hz % a.Z) * ROWS;
+
+        // the pool rows of this warp's keys, for 32 tiles at a time: lane x has those of tile base + x
+        const int* trow = a.table + (size_t)b * a.max_pages;
+        const auto key_of = [&](int t) { return tl.at(t) * kTile + warp * 16; };
+        const auto page_of = [&](int t) {
+            const int j = key_of(t);
+            return t < t1 && j < L ? __ldg(trow + j / ps) : -1;
+        };
+        const auto row_of = [&](int page, int t) {  // -1: a page outside the pool, or nothing to read
+            return page >= 0 && page < a.c.num_pages ? ((long long)page * a.Hkv + g) * ps + key_of(t) % ps : -1;
+        };
+        int base = t0;
+        int next_page = page_of(t0 + lane);
+        long long rows_at = row_of(next_page, t0 + lane);
+        next_page = page_of(t0 + 32 + lane);
+        uint32_t held = 0;  // bit t % 32: the stage of tile t was read from the pool
+        const auto issue = [&](int t) {
+            if (t < t1) {
+                if (t - base == 32) {
+                    base = t;
+                    rows_at = row_of(next_page, t + lane);
+                    next_page = page_of(t + 32 + lane);
+                }
+                const long long at = __shfl_sync(0xffffffffu, rows_at, t - base);
+                if (at >= 0) St::load(ring_at + (t % kStages) * St::kBytes, a.c, (size_t)at, lane);
+                held = (held & ~(1u << (t & 31))) | ((at >= 0 ? 1u : 0u) << (t & 31));
+            }
+            copy_commit();
+        };
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
-        float lt = 0.f, y = 0.f;
+        for (int x = 0; x < kStages - 1; ++x) issue(t0 + x);
+
+        // Q^T fragments, each row scaled to maximum 1..2, and the visible range of the lane's own rows
+        uint32_t qf[NT][NG][2][2];
+        float sc[NT][2];
+        int vis_lo[NT][2], vis_hi[NT][2];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = sm_m[w][r] == -INFINITY ? 0.f : ptx::ex2(sm_m[w][r] - mx);
-            lt = fmaf(f, sm_l[w][r], lt);
-            y = fmaf(f, sm_acc[w][r][d], y);
-        }
-        const int h = g * a.G + (r0 + r) / a.M, i = (r0 + r) % a.M;
-        const size_t row = ((size_t)b * a.Hq + h) * a.M + i;
-        if (a.S == 1) {
-            put<T>(a.o, row * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
-        } else {
-            const size_t at = row * a.S + split;
-            a.ws_acc[at * D + d] = y;
-            if (d == 0) {
-                a.ws_m[at] = mx;
-                a.ws_l[at] = lt;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r0 + nt * 8 + gq;
+            float x[NG][8], top = 0.f;
+            const bool row = r < R;
+            const int h = g * a.G + (row ? r / a.M : 0), i = row ? r % a.M : 0;
+            const uint32_t* qrow =
+                reinterpret_cast<const uint32_t*>(a.q) + (((size_t)b * a.Hq + h) * a.M + i) * (D / 2) + cq * 4;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+                const uint4 w = row ? __ldg(reinterpret_cast<const uint4*>(qrow + n * 16)) : make_uint4(0, 0, 0, 0);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n][2 * e] = lo_of<T>(ww[e]);
+                    x[n][2 * e + 1] = lo_of<T>(ww[e] >> 16);
+                    top = fmaxf(top, fmaxf(fabsf(x[n][2 * e]), fabsf(x[n][2 * e + 1])));
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // biased exponent of the row's maximum, kept where 2^e and 2^-e are both normal
+            int e = (int)(__float_as_uint(top) >> 23);
+            e = top == 0.f ? 127 : min(max(e, 1), 253);
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+            const float up = __uint_as_float((uint32_t)e << 23) * a.scale_log2;
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        qf[nt][n][s][t] = ptx::pack_f16(x[n][2 * s + t] * down, x[n][4 + 2 * s + t] * down);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                sc[nt][t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
+                const int rt = r0 + nt * 8 + 2 * cq + t;
+                const int p = rt < R ? rt % a.M + L - a.M : L - 1;
+                key_range(p, L, a.causal, a.window, &vis_lo[nt][t], &vis_hi[nt][t]);
             }
         }
+        // keys [all_lo, all_hi) are visible to every row
+        int all_lo, all_hi, skip;
+        key_range(L - 1, L, a.causal, a.window, &all_lo, &skip);
+        key_range(L - a.M, L, a.causal, a.window, &skip, &all_hi);
+
+        float m[NT][2], mu[NT][2], l[NT][2], acc[NT][2 * NG][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                m[nt][t] = -INFINITY;
+                mu[nt][t] = -kPShift;  // m less the shift; while every key so far is masked, 0 stands for m
+                l[nt][t] = 0.f;
+            }
+#pragma unroll
+            for (int n = 0; n < 2 * NG; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][n][e] = 0.f;
+        }
+
+        for (int t = t0; t < t1; ++t) {
+            copy_wait<kStages - 2>();
+            __syncwarp();
+            issue(t + kStages - 1);  // into the stage that was read in the last step
+            const int j0 = key_of(t);
+            if (j0 >= L) continue;
+            const bool live = (held >> (t & 31)) & 1u;  // a page outside the pool reads as zeros
+            const uint8_t* st = ring + (t % kStages) * St::kBytes;
+
+            // ---- S^T = K Q^T ----
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+            {
+                union {
+                    KChunk v;
+                    uint32_t w[NG];
+                } k0, k1;
+                k0.v = *reinterpret_cast<const KChunk*>(st + St::kK + gq * St::kRow + cq * (4 * NG));
+                k1.v = *reinterpret_cast<const KChunk*>(st + St::kK + (gq + 8) * St::kRow + cq * (4 * NG));
+                uint32_t s0 = *reinterpret_cast<const Scales*>(st + St::kKs + key_slot * NG);
+                uint32_t s1 = *reinterpret_cast<const Scales*>(st + St::kKs + (key_slot + 8) * NG);
+                if (!live) s0 = s1 = 0;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    // the scale in both halves
+                    const uint32_t f0 = e4m3x2(((s0 >> (8 * n)) & 0xFFu) * 0x0101u);
+                    const uint32_t f1 = e4m3x2(((s1 >> (8 * n)) & 0xFFu) * 0x0101u);
+                    const uint32_t n0 = hmul2(f0, kMinus72), n1 = hmul2(f1, kMinus72);
+                    const uint32_t x0[4] = {expand<0>(k0.w[n], f0, n0), expand<0>(k1.w[n], f1, n1),
+                                            expand<1>(k0.w[n], f0, n0), expand<1>(k1.w[n], f1, n1)};
+                    const uint32_t x1[4] = {expand<2>(k0.w[n], f0, n0), expand<2>(k1.w[n], f1, n1),
+                                            expand<3>(k0.w[n], f0, n0), expand<3>(k1.w[n], f1, n1)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(s[nt], x0, qf[nt][n][0][0], qf[nt][n][0][1]);
+                        mma_16816(s[nt], x1, qf[nt][n][1][0], qf[nt][n][1][1]);
+                    }
+                }
+            }
+
+            // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
+            const bool whole = j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks);
+            bool rises = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[nt][e] *= sc[nt][e & 1];
+                    if (!whole) {
+                        const int j = j0 + key_slot + 8 * (e >> 1);
+                        const bool see = j < vis_hi[nt][e & 1] && (j >= vis_lo[nt][e & 1] || j < a.sinks);
+                        if (!see) s[nt][e] = -INFINITY;  // a masked key scores -inf
+                    }
+                    rises |= s[nt][e] > m[nt][e & 1];
+                }
+            if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(m[nt][e], fmaxf(s[nt][e], s[nt][2 + e]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        if (mx > m[nt][e]) {
+                            const float alpha = ptx::ex2(m[nt][e] - mx);
+                            m[nt][e] = mx;
+                            mu[nt][e] = mx - kPShift;
+                            l[nt][e] *= alpha;
+#pragma unroll
+                            for (int n = 0; n < 2 * NG; ++n) {
+                                acc[nt][n][e] *= alpha;
+                                acc[nt][n][2 + e] *= alpha;
+                            }
+                        }
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(s[nt][e] - mu[nt][e & 1]);
+                l[nt][0] += p[0] + p[2];
+                l[nt][1] += p[1] + p[3];
+                pb[nt][0] = transpose8(ptx::pack_f16(p[0], p[1]));
+                pb[nt][1] = transpose8(ptx::pack_f16(p[2], p[3]));
+            }
+
+            // ---- O^T += V^T P^T: the lane's keys are cq + 4 e ----
+            {
+                union VWords {
+                    VChunk v;
+                    uint32_t w[(NG + 1) / 2];
+                } v[4];
+                uint32_t vs[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int k = cq + 4 * e;
+                    const int byte = D == 128 ? (gq * 8) ^ ((k & 2) * 16) : gq * (2 * NG);
+                    v[e].w[0] = 0;
+                    v[e].v = *reinterpret_cast<const VChunk*>(st + St::kV + k * St::kRow + byte);
+                    vs[e] = *reinterpret_cast<const Scales*>(st + St::kVs + k * NG);
+                    // whatever stands behind the sequence, and a page outside the pool, counts as zero
+                    if (!live || (!whole && j0 + k >= L)) vs[e] = 0;
+                }
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const uint32_t pick = n & 1 ? 0x7632u : 0x5410u, byte = (uint32_t)(n | ((4 + n) << 4));
+                    const uint32_t w0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], pick);
+                    const uint32_t w1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], pick);
+                    const uint32_t f0 = e4m3x2(__byte_perm(vs[0], vs[1], byte));
+                    const uint32_t f1 = e4m3x2(__byte_perm(vs[2], vs[3], byte));
+                    const uint32_t n0 = hmul2(f0, kMinus72), n1 = hmul2(f1, kMinus72);
+                    const uint32_t x0[4] = {expand<0>(w0, f0, n0), expand<1>(w0, f0, n0), expand<0>(w1, f1, n1),
+                                            expand<1>(w1, f1, n1)};
+                    const uint32_t x1[4] = {expand<2>(w0, f0, n0), expand<3>(w0, f0, n0), expand<2>(w1, f1, n1),
+                                            expand<3>(w1, f1, n1)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(acc[nt][2 * n], x0, pb[nt][0], pb[nt][1]);
+                        mma_16816(acc[nt][2 * n + 1], x1, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+        }
+
+        // ---- join the warps ----
+        copy_wait<0>();
+        __syncthreads();  // every warp is done with the rings (and with the sums of the last part)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nt][t] += __shfl_xor_sync(0xffffffffu, l[nt][t], d);
+                const int r = nt * 8 + 2 * cq + t;
+                if (gq == 0) {
+                    sm_m[warp][r] = m[nt][t];
+                    sm_l[warp][r] = l[nt][t];
+                }
+                // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even) or gq + 8
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) =
+                        make_float4(acc[nt][2 * n][t], acc[nt][2 * n][2 + t], acc[nt][2 * n + 1][t],
+                                    acc[nt][2 * n + 1][2 + t]);
+            }
+        }
+        __syncthreads();
+        const bool done = t0 == 0 && t1 == tl.n;
+        const size_t part_row = ((size_t)blockIdx.x * 2 + (t0 == 0)) * ROWS;
+        if (t0 == 0 && !done && threadIdx.x == 0) {
+            // the block that holds the segment's last tile: the last one that starts at or before it
+            const long long e = u + tl.n;
+            a.cut[blockIdx.x] = make_int4(b, hz, (int)((e * blocks + total - 1) / total - 1), 0);
+        }
+        for (int x = threadIdx.x; x < ROWS * D; x += kThreads) {
+            const int r = x / D, d = x % D;
+            if (r0 + r >= R) break;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
+            float lt = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = sm_m[w][r] == -INFINITY ? 0.f : ptx::ex2(sm_m[w][r] - mx);
+                lt = fmaf(f, sm_l[w][r], lt);
+                y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
+            }
+            if (done) {
+                const int h = g * a.G + (r0 + r) / a.M, i = (r0 + r) % a.M;
+                put<T>(a.o, (((size_t)b * a.Hq + h) * a.M + i) * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
+            } else {
+                a.ws_acc[(part_row + r) * D + d] = y;
+                if (d == 0) {
+                    a.ws_m[part_row + r] = mx;
+                    a.ws_l[part_row + r] = lt;
+                }
+            }
+        }
+        __syncthreads();  // the sums are read: the rings may be filled again
+        u += t1 - t0;
+        rem += t1 - t0;
+        if (rem == (long long)tl.n * H) {
+            ++b;
+            rem = 0;
+        }
     }
+}
+
+// Joins the parts of the segment that block `blockIdx.x` of the decode kernel left unfinished, one row per block: the
+// part in that block's second place and those in the first places of the blocks behind it. Four warps share the parts.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const DecodeArgs a) {
+    __shared__ float sm_l[kWarps];
+    __shared__ float4 sm_y[kWarps][D / 4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 cut = a.cut[blockIdx.x];
+    const int r = blockIdx.y, r0 = (cut.y % a.Z) * ROWS, R = a.G * a.M;
+    if (cut.x < 0 || r0 + r >= R) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = cut.z - (int)blockIdx.x + 1;
+    const auto row_of = [&](int x) { return ((size_t)(blockIdx.x + x) * 2 + (x == 0)) * ROWS + r; };
+    float mx = -INFINITY;
+    for (int x = lane; x < parts; x += 32) mx = fmaxf(mx, a.ws_m[row_of(x)]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = warp; x < parts; x += kWarps) {
+        const size_t row = row_of(x);
+        const float mp = a.ws_m[row];
+        const float f = mp == -INFINITY ? 0.f : ptx::ex2(mp - mx);
+        l = fmaf(f, a.ws_l[row], l);
+        if (lane < D / 4) {
+            const float4 v = reinterpret_cast<const float4*>(a.ws_acc + row * D)[lane];
+            y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+        }
+    }
+    if (lane == 0) sm_l[warp] = l;
+    if (lane < D / 4) sm_y[warp][lane] = y;
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    float lt = 0.f, yt = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        lt += sm_l[w];
+        yt += reinterpret_cast<const float*>(sm_y[w])[threadIdx.x];
+    }
+    const int h = (cut.y / a.Z) * a.G + (r0 + r) / a.M, i = (r0 + r) % a.M;
+    put<T>(a.o, (((size_t)cut.x * a.Hq + h) * a.M + i) * D + threadIdx.x, lt > 0.f ? yt * (a.v_scale / lt) : 0.f);
 }
 
 struct Kv4Call {
@@ -387,8 +638,11 @@ struct Kv4Call {
 
 int rows_per_block(const Problem& p) { return (long long)p.G * p.M <= 8 ? 8 : 16; }
 
-// Tiles of the longest range a sequence can have, in splits enough for about four blocks per SM.
-void plan_splits(const Kv4Call& c, int* per_split, int* S) {
+// Blocks that are resident at once, from the kernels' registers (at most 128 a thread for 8 rows, 168 for 16) and rings.
+int blocks_per_sm(const Problem& p) { return rows_per_block(p) == 8 ? 4 : 3; }
+
+// One block for every place on the GPU, fewer while the longest lengths could not give each kMinTiles tiles.
+int plan_blocks(const Kv4Call& c) {
     const Problem& p = c.p;
     long long tiles = ((long long)c.max_len + kTile - 1) / kTile;
     if (p.window > 0) {
@@ -398,25 +652,49 @@ void plan_splits(const Kv4Call& c, int* per_split, int* S) {
     }
     if (tiles < 1) tiles = 1;
     const int rows = rows_per_block(p);
-    const long long groups = (long long)p.B * p.Hkv * (((long long)p.G * p.M + rows - 1) / rows);
+    tiles *= (long long)p.B * p.Hkv * (((long long)p.G * p.M + rows - 1) / rows);
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
-    long long s = (4LL * sms + groups - 1) / groups;
-    if (s > tiles) s = tiles;
-    if (s > 512) s = 512;
-    const long long per = (tiles + s - 1) / s;
-    *per_split = (int)per;
-    *S = (int)((tiles + per - 1) / per);
+    const long long most = (long long)sms * blocks_per_sm(p), want = (tiles + kMinTiles - 1) / kMinTiles;
+    return (int)(want < most ? want : most);
 }
 
-template <typename T, int NT>
-cudaError_t launch_d(const DecodeArgs& a, int D, dim3 grid, cudaStream_t s) {
-    switch (D) {
-        case 32: kv4_decode_kernel<T, 32, NT><<<grid, kWarps * 32, 0, s>>>(a); break;
-        case 64: kv4_decode_kernel<T, 64, NT><<<grid, kWarps * 32, 0, s>>>(a); break;
-        default: kv4_decode_kernel<T, 128, NT><<<grid, kWarps * 32, 0, s>>>(a); break;
+template <typename T, int D, int NT>
+cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
+    constexpr int kRing = kWarps * kStages * Stage<D>::kBytes, kSums = kWarps * 8 * NT * D * (int)sizeof(float);
+    constexpr int kSmem = kRing > kSums ? kRing : kSums;
+    static PerDeviceOnce once;
+    cudaError_t e = once_per_device(once, [] {
+        return cudaFuncSetAttribute(kv4_decode_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    kv4_decode_kernel<T, D, NT><<<(unsigned)blocks, kThreads, kSmem, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || blocks == 1) return e;
+    // launched while the decode kernel runs; waits for its end before it reads
+    const int rows = a.G * a.M < 8 * NT ? a.G * a.M : 8 * NT;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)rows);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, 8 * NT>, a);
+}
+
+template <typename T>
+cudaError_t launch_d(const DecodeArgs& a, int D, int rows, int blocks, cudaStream_t s) {
+    switch (D + (rows == 16)) {
+        case 32: return launch_t<T, 32, 1>(a, blocks, s);
+        case 33: return launch_t<T, 32, 2>(a, blocks, s);
+        case 64: return launch_t<T, 64, 1>(a, blocks, s);
+        case 65: return launch_t<T, 64, 2>(a, blocks, s);
+        case 128: return launch_t<T, 128, 1>(a, blocks, s);
+        default: return launch_t<T, 128, 2>(a, blocks, s);
     }
-    return cudaGetLastError();
 }
 
 constexpr int64_t kI32Max = 2147483647LL;
@@ -434,13 +712,15 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
     if (rc != ATTN_OK) return rc;
     const int G = Hkv > 0 ? Hq / Hkv : 1;
     const int64_t nq = (int64_t)B * Hq * M * D, ntab = (int64_t)B * max_pages;
-    if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + 15) / 16 > 65535)
+    const int64_t cover = (int64_t)max_pages * cache.page_size;
+    const int64_t longest = cover < max_seq_len ? cover : max_seq_len;
+    if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + 15) / 16 > 65535 ||
+        longest > kI32Max - kTile)
         return ATTN_ERR_OVERFLOW;
     if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
     if ((nq > 0 && (!q || !o)) || (ntab > 0 && !table) || (B > 0 && !lens)) return ATTN_ERR_NULL;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(table, 4) || !aligned(lens, 4)) return ATTN_ERR_ALIGN;
-    const int64_t cover = (int64_t)max_pages * cache.page_size;
-    const int max_len = (int)(cover < max_seq_len ? cover : max_seq_len);
+    const int max_len = (int)longest;
     Problem& p = c->p;
     p.B = B;
     p.Hq = Hq;
@@ -469,36 +749,26 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
 
 bool nothing_to_attend(const Kv4Call& c) { return c.max_len == 0 || c.c.num_pages == 0; }
 
+// Parts of cut segments, two per block, and the cut segments: [blocks] int4, then m, l and acc.
 size_t workspace_bytes(const Kv4Call& c) {
-    int per = 0, S = 0;
-    plan_splits(c, &per, &S);
-    return S == 1 ? 0 : split_workspace_bytes(c.p.B * c.p.Hq * c.p.M, S, c.p.D);
+    const size_t rows = (size_t)plan_blocks(c) * 2 * rows_per_block(c.p);
+    return plan_blocks(c) * sizeof(int4) + rows * (2 + c.p.D) * sizeof(float);
 }
 
 int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void* o, void* ws, size_t ws_bytes,
         cudaStream_t s) {
     const Problem& p = c.p;
-    int per = 0, S = 0;
-    plan_splits(c, &per, &S);
-    const int rows = p.B * p.Hq * p.M;
-    SplitWorkspace w{nullptr, nullptr, nullptr};
-    if (S > 1) {
-        if (!ws || ws_bytes < split_workspace_bytes(rows, S, p.D)) return ATTN_ERR_WORKSPACE;
-        if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
-        w = split_workspace(ws, rows, S, p.D);
-    }
-    const DecodeArgs a{q, c.c, table, lens, o, w.m, w.l, w.acc, p.Hq, p.Hkv, p.M, p.G, c.max_pages, c.max_len,
-                       p.causal, p.window, c.sinks, p.scale_log2, c.v_descale, per, S};
-    const int rb = rows_per_block(p);
-    const dim3 grid((unsigned)S, (unsigned)(p.B * p.Hkv), (unsigned)((p.G * p.M + rb - 1) / rb));
-    cudaError_t e;
-    if (p.dtype == ATTN_BF16)
-        e = rb == 8 ? launch_d<__nv_bfloat16, 1>(a, p.D, grid, s) : launch_d<__nv_bfloat16, 2>(a, p.D, grid, s);
-    else
-        e = rb == 8 ? launch_d<__half, 1>(a, p.D, grid, s) : launch_d<__half, 2>(a, p.D, grid, s);
-    if (e == cudaSuccess && S > 1)
-        e = launch_merge(w.m, w.l, w.acc, o, nullptr, nullptr, nullptr, rows, S, p.D, p.dtype, 1.0f, false, s,
-                         c.v_descale);
+    if (!ws || ws_bytes < workspace_bytes(c)) return ATTN_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
+    const int blocks = plan_blocks(c), rows = rows_per_block(p);
+    const size_t n = (size_t)blocks * 2 * rows;
+    int4* cut = static_cast<int4*>(ws);
+    float* wm = reinterpret_cast<float*>(cut + blocks);
+    const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G,
+                       (p.G * p.M + rows - 1) / rows, c.max_pages, c.max_len, p.causal, p.window, c.sinks,
+                       p.scale_log2, c.v_descale};
+    const cudaError_t e = p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, rows, blocks, s)
+                                               : launch_d<__half>(a, p.D, rows, blocks, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -538,7 +808,7 @@ int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scal
     if (nothing_to_attend(c))  // no sequence can hold a key: every row outputs 0
         return cudaMemsetAsync(o, 0, (size_t)B * Hq * M * D * 2, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     const size_t bytes = workspace ? 0 : workspace_bytes(c);
-    if (workspace || bytes == 0) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, s);
+    if (workspace) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, s);
     void* ws = nullptr;
     if (cudaMallocAsync(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
     rc = run(c, q, block_table, seq_lens, o, ws, bytes, s);
