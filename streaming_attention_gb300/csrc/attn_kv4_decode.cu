@@ -20,13 +20,14 @@
 // A warp's products run transposed, on m16n8k16 matrix instructions with the
 // cache as the left operand, so that a row of the cache is expanded once for all
 // the query rows: S^T = K Q^T (16 keys by 8 rows) and O^T += V^T P^T (16 elements
-// by 8 rows). Codes become FP16 in registers: a nibble in bits 4..7 of a half with
-// exponent 0x54 is 64 + n, and one fused multiply-add with s and -72 s gives
-// s (n - 8), exact in FP16 (s has 4 significant bits, n - 8 has 4).
+// by 8 rows). Codes become halves n - 8 in registers, exactly; the scales are
+// applied where there are fewer numbers than elements: a key's to the sum of a
+// group's 32 products, a value's to the probabilities, once per group.
 // Rounded below 32 bits: Q to FP16 after scaling each row by a power of two to
-// maximum 1..2 (exact for elements above 2^-14 of the maximum), and the
-// probabilities to FP16, kept 64 times too large to stay clear of its small
-// numbers; the row sum adds them unrounded.
+// maximum 1..2 (exact for elements above 2^-14 of the maximum), the probabilities
+// to FP16, kept 64 times too large to stay clear of its small numbers (the row sum
+// adds them unrounded), and their products with the values' scales (2^-9 .. 448,
+// so between 2^-3 and 28672 at probability 1) to FP16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -48,6 +49,11 @@ constexpr int kStages = 5;          // tiles in a warp's ring
 constexpr int kMinTiles = 2;        // a block's range is at least this long while there are blocks to spare
 constexpr float kPShift = 6.0f;     // probabilities are kept times 2^6
 
+// The exponents under which a nibble of a half is a small whole number (see low_nibble).
+struct Exponents {
+    uint32_t low = 0x64006400u, high = 0x54005400u;
+};
+
 struct DecodeArgs {
     const void* q;
     Kv4Cache c;
@@ -61,6 +67,7 @@ struct DecodeArgs {
     int causal, window, sinks;
     float scale_log2;  // logit scale and K factor, times log2(e)
     float v_scale;
+    Exponents ex;
 };
 
 // The tiles that any row of a sequence of L keys may see: those of the first `sinks` keys, then those of the
@@ -107,12 +114,14 @@ struct Bytes<1> {
     using T = uint8_t;
 };
 
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// D = A B + C, FP16 in, FP32 out; the left operand's four registers one by one
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, const float (&c)[4]) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 // transposes an 8 x 8 matrix of halves held by the warp (two per lane)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -120,9 +129,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -132,16 +141,27 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 // two E4M3 bytes -> two halves
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    uint32_t d;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(two));
+    return d;
 }
-constexpr uint32_t kMinus72 = 0xD480D480u;  // -72 in both halves
+__device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
-// nibble x of each half of w, as s (n - 8): s and ns = -72 s per half
-template <int x>
-__device__ __forceinline__ uint32_t expand(uint32_t w, uint32_t s, uint32_t ns) {
-    const uint32_t sh = x == 0 ? w << 4 : x == 1 ? w : x == 2 ? w >> 4 : w >> 8;
-    return hfma2((sh & 0x00F000F0u) | 0x54005400u, s, ns);
+// Nibbles x (0..3) of both halves of w as halves n - 8. Only the low byte of each half is taken, so w is the word
+// itself for x = 0 and 1 and the word shifted down by 8 for x = 2 and 3. Under the exponent 0x64 the bits 0..3 count
+// 1 on top of 1024, under 0x54 the bits 4..7 count 1 on top of 64: the subtraction is exact. The two exponents come
+// from the kernel's arguments: as constants the compiler writes both them and the masks into the instructions, which
+// takes two where one does (measured: 64 of 529 instructions of a step).
+__device__ __forceinline__ uint32_t masked_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(bits));
+    return d;
+}
+__device__ __forceinline__ uint32_t low_nibble(uint32_t w, const Exponents& e) {
+    return hadd2(masked_or(w, 0x000F000Fu, e.low), 0xE408E408u);  // - 1032
+}
+__device__ __forceinline__ uint32_t high_nibble(uint32_t w, const Exponents& e) {
+    return hadd2(masked_or(w, 0x00F000F0u, e.high), 0xD480D480u);  // - 72
 }
 
 template <typename T>
@@ -188,25 +208,40 @@ struct Stage {
     static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
     static constexpr int kBytes = 2 * kCodes + 2 * kScales;
 
-    // lane's part of the copy of rows at .. at + 15 of the pools
-    static __device__ __forceinline__ void load(uint32_t dst, const Kv4Cache& c, size_t at, int lane) {
-        constexpr int Q = kRow / 16;  // chunks of a row
-#pragma unroll
-        for (int i = 0; i < (kCodes + 511) / 512; ++i) {
-            const int x = lane + 32 * i;
-            if (kCodes >= 512 || x < kCodes / 16) {
-                const int r = x / Q, q = x % Q;
-                const int slot = (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1);
-                const int vq = D == 128 ? q ^ (r & 2) : q;
-                copy16(dst + kK + slot * kRow + q * 16, c.k_codes + at * kRow + x * 16);
-                copy16(dst + kV + r * kRow + vq * 16, c.v_codes + at * kRow + x * 16);
+    static constexpr int Q = kRow / 16;     // chunks of a row's codes
+    static constexpr int S = kScales / 16;  // chunks of 16 rows' scales
+
+    // Where a lane reads and writes; the pools' rows come in blocks of 16, numbered in 32 bits.
+    const uint8_t *k, *v, *s;
+    uint32_t to_k, to_v, to_s;
+    bool codes, scales;
+    __device__ __forceinline__ Stage(const Kv4Cache& c, int lane) {
+        const int x = lane & (kCodes / 16 - 1), r = x / Q, q = x % Q;
+        k = c.k_codes + x * 16;
+        v = c.v_codes + x * 16;
+        to_k = kK + ((r & 8) | ((r & 3) << 1) | ((r >> 2) & 1)) * kRow + q * 16;
+        to_v = kV + r * kRow + (D == 128 ? q ^ (r & 2) : q) * 16;
+        codes = lane < kCodes / 16;
+        const bool vs = lane >= S;
+        s = (vs ? c.v_scales : c.k_scales) + (vs ? lane - S : lane) * 16;
+        to_s = vs ? kVs + (lane - S) * 16 : kKs + lane * 16;
+        scales = lane < 2 * S;
+    }
+    // The lane's part of the copy of block `at`; -1, a page outside the pool, reads as zeros: scales of zero.
+    __device__ __forceinline__ void load(uint32_t dst, int at) const {
+        if (at >= 0) {
+            const size_t n = (size_t)(uint32_t)at * kCodes;
+            if (kCodes >= 512 || codes) {
+                copy16(dst + to_k, k + n);
+                copy16(dst + to_v, v + n);
+                if (kCodes == 1024) {  // rows 8 .. 15
+                    copy16(dst + to_k + 512, k + n + 512);
+                    copy16(dst + to_v + 512, v + n + 512);
+                }
             }
-        }
-        constexpr int S = kScales / 16;
-        if (lane < 2 * S) {
-            const bool v = lane >= S;
-            const int x = v ? lane - S : lane;
-            copy16(dst + (v ? kVs : kKs) + x * 16, (v ? c.v_scales : c.k_scales) + at * NG + x * 16);
+            if (scales) copy16(dst + to_s, s + (size_t)(uint32_t)at * kScales);
+        } else if (scales) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + to_s), "r"(0) : "memory");
         }
     }
 };
@@ -253,6 +288,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
     const int key_slot = (gq >> 1) + 4 * (gq & 1);  // the key of slot gq; slot gq + 8: 8 more
     uint8_t* ring = smem + warp * (kStages * St::kBytes);
     const uint32_t ring_at = ptx::smem_u32(ring);
+    const St from(a.c, lane);
+    const Exponents ex = a.ex;
+    // where the lane reads in a stage; the values' chunks of every other pair of rows are exchanged
+    const int at_k = St::kK + gq * St::kRow + cq * (4 * NG), at_ks = St::kKs + key_slot * NG;
+    const int at_v = St::kV + cq * St::kRow + (D == 128 ? (gq * 8) ^ ((cq & 2) * 16) : gq * (2 * NG));
+    const int at_vs = St::kVs + cq * NG;
     const int H = a.Hkv * a.Z;
     const int R = a.G * a.M;
     const int ps = a.c.page_size;
@@ -296,31 +337,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
         const int t1 = (int)min((long long)tl.n, t0 + (u1 - u));
         const int g = hz / a.Z, r0 = (hz % a.Z) * ROWS;
 
-        // the pool rows of this warp's keys, for 32 tiles at a time: lane x has those of tile base + x
+        // the pool's blocks of this warp's keys, for 32 tiles at a time: lane x has that of tile base + x
         const int* trow = a.table + (size_t)b * a.max_pages;
         const auto key_of = [&](int t) { return tl.at(t) * kTile + warp * 16; };
         const auto page_of = [&](int t) {
             const int j = key_of(t);
             return t < t1 && j < L ? __ldg(trow + j / ps) : -1;
         };
-        const auto row_of = [&](int page, int t) {  // -1: a page outside the pool, or nothing to read
-            return page >= 0 && page < a.c.num_pages ? ((long long)page * a.Hkv + g) * ps + key_of(t) % ps : -1;
+        const auto block_of = [&](int page, int t) {  // -1: a page outside the pool, or nothing to read
+            return page >= 0 && page < a.c.num_pages ? (page * a.Hkv + g) * (ps / 16) + key_of(t) % ps / 16 : -1;
         };
         int base = t0;
         int next_page = page_of(t0 + lane);
-        long long rows_at = row_of(next_page, t0 + lane);
+        int blocks_at = block_of(next_page, t0 + lane);
         next_page = page_of(t0 + 32 + lane);
-        uint32_t held = 0;  // bit t % 32: the stage of tile t was read from the pool
+        uint32_t fill = 0, read = 0;  // the ring's places, in bytes
         const auto issue = [&](int t) {
             if (t < t1) {
                 if (t - base == 32) {
                     base = t;
-                    rows_at = row_of(next_page, t + lane);
+                    blocks_at = block_of(next_page, t + lane);
                     next_page = page_of(t + 32 + lane);
                 }
-                const long long at = __shfl_sync(0xffffffffu, rows_at, t - base);
-                if (at >= 0) St::load(ring_at + (t % kStages) * St::kBytes, a.c, (size_t)at, lane);
-                held = (held & ~(1u << (t & 31))) | ((at >= 0 ? 1u : 0u) << (t & 31));
+                from.load(ring_at + fill, __shfl_sync(0xffffffffu, blocks_at, t - base));
+                fill = fill == (kStages - 1) * St::kBytes ? 0 : fill + St::kBytes;
             }
             copy_commit();
         };
@@ -392,64 +432,84 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
                 for (int e = 0; e < 4; ++e) acc[nt][n][e] = 0.f;
         }
 
-        for (int t = t0; t < t1; ++t) {
+        int j0 = key_of(t0);
+        const int after_sink = tl.sink - 1;
+        const int jump = (tl.win - tl.sink + 1) * kTile;  // from the last tile of the sinks to the window's first
+        for (int t = t0; t < t1; ++t, j0 += t - 1 == after_sink ? jump : kTile) {
             copy_wait<kStages - 2>();
             __syncwarp();
-            issue(t + kStages - 1);  // into the stage that was read in the last step
-            const int j0 = key_of(t);
+            issue(t + kStages - 1);  // into the place that was read in the last step
+            const uint8_t* st = ring + read;
+            read = read == (kStages - 1) * St::kBytes ? 0 : read + St::kBytes;
             if (j0 >= L) continue;
-            const bool live = (held >> (t & 31)) & 1u;  // a page outside the pool reads as zeros
-            const uint8_t* st = ring + (t % kStages) * St::kBytes;
 
-            // ---- S^T = K Q^T ----
+            // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
             float s[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
             {
                 union {
                     KChunk v;
                     uint32_t w[NG];
                 } k0, k1;
-                k0.v = *reinterpret_cast<const KChunk*>(st + St::kK + gq * St::kRow + cq * (4 * NG));
-                k1.v = *reinterpret_cast<const KChunk*>(st + St::kK + (gq + 8) * St::kRow + cq * (4 * NG));
-                uint32_t s0 = *reinterpret_cast<const Scales*>(st + St::kKs + key_slot * NG);
-                uint32_t s1 = *reinterpret_cast<const Scales*>(st + St::kKs + (key_slot + 8) * NG);
-                if (!live) s0 = s1 = 0;
+                k0.v = *reinterpret_cast<const KChunk*>(st + at_k);
+                k1.v = *reinterpret_cast<const KChunk*>(st + at_k + 8 * St::kRow);
+                const uint32_t s0 = *reinterpret_cast<const Scales*>(st + at_ks);
+                const uint32_t s1 = *reinterpret_cast<const Scales*>(st + at_ks + 8 * NG);
+                float f0[NG < 2 ? 2 : NG], f1[NG < 2 ? 2 : NG];
+#pragma unroll
+                for (int n = 0; n < NG; n += 2) {
+                    const float2 x = halves(e4m3x2(s0 >> (8 * n))), y = halves(e4m3x2(s1 >> (8 * n)));
+                    f0[n] = x.x;
+                    f0[n + 1] = x.y;
+                    f1[n] = y.x;
+                    f1[n + 1] = y.y;
+                }
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    // the scale in both halves
-                    const uint32_t f0 = e4m3x2(((s0 >> (8 * n)) & 0xFFu) * 0x0101u);
-                    const uint32_t f1 = e4m3x2(((s1 >> (8 * n)) & 0xFFu) * 0x0101u);
-                    const uint32_t n0 = hmul2(f0, kMinus72), n1 = hmul2(f1, kMinus72);
-                    const uint32_t x0[4] = {expand<0>(k0.w[n], f0, n0), expand<0>(k1.w[n], f1, n1),
-                                            expand<1>(k0.w[n], f0, n0), expand<1>(k1.w[n], f1, n1)};
-                    const uint32_t x1[4] = {expand<2>(k0.w[n], f0, n0), expand<2>(k1.w[n], f1, n1),
-                                            expand<3>(k0.w[n], f0, n0), expand<3>(k1.w[n], f1, n1)};
+                    const uint32_t u0 = k0.w[n], u1 = k1.w[n], h0 = u0 >> 8, h1 = u1 >> 8;
+                    const uint32_t a0 = low_nibble(u0, ex), a1 = low_nibble(u1, ex), a2 = high_nibble(u0, ex), a3 = high_nibble(u1, ex);
+                    const uint32_t c0 = low_nibble(h0, ex), c1 = low_nibble(h1, ex), c2 = high_nibble(h0, ex), c3 = high_nibble(h1, ex);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(s[nt], x0, qf[nt][n][0][0], qf[nt][n][0][1]);
-                        mma_16816(s[nt], x1, qf[nt][n][1][0], qf[nt][n][1][1]);
+                        float x[4];
+                        mma_16816(x, a0, a1, a2, a3, qf[nt][n][0][0], qf[nt][n][0][1], zero);
+                        mma_16816(x, c0, c1, c2, c3, qf[nt][n][1][0], qf[nt][n][1][1], x);
+                        if (n == 0) {
+                            s[nt][0] = x[0] * f0[n];
+                            s[nt][1] = x[1] * f0[n];
+                            s[nt][2] = x[2] * f1[n];
+                            s[nt][3] = x[3] * f1[n];
+                        } else {
+                            s[nt][0] = fmaf(x[0], f0[n], s[nt][0]);
+                            s[nt][1] = fmaf(x[1], f0[n], s[nt][1]);
+                            s[nt][2] = fmaf(x[2], f1[n], s[nt][2]);
+                            s[nt][3] = fmaf(x[3], f1[n], s[nt][3]);
+                        }
                     }
                 }
             }
 
             // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
             const bool whole = j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks);
-            bool rises = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[nt][e] *= sc[nt][e & 1];
-                    if (!whole) {
+                for (int e = 0; e < 4; ++e) s[nt][e] *= sc[nt][e & 1];
+            if (!whole) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         const int j = j0 + key_slot + 8 * (e >> 1);
                         const bool see = j < vis_hi[nt][e & 1] && (j >= vis_lo[nt][e & 1] || j < a.sinks);
                         if (!see) s[nt][e] = -INFINITY;  // a masked key scores -inf
                     }
-                    rises |= s[nt][e] > m[nt][e & 1];
-                }
+            }
+            bool rises = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rises |= s[nt][e] > m[nt][e & 1];
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -483,39 +543,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
                 pb[nt][1] = transpose8(ptx::pack_f16(p[2], p[3]));
             }
 
-            // ---- O^T += V^T P^T: the lane's keys are cq + 4 e ----
+            // ---- O^T += V^T (P s)^T: the lane's keys are cq + 4 e ----
             {
                 union VWords {
                     VChunk v;
                     uint32_t w[(NG + 1) / 2];
                 } v[4];
-                uint32_t vs[4];
+                uint32_t vs[4], vs2[2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int k = cq + 4 * e;
-                    const int byte = D == 128 ? (gq * 8) ^ ((k & 2) * 16) : gq * (2 * NG);
                     v[e].w[0] = 0;
-                    v[e].v = *reinterpret_cast<const VChunk*>(st + St::kV + k * St::kRow + byte);
-                    vs[e] = *reinterpret_cast<const Scales*>(st + St::kVs + k * NG);
-                    // whatever stands behind the sequence, and a page outside the pool, counts as zero
-                    if (!live || (!whole && j0 + k >= L)) vs[e] = 0;
+                    v[e].v = *reinterpret_cast<const VChunk*>(st + at_v + 4 * e * St::kRow);
+                    vs[e] = *reinterpret_cast<const Scales*>(st + at_vs + 4 * e * NG);
+                }
+                if (!whole) {  // whatever stands behind the sequence counts as zero
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j0 + cq + 4 * e >= L) vs[e] = 0;
                 }
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    const uint32_t pick = n & 1 ? 0x7632u : 0x5410u, byte = (uint32_t)(n | ((4 + n) << 4));
-                    const uint32_t w0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], pick);
-                    const uint32_t w1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], pick);
-                    const uint32_t f0 = e4m3x2(__byte_perm(vs[0], vs[1], byte));
-                    const uint32_t f1 = e4m3x2(__byte_perm(vs[2], vs[3], byte));
-                    const uint32_t n0 = hmul2(f0, kMinus72), n1 = hmul2(f1, kMinus72);
-                    const uint32_t x0[4] = {expand<0>(w0, f0, n0), expand<1>(w0, f0, n0), expand<0>(w1, f1, n1),
-                                            expand<1>(w1, f1, n1)};
-                    const uint32_t x1[4] = {expand<2>(w0, f0, n0), expand<3>(w0, f0, n0), expand<2>(w1, f1, n1),
-                                            expand<3>(w1, f1, n1)};
+                    if (n % 2 == 0) {  // scales of two groups, those of a pair of keys side by side
+                        const uint32_t pick = n == 0 ? 0x5140u : 0x7362u;
+                        vs2[0] = __byte_perm(vs[0], vs[1], pick);
+                        vs2[1] = __byte_perm(vs[2], vs[3], pick);
+                    }
+                    const uint32_t f0 = e4m3x2(vs2[0] >> (16 * (n % 2))), f1 = e4m3x2(vs2[1] >> (16 * (n % 2)));
+                    // the unit of group n of both keys of a pair: its low byte and its high byte
+                    const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
+                    const uint32_t u0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], lo);
+                    const uint32_t u1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], lo);
+                    const uint32_t h0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], hi);
+                    const uint32_t h1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], hi);
+                    const uint32_t a0 = low_nibble(u0, ex), a1 = high_nibble(u0, ex), a2 = low_nibble(u1, ex), a3 = high_nibble(u1, ex);
+                    const uint32_t c0 = low_nibble(h0, ex), c1 = high_nibble(h0, ex), c2 = low_nibble(h1, ex), c3 = high_nibble(h1, ex);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(acc[nt][2 * n], x0, pb[nt][0], pb[nt][1]);
-                        mma_16816(acc[nt][2 * n + 1], x1, pb[nt][0], pb[nt][1]);
+                        const uint32_t p0 = hmul2(pb[nt][0], f0), p1 = hmul2(pb[nt][1], f1);
+                        mma_16816(acc[nt][2 * n], a0, a1, a2, a3, p0, p1, acc[nt][2 * n]);
+                        mma_16816(acc[nt][2 * n + 1], c0, c1, c2, c3, p0, p1, acc[nt][2 * n + 1]);
                     }
                 }
             }
@@ -715,7 +781,7 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
     const int64_t cover = (int64_t)max_pages * cache.page_size;
     const int64_t longest = cover < max_seq_len ? cover : max_seq_len;
     if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + 15) / 16 > 65535 ||
-        longest > kI32Max - kTile)
+        longest > kI32Max - kTile || (int64_t)cache.num_pages * (cache.page_size / 16) * Hkv > kI32Max)
         return ATTN_ERR_OVERFLOW;
     if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
     if ((nq > 0 && (!q || !o)) || (ntab > 0 && !table) || (B > 0 && !lens)) return ATTN_ERR_NULL;
@@ -766,7 +832,7 @@ int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void
     float* wm = reinterpret_cast<float*>(cut + blocks);
     const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G,
                        (p.G * p.M + rows - 1) / rows, c.max_pages, c.max_len, p.causal, p.window, c.sinks,
-                       p.scale_log2, c.v_descale};
+                       p.scale_log2, c.v_descale, Exponents{}};
     const cudaError_t e = p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, rows, blocks, s)
                                                : launch_d<__half>(a, p.D, rows, blocks, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -82,11 +82,14 @@ def visible(L, M, i, causal, window, sinks):
     return see
 
 
-def attention(q, k, v, causal, window, sinks, scale, out_dtype):
+def attention(q, k, v, causal, window, sinks, scale, out_dtype, vd=0.125):
     """Rows q [Hq, M, D] over k, v [Hkv, L, D], 64-bit numpy: (o, bound). The bound per element counts
       the output's rounding                            eps/2 |o|
-      the probabilities' rounding to FP16              2^-11 A,            A = sum w |v|
-      those below its normal range (2^-14 of 2^6)      L 2^-31 max|v|
+      two roundings to FP16, of the probability p (times 2^6, at most 2^6) and of its product with the
+      value's scale                                    2 * 2^-11 A,        A = sum w |v|
+      such products below FP16's normal range: each is off by at most 2^-25, times a code of at most 8 and
+      the factor vd, over a sum of p that is at least 2^6; the same again for p itself
+                                                       L 2 * 2^-25 8 vd / 2^6 max(1, s)
       FP32 sums over the keys, 16 a matrix instruction (L/16 + 64) 2^-23 A
       the logits: the query's small elements (2^-25 of the row's largest), FP32 sums over D (truncating
       adders counted: 2^-23 a term) and the exponent's argument, whose error counts twice (weight and sum)."""
@@ -111,8 +114,9 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype):
             logit = (D + 8) * 2.0 ** -23 * size + 2.0 ** -25 * np.abs(qq).max() * abs(scale) * np.abs(kk).sum(1)
             logit = (logit + 4 * 2.0 ** -24 * (np.abs(s) + abs(s.max()))).max()
             n = len(s)
-            bound[h, i] = (half * np.abs(o[h, i]) + A * (2.0 ** -11 + (n / 16 + 64) * 2.0 ** -23 + 2 * logit)
-                           + n * 2.0 ** -31 * np.abs(vv).max() + 1e-30)
+            small = n * 2.0 ** -27 * max(vd, np.abs(vv).max())  # 8 vd s is at most the largest value and more
+            bound[h, i] = (half * np.abs(o[h, i]) + A * (2.0 ** -10 + (n / 16 + 64) * 2.0 ** -23 + 2 * logit)
+                           + small + 1e-30)
             if out_dtype == torch.float16:
                 bound[h, i] += 2.0 ** -25  # its smallest numbers
     return o, bound
