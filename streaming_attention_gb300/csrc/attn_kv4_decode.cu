@@ -20,17 +20,27 @@
 // A warp's products run transposed, on m16n8k16 matrix instructions with the
 // cache as the left operand, so that a row of the cache is expanded once for all
 // the query rows: S^T = K Q^T (16 keys by 8 rows) and O^T += V^T P^T (16 elements
-// by 8 rows). Codes become halves n - 8 in registers, exactly; the scales are
-// applied where there are fewer numbers than elements: a key's to the sum of a
-// group's 32 products, a value's to the probabilities, once per group.
+// by 8 rows). A nibble masked out of a 16-bit half is an FP16 number as it stands:
+// below 2^11 a half's bits count units of 2^-24, so bits 0..3 are n 2^-24 and bits
+// 4..7 are n 2^-20, exactly, and the matrix instructions take FP16's small numbers
+// at full value. One AND per two elements is all the expansion there is; the factor
+// 16 between the two kinds goes into Q (keys) or into the outputs (values), and the
+// 8 of n - 8 is subtracted from sums: 8 times a group's sum of Q is where the key
+// product's accumulator starts, and the sums of P, which a product with a matrix of
+// ones gives in the accumulators' own layout, are taken off at the end. (Exact
+// n - 8 in halves took one more addition per pair: 430 -> 350 instructions per 16
+// keys.) The scales are applied where there are fewer numbers than elements: a
+// key's to the sum of a group's 32 products, a value's to the probabilities, once
+// per group.
 // Rounded below 32 bits: Q to FP16 after scaling each row by a power of two to
-// maximum 1..2 (exact for elements above 2^-14 of the maximum), the probabilities
-// to FP16, kept 64 times too large to stay clear of its small numbers (the row sum
-// adds them unrounded), and their products with the values' scales (2^-9 .. 448,
-// so between 2^-3 and 28672 at probability 1) to FP16.
+// maximum 2^14..2^15 (exact for elements above 2^-20 of the maximum), the
+// probabilities to FP16, kept 64 times too large to stay clear of its small numbers
+// (the row sum adds them unrounded), and their products with the values' scales
+// (2^-9 .. 448, so between 2^-3 and 28672 at probability 1) to FP16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -49,11 +59,6 @@ constexpr int kStages = 5;          // tiles in a warp's ring
 constexpr int kMinTiles = 2;        // a block's range is at least this long while there are blocks to spare
 constexpr float kPShift = 6.0f;     // probabilities are kept times 2^6
 
-// The exponents under which a nibble of a half is a small whole number (see low_nibble).
-struct Exponents {
-    uint32_t low = 0x64006400u, high = 0x54005400u;
-};
-
 struct DecodeArgs {
     const void* q;
     Kv4Cache c;
@@ -67,7 +72,6 @@ struct DecodeArgs {
     int causal, window, sinks;
     float scale_log2;  // logit scale and K factor, times log2(e)
     float v_scale;
-    Exponents ex;
 };
 
 // The tiles that any row of a sequence of L keys may see: those of the first `sinks` keys, then those of the
@@ -91,29 +95,6 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
     return min(max(__ldg(a.lens + b), 0), a.max_len);
 }
 
-template <int N>
-struct Bytes;
-template <>
-struct Bytes<16> {
-    using T = uint4;
-};
-template <>
-struct Bytes<8> {
-    using T = uint2;
-};
-template <>
-struct Bytes<4> {
-    using T = uint32_t;
-};
-template <>
-struct Bytes<2> {
-    using T = uint16_t;
-};
-template <>
-struct Bytes<1> {
-    using T = uint8_t;
-};
-
 // D = A B + C, FP16 in, FP32 out; the left operand's four registers one by one
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1, const float (&c)[4]) {
@@ -129,11 +110,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -145,23 +121,50 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(two));
     return d;
 }
+// pairs of floats in one instruction
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+    ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(x, y), ptx::f2_pack(a, b)), x, y);
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(x, y), ptx::f2_pack(a, b)), x, y);
+}
+__device__ __forceinline__ void sub2(float& x, float& y, float a, float b) { add2(x, y, -a, -b); }
 __device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
-// Nibbles x (0..3) of both halves of w as halves n - 8. Only the low byte of each half is taken, so w is the word
-// itself for x = 0 and 1 and the word shifted down by 8 for x = 2 and 3. Under the exponent 0x64 the bits 0..3 count
-// 1 on top of 1024, under 0x54 the bits 4..7 count 1 on top of 64: the subtraction is exact. The two exponents come
-// from the kernel's arguments: as constants the compiler writes both them and the masks into the instructions, which
-// takes two where one does (measured: 64 of 529 instructions of a step).
-__device__ __forceinline__ uint32_t masked_or(uint32_t w, uint32_t mask, uint32_t bits) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(bits));
-    return d;
+// Bits 0..3 and 4..7 of both halves: n 2^-24 and n 2^-20 as FP16.
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+constexpr float kLowUnit = 0x1p-24f, kHighUnit = 0x1p-20f;
+constexpr uint32_t kOnes = 0x3C003C00u;
+
+// shared memory by its 32-bit address
+__device__ __forceinline__ void load_shared(uint32_t (&w)[4], uint32_t at) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at)
+                 : "memory");
 }
-__device__ __forceinline__ uint32_t low_nibble(uint32_t w, const Exponents& e) {
-    return hadd2(masked_or(w, 0x000F000Fu, e.low), 0xE408E408u);  // - 1032
+__device__ __forceinline__ void load_shared(uint32_t (&w)[2], uint32_t at) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ uint32_t high_nibble(uint32_t w, const Exponents& e) {
-    return hadd2(masked_or(w, 0x00F000F0u, e.high), 0xD480D480u);  // - 72
+__device__ __forceinline__ void load_shared(uint32_t (&w)[1], uint32_t at) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+}
+// 1, 2 or 4 bytes, the rest zero
+template <int N>
+__device__ __forceinline__ uint32_t load_shared_small(uint32_t at) {
+    uint32_t w;
+    if constexpr (N == 4)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(w) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+    return w;
+}
+__device__ __forceinline__ const void* row_block(const uint8_t* pool, uint32_t block, uint32_t bytes) {
+    uint64_t p;
+    asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(p) : "r"(block), "r"(bytes), "l"(reinterpret_cast<uint64_t>(pool)));
+    return reinterpret_cast<const void*>(p);
 }
 
 template <typename T>
@@ -192,6 +195,22 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The part of a segment that a block is at: tiles [t0, t1) of it. Kept in shared memory, so that what the warps need
+// only before and after a part's tiles takes no registers while they run through them.
+struct Part {
+    long long u, rem;    // tiles before the part: of all, and of its sequence
+    long long end, total, blocks;  // the block's range ends at tile `end` of `total`; blocks with a range
+    int b, L, hz, t0, t1;
+    Tiles tl;
+};
+__device__ __forceinline__ void set_part(Part& p, const DecodeArgs& a) {
+    p.L = length_of(a, p.b);
+    p.tl = tiles_of(a, p.L);
+    p.hz = (int)(p.rem / p.tl.n);
+    p.t0 = (int)(p.rem % p.tl.n);
+    p.t1 = (int)min((long long)p.tl.n, p.t0 + (p.end - p.u));
 }
 
 // One stage of a warp's ring: the codes and scales of 16 keys and values. Row `slot` of the S^T product's left
@@ -230,16 +249,17 @@ struct Stage {
     // The lane's part of the copy of block `at`; -1, a page outside the pool, reads as zeros: scales of zero.
     __device__ __forceinline__ void load(uint32_t dst, int at) const {
         if (at >= 0) {
-            const size_t n = (size_t)(uint32_t)at * kCodes;
             if (kCodes >= 512 || codes) {
-                copy16(dst + to_k, k + n);
-                copy16(dst + to_v, v + n);
+                const uint8_t* kp = static_cast<const uint8_t*>(row_block(k, (uint32_t)at, kCodes));
+                const uint8_t* vp = static_cast<const uint8_t*>(row_block(v, (uint32_t)at, kCodes));
+                copy16(dst + to_k, kp);
+                copy16(dst + to_v, vp);
                 if (kCodes == 1024) {  // rows 8 .. 15
-                    copy16(dst + to_k + 512, k + n + 512);
-                    copy16(dst + to_v + 512, v + n + 512);
+                    copy16(dst + to_k + 512, kp + 512);
+                    copy16(dst + to_v + 512, vp + 512);
                 }
             }
-            if (scales) copy16(dst + to_s, s + (size_t)(uint32_t)at * kScales);
+            if (scales) copy16(dst + to_s, row_block(s, (uint32_t)at, kScales));
         } else if (scales) {
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + to_s), "r"(0) : "memory");
         }
@@ -273,23 +293,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
     constexpr int ROWS = 8 * NT;
-    using KChunk = typename Bytes<4 * NG>::T;
-    using VChunk = typename Bytes<2 * NG>::T;
-    using Scales = typename Bytes<NG>::T;
     extern __shared__ __align__(16) uint8_t smem[];
     // the rings, and after them in the same place the warps' sums of a part
     float* sm_acc = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D]
     __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-    __shared__ long long part[kWarps], found_before;
-    __shared__ int found_b;
+    __shared__ int2 sm_vis[ROWS];  // the visible range of every row
+    __shared__ long long sums[kWarps];
+    __shared__ Part part;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, cq = lane & 3;  // the lane's place in a matrix fragment
     const int key_slot = (gq >> 1) + 4 * (gq & 1);  // the key of slot gq; slot gq + 8: 8 more
-    uint8_t* ring = smem + warp * (kStages * St::kBytes);
-    const uint32_t ring_at = ptx::smem_u32(ring);
+    const uint32_t ring = ptx::smem_u32(smem) + warp * (kStages * St::kBytes);
     const St from(a.c, lane);
-    const Exponents ex = a.ex;
     // where the lane reads in a stage; the values' chunks of every other pair of rows are exchanged
     const int at_k = St::kK + gq * St::kRow + cq * (4 * NG), at_ks = St::kKs + key_slot * NG;
     const int at_v = St::kV + cq * St::kRow + (D == 128 ? (gq * 8) ^ ((cq & 2) * 16) : gq * (2 * NG));
@@ -301,41 +317,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- this block's range of the tiles ----
-    long long total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        long long all;
-        block_sum(b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0, part, &all);
-        total += all;
-    }
-    const long long want = (total + kMinTiles - 1) / kMinTiles;
-    const long long blocks = want < gridDim.x ? want : gridDim.x;
-    if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (blockIdx.x >= blocks) return;
-    const long long u0 = total * blockIdx.x / blocks, u1 = total * (blockIdx.x + 1) / blocks;
-    long long before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        const long long n = b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0;
-        long long all;
-        const long long s = before + block_sum(n, part, &all);
-        if (s <= u0 && u0 < s + n) {
-            found_b = b;
-            found_before = s;
+    {
+        long long total = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            long long all;
+            block_sum(b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0, sums, &all);
+            total += all;
         }
-        before += all;
-        if (u0 < before) break;
+        const long long want = (total + kMinTiles - 1) / kMinTiles;
+        const long long blocks = want < gridDim.x ? want : gridDim.x;
+        if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (blockIdx.x >= blocks) return;
+        const long long u0 = total * blockIdx.x / blocks;
+        long long before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + threadIdx.x;
+            const long long n = b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0;
+            long long all;
+            const long long s = before + block_sum(n, sums, &all);
+            if (s <= u0 && u0 < s + n) {
+                part.u = u0;
+                part.rem = u0 - s;
+                part.end = total * (blockIdx.x + 1) / blocks;
+                part.total = total;
+                part.blocks = blocks;
+                part.b = b;
+                set_part(part, a);
+            }
+            before += all;
+            if (u0 < before) break;
+        }
     }
-    __syncthreads();
-    int b = found_b;
-    long long rem = u0 - found_before;  // tiles of sequence b before this block's
 
-    for (long long u = u0; u < u1;) {
-        const int L = length_of(a, b);
-        const Tiles tl = tiles_of(a, L);
-        const int hz = (int)(rem / tl.n), t0 = (int)(rem % tl.n);
-        const int t1 = (int)min((long long)tl.n, t0 + (u1 - u));
-        const int g = hz / a.Z, r0 = (hz % a.Z) * ROWS;
+    for (;;) {
+        __syncthreads();  // the part is set; the last one's sums are read
+        if (part.u >= part.end) return;
+        const int b = part.b, L = part.L, t0 = part.t0, t1 = part.t1;
+        const Tiles tl = part.tl;
+        const int g = part.hz / a.Z, r0 = (part.hz % a.Z) * ROWS;
 
         // the pool's blocks of this warp's keys, for 32 tiles at a time: lane x has that of tile base + x
         const int* trow = a.table + (size_t)b * a.max_pages;
@@ -359,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
                     blocks_at = block_of(next_page, t + lane);
                     next_page = page_of(t + 32 + lane);
                 }
-                from.load(ring_at + fill, __shfl_sync(0xffffffffu, blocks_at, t - base));
+                from.load(ring + fill, __shfl_sync(0xffffffffu, blocks_at, t - base));
                 fill = fill == (kStages - 1) * St::kBytes ? 0 : fill + St::kBytes;
             }
             copy_commit();
@@ -367,10 +387,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
 #pragma unroll
         for (int x = 0; x < kStages - 1; ++x) issue(t0 + x);
 
-        // Q^T fragments, each row scaled to maximum 1..2, and the visible range of the lane's own rows
+        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that)
+        // and minus 8 times their sums by group
         uint32_t qf[NT][NG][2][2];
+        float start[NT][NG][2];
         float sc[NT][2];
-        int vis_lo[NT][2], vis_hi[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = r0 + nt * 8 + gq;
@@ -396,40 +417,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
             int e = (int)(__float_as_uint(top) >> 23);
             e = top == 0.f ? 127 : min(max(e, 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-            const float up = __uint_as_float((uint32_t)e << 23) * a.scale_log2;
+            const float up = __uint_as_float((uint32_t)e << 23) * a.scale_log2 * (0x1p-14f / kLowUnit);
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
+            for (int n = 0; n < NG; ++n) {
+                float sum = 0.f;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        qf[nt][n][s][t] = ptx::pack_f16(x[n][2 * s + t] * down, x[n][4 + 2 * s + t] * down);
+                    for (int t = 0; t < 2; ++t) {
+                        const float unit = t == 0 ? 0x1p14f : 0x1p14f * (kLowUnit / kHighUnit);
+                        qf[nt][n][s][t] = ptx::pack_f16(x[n][2 * s + t] * down * unit, x[n][4 + 2 * s + t] * down * unit);
+                        const float2 y = halves(qf[nt][n][s][t]);
+                        sum += (y.x + y.y) * (t == 0 ? kLowUnit : kHighUnit);
+                    }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) start[nt][n][t] = -8.f * __shfl_sync(0xffffffffu, sum, (2 * cq + t) * 4);
+            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 sc[nt][t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
-                const int rt = r0 + nt * 8 + 2 * cq + t;
-                const int p = rt < R ? rt % a.M + L - a.M : L - 1;
-                key_range(p, L, a.causal, a.window, &vis_lo[nt][t], &vis_hi[nt][t]);
             }
         }
+        if (lane < ROWS) {  // every warp writes the same
+            const int p = r0 + lane < R ? (r0 + lane) % a.M + L - a.M : L - 1;
+            int2 v;
+            key_range(p, L, a.causal, a.window, &v.x, &v.y);
+            sm_vis[lane] = v;
+        }
+        __syncwarp();
         // keys [all_lo, all_hi) are visible to every row
         int all_lo, all_hi, skip;
         key_range(L - 1, L, a.causal, a.window, &all_lo, &skip);
         key_range(L - a.M, L, a.causal, a.window, &skip, &all_hi);
 
-        float m[NT][2], mu[NT][2], l[NT][2], acc[NT][2 * NG][4];
+        float m[NT][2], l[NT][2], acc[NT][2 * NG][4];
+        float psum[NT][NG][2];  // of the probabilities times a group's scales, as rounded for the products
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                m[nt][t] = -INFINITY;
-                mu[nt][t] = -kPShift;  // m less the shift; while every key so far is masked, 0 stands for m
+                m[nt][t] = -FLT_MAX;  // finite: a masked key's -inf less it is -inf, never NaN
                 l[nt][t] = 0.f;
             }
 #pragma unroll
             for (int n = 0; n < 2 * NG; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[nt][n][e] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NG; ++n) psum[nt][n][0] = psum[nt][n][1] = 0.f;
         }
 
         int j0 = key_of(t0);
@@ -439,73 +476,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
             copy_wait<kStages - 2>();
             __syncwarp();
             issue(t + kStages - 1);  // into the place that was read in the last step
-            const uint8_t* st = ring + read;
+            const uint32_t st = ring + read;
             read = read == (kStages - 1) * St::kBytes ? 0 : read + St::kBytes;
             if (j0 >= L) continue;
 
             // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
             float s[NT][4];
             {
-                union {
-                    KChunk v;
-                    uint32_t w[NG];
-                } k0, k1;
-                k0.v = *reinterpret_cast<const KChunk*>(st + at_k);
-                k1.v = *reinterpret_cast<const KChunk*>(st + at_k + 8 * St::kRow);
-                const uint32_t s0 = *reinterpret_cast<const Scales*>(st + at_ks);
-                const uint32_t s1 = *reinterpret_cast<const Scales*>(st + at_ks + 8 * NG);
-                float f0[NG < 2 ? 2 : NG], f1[NG < 2 ? 2 : NG];
+                uint32_t k0[NG], k1[NG];
+                load_shared(k0, st + at_k);
+                load_shared(k1, st + at_k + 8 * St::kRow);
+                const uint32_t s0 = load_shared_small<NG>(st + at_ks), s1 = load_shared_small<NG>(st + at_ks + 8 * NG);
+                float2 f0[(NG + 1) / 2], f1[(NG + 1) / 2];
 #pragma unroll
                 for (int n = 0; n < NG; n += 2) {
-                    const float2 x = halves(e4m3x2(s0 >> (8 * n))), y = halves(e4m3x2(s1 >> (8 * n)));
-                    f0[n] = x.x;
-                    f0[n + 1] = x.y;
-                    f1[n] = y.x;
-                    f1[n + 1] = y.y;
+                    f0[n / 2] = halves(e4m3x2(s0 >> (8 * n)));
+                    f1[n / 2] = halves(e4m3x2(s1 >> (8 * n)));
                 }
-                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    const uint32_t u0 = k0.w[n], u1 = k1.w[n], h0 = u0 >> 8, h1 = u1 >> 8;
-                    const uint32_t a0 = low_nibble(u0, ex), a1 = low_nibble(u1, ex), a2 = high_nibble(u0, ex), a3 = high_nibble(u1, ex);
-                    const uint32_t c0 = low_nibble(h0, ex), c1 = low_nibble(h1, ex), c2 = high_nibble(h0, ex), c3 = high_nibble(h1, ex);
+                    const uint32_t h0 = k0[n] >> 8, h1 = k1[n] >> 8;
+                    const float y0 = n & 1 ? f0[n / 2].y : f0[n / 2].x, y1 = n & 1 ? f1[n / 2].y : f1[n / 2].x;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float x[4];
-                        mma_16816(x, a0, a1, a2, a3, qf[nt][n][0][0], qf[nt][n][0][1], zero);
-                        mma_16816(x, c0, c1, c2, c3, qf[nt][n][1][0], qf[nt][n][1][1], x);
-                        if (n == 0) {
-                            s[nt][0] = x[0] * f0[n];
-                            s[nt][1] = x[1] * f0[n];
-                            s[nt][2] = x[2] * f1[n];
-                            s[nt][3] = x[3] * f1[n];
-                        } else {
-                            s[nt][0] = fmaf(x[0], f0[n], s[nt][0]);
-                            s[nt][1] = fmaf(x[1], f0[n], s[nt][1]);
-                            s[nt][2] = fmaf(x[2], f1[n], s[nt][2]);
-                            s[nt][3] = fmaf(x[3], f1[n], s[nt][3]);
-                        }
+                        float x[4] = {start[nt][n][0], start[nt][n][1], start[nt][n][0], start[nt][n][1]};
+                        mma_16816(x, k0[n] & kLow, k1[n] & kLow, k0[n] & kHigh, k1[n] & kHigh, qf[nt][n][0][0],
+                                  qf[nt][n][0][1], x);
+                        mma_16816(x, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qf[nt][n][1][0], qf[nt][n][1][1], x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(x[e], e < 2 ? y0 : y1, n == 0 ? 0.f : s[nt][e]);
                     }
                 }
             }
 
             // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
             const bool whole = j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks);
+            bool rises = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] *= sc[nt][e & 1];
+            for (int nt = 0; nt < NT; ++nt) {
+                mul2(s[nt][0], s[nt][1], sc[nt][0], sc[nt][1]);
+                mul2(s[nt][2], s[nt][3], sc[nt][0], sc[nt][1]);
+            }
             if (!whole) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int j = j0 + key_slot + 8 * (e >> 1);
-                        const bool see = j < vis_hi[nt][e & 1] && (j >= vis_lo[nt][e & 1] || j < a.sinks);
-                        if (!see) s[nt][e] = -INFINITY;  // a masked key scores -inf
+                        const int2 vis = sm_vis[nt * 8 + 2 * cq + (e & 1)];
+                        if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[nt][e] = -INFINITY;  // a masked key scores -inf
                     }
             }
-            bool rises = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -518,43 +539,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
                         float mx = fmaxf(m[nt][e], fmaxf(s[nt][e], s[nt][2 + e]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        if (mx > m[nt][e]) {
-                            const float alpha = ptx::ex2(m[nt][e] - mx);
-                            m[nt][e] = mx;
-                            mu[nt][e] = mx - kPShift;
-                            l[nt][e] *= alpha;
+                        const float alpha = ptx::ex2(m[nt][e] - mx);
+                        m[nt][e] = mx;
+                        l[nt][e] *= alpha;
 #pragma unroll
-                            for (int n = 0; n < 2 * NG; ++n) {
-                                acc[nt][n][e] *= alpha;
-                                acc[nt][n][2 + e] *= alpha;
-                            }
+                        for (int n = 0; n < 2 * NG; ++n) {
+                            acc[nt][n][e] *= alpha;
+                            acc[nt][n][2 + e] *= alpha;
                         }
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) psum[nt][n][e] *= alpha;
                     }
             }
             uint32_t pb[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
+                float mu0 = kPShift, mu1 = kPShift;
+                sub2(mu0, mu1, m[nt][0], m[nt][1]);
+                add2(s[nt][0], s[nt][1], mu0, mu1);
+                add2(s[nt][2], s[nt][3], mu0, mu1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ptx::ex2(s[nt][e] - mu[nt][e & 1]);
-                l[nt][0] += p[0] + p[2];
-                l[nt][1] += p[1] + p[3];
-                pb[nt][0] = transpose8(ptx::pack_f16(p[0], p[1]));
-                pb[nt][1] = transpose8(ptx::pack_f16(p[2], p[3]));
+                for (int e = 0; e < 4; ++e) s[nt][e] = ptx::ex2(s[nt][e]);
+                pb[nt][0] = transpose8(ptx::pack_f16(s[nt][0], s[nt][1]));
+                pb[nt][1] = transpose8(ptx::pack_f16(s[nt][2], s[nt][3]));
+                add2(l[nt][0], l[nt][1], s[nt][0], s[nt][1]);
+                add2(l[nt][0], l[nt][1], s[nt][2], s[nt][3]);
             }
 
             // ---- O^T += V^T (P s)^T: the lane's keys are cq + 4 e ----
             {
-                union VWords {
-                    VChunk v;
-                    uint32_t w[(NG + 1) / 2];
-                } v[4];
-                uint32_t vs[4], vs2[2];
+                uint32_t v[4][(NG + 1) / 2], vs[4], vs2[2];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    v[e].w[0] = 0;
-                    v[e].v = *reinterpret_cast<const VChunk*>(st + at_v + 4 * e * St::kRow);
-                    vs[e] = *reinterpret_cast<const Scales*>(st + at_vs + 4 * e * NG);
+                    if constexpr (NG == 1)
+                        v[e][0] = load_shared_small<2>(st + at_v + 4 * e * St::kRow);
+                    else
+                        load_shared(v[e], st + at_v + 4 * e * St::kRow);
+                    vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
                 }
                 if (!whole) {  // whatever stands behind the sequence counts as zero
 #pragma unroll
@@ -571,17 +592,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
                     const uint32_t f0 = e4m3x2(vs2[0] >> (16 * (n % 2))), f1 = e4m3x2(vs2[1] >> (16 * (n % 2)));
                     // the unit of group n of both keys of a pair: its low byte and its high byte
                     const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
-                    const uint32_t u0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], lo);
-                    const uint32_t u1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], lo);
-                    const uint32_t h0 = __byte_perm(v[0].w[n / 2], v[1].w[n / 2], hi);
-                    const uint32_t h1 = __byte_perm(v[2].w[n / 2], v[3].w[n / 2], hi);
-                    const uint32_t a0 = low_nibble(u0, ex), a1 = high_nibble(u0, ex), a2 = low_nibble(u1, ex), a3 = high_nibble(u1, ex);
-                    const uint32_t c0 = low_nibble(h0, ex), c1 = high_nibble(h0, ex), c2 = low_nibble(h1, ex), c3 = high_nibble(h1, ex);
+                    const uint32_t u0 = __byte_perm(v[0][n / 2], v[1][n / 2], lo), u1 = __byte_perm(v[2][n / 2], v[3][n / 2], lo);
+                    const uint32_t h0 = __byte_perm(v[0][n / 2], v[1][n / 2], hi), h1 = __byte_perm(v[2][n / 2], v[3][n / 2], hi);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const uint32_t p0 = hmul2(pb[nt][0], f0), p1 = hmul2(pb[nt][1], f1);
-                        mma_16816(acc[nt][2 * n], a0, a1, a2, a3, p0, p1, acc[nt][2 * n]);
-                        mma_16816(acc[nt][2 * n + 1], c0, c1, c2, c3, p0, p1, acc[nt][2 * n + 1]);
+                        float (&lo_acc)[4] = acc[nt][2 * n], (&hi_acc)[4] = acc[nt][2 * n + 1];
+                        mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
+                        mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
+                        float x[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, x);
+                        add2(psum[nt][n][0], psum[nt][n][1], x[0], x[1]);
                     }
                 }
             }
@@ -589,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
 
         // ---- join the warps ----
         copy_wait<0>();
-        __syncthreads();  // every warp is done with the rings (and with the sums of the last part)
+        __syncthreads();  // every warp is done with the rings
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -601,52 +622,63 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
                     sm_m[warp][r] = m[nt][t];
                     sm_l[warp][r] = l[nt][t];
                 }
-                // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even) or gq + 8
+                // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even: low nibbles) or gq + 8
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
+                for (int n = 0; n < NG; ++n) {
+                    const float off = -8.f * psum[nt][n][t];
                     *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) =
-                        make_float4(acc[nt][2 * n][t], acc[nt][2 * n][2 + t], acc[nt][2 * n + 1][t],
-                                    acc[nt][2 * n + 1][2 + t]);
-            }
-        }
-        __syncthreads();
-        const bool done = t0 == 0 && t1 == tl.n;
-        const size_t part_row = ((size_t)blockIdx.x * 2 + (t0 == 0)) * ROWS;
-        if (t0 == 0 && !done && threadIdx.x == 0) {
-            // the block that holds the segment's last tile: the last one that starts at or before it
-            const long long e = u + tl.n;
-            a.cut[blockIdx.x] = make_int4(b, hz, (int)((e * blocks + total - 1) / total - 1), 0);
-        }
-        for (int x = threadIdx.x; x < ROWS * D; x += kThreads) {
-            const int r = x / D, d = x % D;
-            if (r0 + r >= R) break;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
-            float lt = 0.f, y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sm_m[w][r] == -INFINITY ? 0.f : ptx::ex2(sm_m[w][r] - mx);
-                lt = fmaf(f, sm_l[w][r], lt);
-                y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
-            }
-            if (done) {
-                const int h = g * a.G + (r0 + r) / a.M, i = (r0 + r) % a.M;
-                put<T>(a.o, (((size_t)b * a.Hq + h) * a.M + i) * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
-            } else {
-                a.ws_acc[(part_row + r) * D + d] = y;
-                if (d == 0) {
-                    a.ws_m[part_row + r] = mx;
-                    a.ws_l[part_row + r] = lt;
+                        make_float4(fmaf(acc[nt][2 * n][t], 1.f / kLowUnit, off),
+                                    fmaf(acc[nt][2 * n][2 + t], 1.f / kHighUnit, off),
+                                    fmaf(acc[nt][2 * n + 1][t], 1.f / kLowUnit, off),
+                                    fmaf(acc[nt][2 * n + 1][2 + t], 1.f / kHighUnit, off));
                 }
             }
         }
-        __syncthreads();  // the sums are read: the rings may be filled again
-        u += t1 - t0;
-        rem += t1 - t0;
-        if (rem == (long long)tl.n * H) {
-            ++b;
-            rem = 0;
+        __syncthreads();
+        {
+            const int pb = part.b, ph = part.hz / a.Z, pr0 = (part.hz % a.Z) * ROWS;
+            const bool begun = part.t0 == 0, done = begun && part.t1 == part.tl.n;
+            const size_t part_row = ((size_t)blockIdx.x * 2 + begun) * ROWS;
+            for (int x = threadIdx.x; x < ROWS * D; x += kThreads) {
+                const int r = x / D, d = x % D;
+                if (pr0 + r >= R) break;
+                float mx = -FLT_MAX;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
+                float lt = 0.f, y = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = ptx::ex2(sm_m[w][r] - mx);  // a warp that saw no key has sums of zero
+                    lt = fmaf(f, sm_l[w][r], lt);
+                    y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
+                }
+                if (done) {
+                    const int h = ph * a.G + (pr0 + r) / a.M, i = (pr0 + r) % a.M;
+                    put<T>(a.o, (((size_t)pb * a.Hq + h) * a.M + i) * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
+                } else {
+                    a.ws_acc[(part_row + r) * D + d] = y;
+                    if (d == 0) {
+                        a.ws_m[part_row + r] = mx;
+                        a.ws_l[part_row + r] = lt;
+                    }
+                }
+            }
+            __syncthreads();  // the part is read
+            if (threadIdx.x == 0) {
+                if (begun && !done) {
+                    // the block that holds the segment's last tile: the last one that starts at or before it
+                    const long long e = part.u + part.tl.n;
+                    a.cut[blockIdx.x] =
+                        make_int4(pb, part.hz, (int)((e * part.blocks + part.total - 1) / part.total - 1), 0);
+                }
+                part.u += part.t1 - part.t0;
+                part.rem += part.t1 - part.t0;
+                if (part.rem == (long long)part.tl.n * H) {
+                    ++part.b;
+                    part.rem = 0;
+                }
+                if (part.u < part.end) set_part(part, a);
+            }
         }
     }
 }
@@ -664,7 +696,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const DecodeArgs a) 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = cut.z - (int)blockIdx.x + 1;
     const auto row_of = [&](int x) { return ((size_t)(blockIdx.x + x) * 2 + (x == 0)) * ROWS + r; };
-    float mx = -INFINITY;
+    float mx = -FLT_MAX;
     for (int x = lane; x < parts; x += 32) mx = fmaxf(mx, a.ws_m[row_of(x)]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -673,8 +705,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const DecodeArgs a) 
 #pragma unroll 4
     for (int x = warp; x < parts; x += kWarps) {
         const size_t row = row_of(x);
-        const float mp = a.ws_m[row];
-        const float f = mp == -INFINITY ? 0.f : ptx::ex2(mp - mx);
+        const float f = ptx::ex2(a.ws_m[row] - mx);
         l = fmaf(f, a.ws_l[row], l);
         if (lane < D / 4) {
             const float4 v = reinterpret_cast<const float4*>(a.ws_acc + row * D)[lane];
@@ -832,7 +863,7 @@ int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void
     float* wm = reinterpret_cast<float*>(cut + blocks);
     const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G,
                        (p.G * p.M + rows - 1) / rows, c.max_pages, c.max_len, p.causal, p.window, c.sinks,
-                       p.scale_log2, c.v_descale, Exponents{}};
+                       p.scale_log2, c.v_descale};
     const cudaError_t e = p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, rows, blocks, s)
                                                : launch_d<__half>(a, p.D, rows, blocks, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -82,21 +82,27 @@ def visible(L, M, i, causal, window, sinks):
     return see
 
 
-def attention(q, k, v, causal, window, sinks, scale, out_dtype, vd=0.125):
-    """Rows q [Hq, M, D] over k, v [Hkv, L, D], 64-bit numpy: (o, bound). The bound per element counts
+def attention(q, k, v, causal, window, sinks, scale, out_dtype, ku=None, vu=None, vd=0.125):
+    """Rows q [Hq, M, D] over k, v [Hkv, L, D], 64-bit numpy: (o, bound). ku, vu: what one code stands for, per
+    element (k and v themselves are codes less 8 times that). Products are taken of the codes 0..15 and of 8 times
+    the unit, whose difference is the value: sums of them are up to 23 units large, whatever the values are. The
+    bound per element counts
       the output's rounding                            eps/2 |o|
       two roundings to FP16, of the probability p (times 2^6, at most 2^6) and of its product with the
       value's scale                                    2 * 2^-11 A,        A = sum w |v|
       such products below FP16's normal range: each is off by at most 2^-25, times a code of at most 8 and
       the factor vd, over a sum of p that is at least 2^6; the same again for p itself
                                                        L 2 * 2^-25 8 vd / 2^6 max(1, s)
-      FP32 sums over the keys, 16 a matrix instruction (L/16 + 64) 2^-23 A
+      FP32 sums over the keys, 16 a matrix instruction (L/16 + 64) 2^-23 23 sum w vu
       the logits: the query's small elements (2^-25 of the row's largest), FP32 sums over D (truncating
-      adders counted: 2^-23 a term) and the exponent's argument, whose error counts twice (weight and sum)."""
+      adders counted: 2^-23 a term) of up to 23 ku |q| each, and the exponent's argument; a logit's error
+      counts twice (weight and sum)."""
     Hq, M, D = q.shape
     Hkv, L, _ = k.shape
     G = Hq // Hkv
     scale = scale or 1.0 / math.sqrt(D)
+    ku = np.abs(k) if ku is None else ku
+    vu = np.abs(v) if vu is None else vu
     o, bound = np.zeros(q.shape), np.zeros(q.shape)
     half = torch.finfo(out_dtype).eps / 2
     for i in range(M):
@@ -109,21 +115,26 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype, vd=0.125):
             w = np.exp(s - s.max())
             w /= w.sum()
             o[h, i] = w @ vv
-            A = w @ np.abs(vv)
-            size = np.abs(kk) @ np.abs(qq) * abs(scale)
+            A, U = w @ np.abs(vv), 23 * (w @ vu[h // G][see])
+            size = 23 * (ku[h // G][see] @ np.abs(qq)) * abs(scale)
             logit = (D + 8) * 2.0 ** -23 * size + 2.0 ** -25 * np.abs(qq).max() * abs(scale) * np.abs(kk).sum(1)
             logit = (logit + 4 * 2.0 ** -24 * (np.abs(s) + abs(s.max()))).max()
             n = len(s)
             small = n * 2.0 ** -27 * max(vd, np.abs(vv).max())  # 8 vd s is at most the largest value and more
-            bound[h, i] = (half * np.abs(o[h, i]) + A * (2.0 ** -10 + (n / 16 + 64) * 2.0 ** -23 + 2 * logit)
+            bound[h, i] = (half * np.abs(o[h, i]) + A * (2.0 ** -10 + 2 * logit) + U * (n / 16 + 64) * 2.0 ** -23
                            + small + 1e-30)
             if out_dtype == torch.float16:
                 bound[h, i] += 2.0 ** -25  # its smallest numbers
     return o, bound
 
 
-def sequences(table, lens, packed, scales, which, descale, page_size, cap=None):
-    """Per sequence [Hkv, L, D] values, through the table; a page outside the pool is zeros."""
+def units(scale_bytes, descale):
+    """What one code stands for, per element."""
+    return np.repeat(e4m3_value(scale_bytes), GROUP, -1) * descale
+
+
+def sequences(table, lens, packed, scales, which, descale, page_size, cap=None, unit=False):
+    """Per sequence [Hkv, L, D] values (or units), through the table; a page outside the pool is zeros."""
     out = []
     pages, Hkv, _, half = packed.shape
     for b, L in enumerate(lens):
@@ -133,7 +144,10 @@ def sequences(table, lens, packed, scales, which, descale, page_size, cap=None):
         for j0 in range(0, L, page_size):
             page, n = int(table[b, j0 // page_size]), min(page_size, L - j0)
             if 0 <= page < pages:
-                x[:, j0:j0 + n] = values(packed[page, :, :n], scales[page, :, :n], which, descale)
+                if unit:
+                    x[:, j0:j0 + n] = units(scales[page, :, :n], descale)
+                else:
+                    x[:, j0:j0 + n] = values(packed[page, :, :n], scales[page, :, :n], which, descale)
         out.append(x)
     return out
 

@@ -65,9 +65,11 @@ def check_decode(o, q, host, table, lens, cap, causal=True, window=0, sinks=0, s
     ps = host[0].shape[2]
     ks = ref.sequences(table, lens, host[0], host[1], "k", kd, ps, cap)
     vs = ref.sequences(table, lens, host[2], host[3], "v", vd, ps, cap)
+    ku = ref.sequences(table, lens, host[0], host[1], "k", kd, ps, cap, unit=True)
+    vu = ref.sequences(table, lens, host[2], host[3], "v", vd, ps, cap, unit=True)
     got, qq = ref.f64(o), ref.f64(q)
     for b in range(len(lens)):
-        want, bound = ref.attention(qq[b], ks[b], vs[b], causal, window, sinks, scale, q.dtype)
+        want, bound = ref.attention(qq[b], ks[b], vs[b], causal, window, sinks, scale, q.dtype, ku[b], vu[b], vd)
         err = np.abs(got[b] - want)
         worst = (err / np.maximum(bound, 1e-300)).max() if err.size else 0
         assert np.isfinite(got[b]).all() and (err <= bound).all(), f"sequence {b}: {worst:.3g} of the bound"
@@ -313,7 +315,9 @@ def test_decode_query_magnitudes():
         o = run_decode(qs, dev, table, lens, 200, True, 0, 0, scale)
         ks = ref.sequences(table, lens, host[0], host[1], "k", 1.0, 16)
         vs = ref.sequences(table, lens, host[2], host[3], "v", 0.125, 16)
-        want, bound = ref.attention(ref.f64(q)[0, h:h + 1], ks[0], vs[0], True, 0, 0, scale, BF16)
+        ku = ref.sequences(table, lens, host[0], host[1], "k", 1.0, 16, unit=True)
+        vu = ref.sequences(table, lens, host[2], host[3], "v", 0.125, 16, unit=True)
+        want, bound = ref.attention(ref.f64(q)[0, h:h + 1], ks[0], vs[0], True, 0, 0, scale, BF16, ku[0], vu[0])
         assert (np.abs(ref.f64(o)[0, h:h + 1] - want) <= bound).all(), h
 
 
@@ -408,9 +412,10 @@ def test_pools_past_32_bits():
     sa.attn_kv4_gather(*dev, i32(table), i32([L]), k, v, 1.0, 0.125)
     q = torch.from_numpy(rng.normal(size=(1, 4, 1, D))).to(BF16).to(DEV)
     o = run_decode(q, dev, table, [L], L)
-    val = [ref.quantize(ref.f64(x[w]).transpose(1, 0, 2), d)[2] for w, d in (("k", 1.0), ("v", 0.125))]
+    quant = [ref.quantize(ref.f64(x[w]).transpose(1, 0, 2), d) for w, d in (("k", 1.0), ("v", 0.125))]
+    val, unit = [z[2] for z in quant], [ref.units(z[1], d) for z, d in zip(quant, (1.0, 0.125))]
     assert np.array_equal(ref.f64(k[0]), val[0]) and np.array_equal(ref.f64(v[0]), val[1])
-    want, bound = ref.attention(ref.f64(q)[0], val[0], val[1], True, 0, 0, 0.0, BF16)
+    want, bound = ref.attention(ref.f64(q)[0], val[0], val[1], True, 0, 0, 0.0, BF16, *unit)
     assert (np.abs(ref.f64(o)[0] - want) <= bound).all()
 
 
@@ -430,7 +435,7 @@ def test_serving_loop(D, ps, dtype):
     d_free, taken = i32(free), 0
     table = i32(np.full((B, width), -1))
     lens = i32([0] * B)
-    told = [[np.zeros((0, Hkv, D)), np.zeros((0, Hkv, D))] for _ in range(B)]
+    told = [[np.zeros((0, Hkv, D)) for _ in range(4)] for _ in range(B)]  # keys, values and their units
     for step, (news, pad) in enumerate((([70, 1, 33], 0), ([1, 1, 1], 2), ([1, 0, 1], 1), ([2, 2, 2], 0), ([1, 1, 1], 5))):
         T = sum(news) + pad
         k = torch.from_numpy(model_rows(rng, (T, Hkv, D), "k")).to(dtype).to(DEV)
@@ -444,7 +449,9 @@ def test_serving_loop(D, ps, dtype):
         lens, at = seq, 0
         for b, n in enumerate(news):
             for which, x, d in ((0, k, kd), (1, v, vd)):
-                told[b][which] = np.concatenate([told[b][which], ref.quantize(ref.f64(x[at:at + n]), d)[2]])
+                z = ref.quantize(ref.f64(x[at:at + n]), d)
+                told[b][which] = np.concatenate([told[b][which], z[2]])
+                told[b][2 + which] = np.concatenate([told[b][2 + which], ref.units(z[1], d)])
             at += n
         M = 2 if step == 3 else 1
         q = torch.from_numpy(rng.normal(size=(B, Hq, M, D))).to(dtype).to(DEV)
@@ -452,8 +459,8 @@ def test_serving_loop(D, ps, dtype):
         sa.attn_decode_paged_kv4(q, *dev, table, lens, o, width * ps, True, 50, 4, 0.0, kd, vd)
         torch.cuda.synchronize()
         for b in range(B):
-            kk, vv = (x.transpose(1, 0, 2) for x in told[b])
-            want, bound = ref.attention(ref.f64(q)[b], kk, vv, True, 50, 4, 0.0, dtype)
+            kk, vv, ku, vu = (x.transpose(1, 0, 2) for x in told[b])
+            want, bound = ref.attention(ref.f64(q)[b], kk, vv, True, 50, 4, 0.0, dtype, ku, vu)
             assert (np.abs(ref.f64(o)[b] - want) <= bound).all(), (step, b)
         if step == 0:  # the prompt of request 0: its chunk of 33 rows over the cached context
             N, M = 70, 33
@@ -461,7 +468,7 @@ def test_serving_loop(D, ps, dtype):
             sa.attn_kv4_gather(*dev, table[:1], lens[:1], ck, cv, kd, vd)
             qc = torch.from_numpy(rng.normal(size=(1, Hq, M, D))).to(dtype).to(DEV)
             oc = sa.attention(qc, ck, cv, causal=True)
-            kk, vv = (x.transpose(1, 0, 2) for x in told[0])
+            kk, vv = (x.transpose(1, 0, 2) for x in told[0][:2])
             want, _ = ref.attention(ref.f64(qc)[0], kk, vv, True, 0, 0, 0.0, dtype)
             assert np.abs(ref.f64(oc)[0] - want).max() <= (1e-2 if dtype == FP16 else 2e-2)
 
