@@ -25,9 +25,10 @@
 // 4..7 are n 2^-20, exactly, and the matrix instructions take FP16's small numbers
 // at full value. One AND per two elements is all the expansion there is; the factor
 // 16 between the two kinds goes into Q (keys) or into the outputs (values), and the
-// 8 of n - 8 is subtracted from sums: 8 times a group's sum of Q is where the key
-// product's accumulator starts, and the sums of P, which a product with a matrix of
-// ones gives in the accumulators' own layout, are taken off at the end. (Exact
+// 8 of n - 8 is subtracted from sums: 8 times the groups' sums of Q, times the keys'
+// scales, is where the logits start (one product more), and the sums of P, which a
+// product with a matrix of ones gives in the accumulators' own layout, are taken off
+// at the end. (Exact
 // n - 8 in halves took one more addition per pair: 430 -> 350 instructions per 16
 // keys.) The scales are applied where there are fewer numbers than elements: a
 // key's to the sum of a group's 32 products, a value's to the probabilities, once
@@ -56,6 +57,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;  // keys of a tile, 16 per warp
 constexpr int kStages = 5;          // tiles in a warp's ring
+constexpr int kBlocks8 = 4, kBlocks16 = 3;  // blocks per SM, of 8 and of 16 rows
 constexpr int kMinTiles = 2;        // a block's range is at least this long while there are blocks to spare
 constexpr float kPShift = 6.0f;     // probabilities are kept times 2^6
 
@@ -107,7 +109,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // transposes an 8 x 8 matrix of halves held by the warp (two per lane)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -115,11 +117,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// two E4M3 bytes -> two halves
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
-    uint32_t d;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(two));
-    return d;
+// four E4M3 bytes -> four halves
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 // pairs of floats in one instruction
 __device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
@@ -128,7 +130,6 @@ __device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
     ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(x, y), ptx::f2_pack(a, b)), x, y);
 }
-__device__ __forceinline__ void sub2(float& x, float& y, float a, float b) { add2(x, y, -a, -b); }
 __device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 // Bits 0..3 and 4..7 of both halves: n 2^-24 and n 2^-20 as FP16.
@@ -213,6 +214,11 @@ __device__ __forceinline__ void set_part(Part& p, const DecodeArgs& a) {
     p.t1 = (int)min((long long)p.tl.n, p.t0 + (p.end - p.u));
 }
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
 // One stage of a warp's ring: the codes and scales of 16 keys and values. Row `slot` of the S^T product's left
 // operand is key (slot / 2) % 4 + 4 (slot % 2) + 8 (slot / 8), so that the four keys that a lane needs of the
 // values (slots 2 cq, 2 cq + 1, 2 cq + 8, 2 cq + 9) are cq + 4 e. Key rows lie in the order of the slots and value
@@ -289,7 +295,7 @@ __device__ __forceinline__ long long block_sum(long long x, long long* part, lon
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_decode_kernel(const DecodeArgs a) {
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
     constexpr int ROWS = 8 * NT;
@@ -298,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
     float* sm_acc = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D]
     __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
     __shared__ int2 sm_vis[ROWS];  // the visible range of every row
+    __shared__ uint4 sm_q[NT][NG][32];
     __shared__ long long sums[kWarps];
     __shared__ Part part;
 
@@ -387,10 +394,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
 #pragma unroll
         for (int x = 0; x < kStages - 1; ++x) issue(t0 + x);
 
-        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that)
-        // and minus 8 times their sums by group
-        uint32_t qf[NT][NG][2][2];
-        float start[NT][NG][2];
+        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that). Every
+        // warp writes the same ones: a warp reads what it wrote itself, without waiting for the others.
+        // start: minus 8 times the rows' sums by group, each as the sum of four halves, as the right operand of a
+        // product with the keys' scales (column k of that product's left operand is the scale of group k % 4).
+        uint32_t start[NT][2];
         float sc[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -418,27 +426,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
             e = top == 0.f ? 127 : min(max(e, 1), 253);
             const float down = __uint_as_float((uint32_t)(254 - e) << 23);
             const float up = __uint_as_float((uint32_t)e << 23) * a.scale_log2 * (0x1p-14f / kLowUnit);
+            float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                float sum = 0.f;
+                uint32_t w[2][2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const float unit = t == 0 ? 0x1p14f : 0x1p14f * (kLowUnit / kHighUnit);
-                        qf[nt][n][s][t] = ptx::pack_f16(x[n][2 * s + t] * down * unit, x[n][4 + 2 * s + t] * down * unit);
-                        const float2 y = halves(qf[nt][n][s][t]);
-                        sum += (y.x + y.y) * (t == 0 ? kLowUnit : kHighUnit);
+                        w[s][t] = ptx::pack_f16(x[n][2 * s + t] * down * unit, x[n][4 + 2 * s + t] * down * unit);
+                        const float2 y = halves(w[s][t]);
+                        sums[n] += (y.x + y.y) * (t == 0 ? kLowUnit : kHighUnit);
                     }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sm_q[nt][n][lane] = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
+                sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], 1);
+                sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], 2);
+            }
+            // rows k of the right operand in this lane: 2 cq, 2 cq + 1 (term cq / 2 of two groups), and 8 further (term 2 more)
+            float two[2] = {-8.f * (cq & 1 ? sums[2] : sums[0]), -8.f * (cq & 1 ? sums[3] : sums[1])};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) start[nt][n][t] = -8.f * __shfl_sync(0xffffffffu, sum, (2 * cq + t) * 4);
+            for (int term = 0; term < 4; ++term) {
+                const uint32_t w = ptx::pack_f16(two[0], two[1]);
+                const float2 y = halves(w);
+                two[0] -= y.x;
+                two[1] -= y.y;
+                if ((term & 1) == (cq >> 1)) start[nt][term >> 1] = w;
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                sc[nt][t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
-            }
+            for (int t = 0; t < 2; ++t) sc[nt][t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
         }
         if (lane < ROWS) {  // every warp writes the same
             const int p = r0 + lane < R ? (r0 + lane) % a.M + L - a.M : L - 1;
@@ -469,68 +485,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
             for (int n = 0; n < NG; ++n) psum[nt][n][0] = psum[nt][n][1] = 0.f;
         }
 
-        int j0 = key_of(t0);
-        const int after_sink = tl.sink - 1;
-        const int jump = (tl.win - tl.sink + 1) * kTile;  // from the last tile of the sinks to the window's first
-        for (int t = t0; t < t1; ++t, j0 += t - 1 == after_sink ? jump : kTile) {
-            copy_wait<kStages - 2>();
-            __syncwarp();
-            issue(t + kStages - 1);  // into the place that was read in the last step
-            const uint32_t st = ring + read;
-            read = read == (kStages - 1) * St::kBytes ? 0 : read + St::kBytes;
-            if (j0 >= L) continue;
-
+        // One step: the 16 keys at j0, from the stage at st. `edge`: some row does not see some of them.
+        const auto step = [&](uint32_t st, int j0, auto edge_tag) {
+            constexpr bool edge = decltype(edge_tag)::value;
             // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
             float s[NT][4];
             {
-                uint32_t k0[NG], k1[NG];
+                uint32_t k0[NG], k1[NG], e0[2], e1[2];
                 load_shared(k0, st + at_k);
                 load_shared(k1, st + at_k + 8 * St::kRow);
-                const uint32_t s0 = load_shared_small<NG>(st + at_ks), s1 = load_shared_small<NG>(st + at_ks + 8 * NG);
-                float2 f0[(NG + 1) / 2], f1[(NG + 1) / 2];
+                e4m3x4(load_shared_small<NG>(st + at_ks), e0[0], e0[1]);
+                e4m3x4(load_shared_small<NG>(st + at_ks + 8 * NG), e1[0], e1[1]);
+                const float2 f0[2] = {halves(e0[0]), halves(e0[1])}, f1[2] = {halves(e1[0]), halves(e1[1])};
+                const uint32_t g0 = cq & 1 ? e0[1] : e0[0], g1 = cq & 1 ? e1[1] : e1[0];
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int n = 0; n < NG; n += 2) {
-                    f0[n / 2] = halves(e4m3x2(s0 >> (8 * n)));
-                    f1[n / 2] = halves(e4m3x2(s1 >> (8 * n)));
-                }
+                for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], g0, g1, g0, g1, start[nt][0], start[nt][1], zero);
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
                     const uint32_t h0 = k0[n] >> 8, h1 = k1[n] >> 8;
                     const float y0 = n & 1 ? f0[n / 2].y : f0[n / 2].x, y1 = n & 1 ? f1[n / 2].y : f1[n / 2].x;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float x[4] = {start[nt][n][0], start[nt][n][1], start[nt][n][0], start[nt][n][1]};
-                        mma_16816(x, k0[n] & kLow, k1[n] & kLow, k0[n] & kHigh, k1[n] & kHigh, qf[nt][n][0][0],
-                                  qf[nt][n][0][1], x);
-                        mma_16816(x, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qf[nt][n][1][0], qf[nt][n][1][1], x);
+                        const uint4 qf = sm_q[nt][n][lane];
+                        float x[4];
+                        mma_16816(x, k0[n] & kLow, k1[n] & kLow, k0[n] & kHigh, k1[n] & kHigh, qf.x, qf.y, zero);
+                        mma_16816(x, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qf.z, qf.w, x);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(x[e], e < 2 ? y0 : y1, n == 0 ? 0.f : s[nt][e]);
+                        for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(x[e], e < 2 ? y0 : y1, s[nt][e]);
                     }
                 }
             }
 
             // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
-            const bool whole = j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks);
             bool rises = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 mul2(s[nt][0], s[nt][1], sc[nt][0], sc[nt][1]);
                 mul2(s[nt][2], s[nt][3], sc[nt][0], sc[nt][1]);
-            }
-            if (!whole) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 4; ++e) {
+                    if (edge) {
                         const int j = j0 + key_slot + 8 * (e >> 1);
                         const int2 vis = sm_vis[nt * 8 + 2 * cq + (e & 1)];
                         if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[nt][e] = -INFINITY;  // a masked key scores -inf
                     }
+                    rises |= s[nt][e] > m[nt][e & 1];
+                }
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) rises |= s[nt][e] > m[nt][e & 1];
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -554,8 +556,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
             uint32_t pb[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float mu0 = kPShift, mu1 = kPShift;
-                sub2(mu0, mu1, m[nt][0], m[nt][1]);
+                const float mu0 = kPShift - m[nt][0], mu1 = kPShift - m[nt][1];
                 add2(s[nt][0], s[nt][1], mu0, mu1);
                 add2(s[nt][2], s[nt][3], mu0, mu1);
 #pragma unroll
@@ -567,45 +568,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) kv4_decode_kernel(c
             }
 
             // ---- O^T += V^T (P s)^T: the lane's keys are cq + 4 e ----
-            {
-                uint32_t v[4][(NG + 1) / 2], vs[4], vs2[2];
+            uint32_t v[4][(NG + 1) / 2], vs[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (NG == 1)
-                        v[e][0] = load_shared_small<2>(st + at_v + 4 * e * St::kRow);
-                    else
-                        load_shared(v[e], st + at_v + 4 * e * St::kRow);
-                    vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
-                }
-                if (!whole) {  // whatever stands behind the sequence counts as zero
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (NG == 1)
+                    v[e][0] = load_shared_small<2>(st + at_v + 4 * e * St::kRow);
+                else
+                    load_shared(v[e], st + at_v + 4 * e * St::kRow);
+                vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
+                // whatever stands behind the sequence counts as zero
+                if (edge && j0 + cq + 4 * e >= L) vs[e] = 0;
+            }
+            // the scales as halves, those of a pair of keys side by side
+            uint32_t f0[4], f1[4];
+            e4m3x4(__byte_perm(vs[0], vs[1], 0x5140u), f0[0], f0[1]);
+            e4m3x4(__byte_perm(vs[2], vs[3], 0x5140u), f1[0], f1[1]);
+            e4m3x4(__byte_perm(vs[0], vs[1], 0x7362u), f0[2], f0[3]);
+            e4m3x4(__byte_perm(vs[2], vs[3], 0x7362u), f1[2], f1[3]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j0 + cq + 4 * e >= L) vs[e] = 0;
-                }
+            for (int n = 0; n < NG; ++n) {
+                // the unit of group n of both keys of a pair: its low byte and its high byte
+                const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
+                const uint32_t u0 = __byte_perm(v[0][n / 2], v[1][n / 2], lo), u1 = __byte_perm(v[2][n / 2], v[3][n / 2], lo);
+                const uint32_t h0 = __byte_perm(v[0][n / 2], v[1][n / 2], hi), h1 = __byte_perm(v[2][n / 2], v[3][n / 2], hi);
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    if (n % 2 == 0) {  // scales of two groups, those of a pair of keys side by side
-                        const uint32_t pick = n == 0 ? 0x5140u : 0x7362u;
-                        vs2[0] = __byte_perm(vs[0], vs[1], pick);
-                        vs2[1] = __byte_perm(vs[2], vs[3], pick);
-                    }
-                    const uint32_t f0 = e4m3x2(vs2[0] >> (16 * (n % 2))), f1 = e4m3x2(vs2[1] >> (16 * (n % 2)));
-                    // the unit of group n of both keys of a pair: its low byte and its high byte
-                    const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
-                    const uint32_t u0 = __byte_perm(v[0][n / 2], v[1][n / 2], lo), u1 = __byte_perm(v[2][n / 2], v[3][n / 2], lo);
-                    const uint32_t h0 = __byte_perm(v[0][n / 2], v[1][n / 2], hi), h1 = __byte_perm(v[2][n / 2], v[3][n / 2], hi);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t p0 = hmul2(pb[nt][0], f0), p1 = hmul2(pb[nt][1], f1);
-                        float (&lo_acc)[4] = acc[nt][2 * n], (&hi_acc)[4] = acc[nt][2 * n + 1];
-                        mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
-                        mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
-                        float x[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, x);
-                        add2(psum[nt][n][0], psum[nt][n][1], x[0], x[1]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t p0 = hmul2(pb[nt][0], f0[n]), p1 = hmul2(pb[nt][1], f1[n]);
+                    float (&lo_acc)[4] = acc[nt][2 * n], (&hi_acc)[4] = acc[nt][2 * n + 1];
+                    mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
+                    mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
+                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                    float x[4];
+                    mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, zero);
+                    add2(psum[nt][n][0], psum[nt][n][1], x[0], x[1]);
                 }
             }
+        };
+
+        int j0 = key_of(t0);
+        const int after_sink = tl.sink - 1;
+        const int jump = (tl.win - tl.sink + 1) * kTile;  // from the last tile of the sinks to the window's first
+        for (int t = t0; t < t1; ++t, j0 += t - 1 == after_sink ? jump : kTile) {
+            copy_wait<kStages - 2>();
+            __syncwarp();
+            issue(t + kStages - 1);  // into the place that was read in the last step
+            const uint32_t st = ring + read;
+            read = read == (kStages - 1) * St::kBytes ? 0 : read + St::kBytes;
+            if (j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks))
+                step(st, j0, Flag<false>());
+            else if (j0 < L)
+                step(st, j0, Flag<true>());
         }
 
         // ---- join the warps ----
@@ -735,8 +747,7 @@ struct Kv4Call {
 
 int rows_per_block(const Problem& p) { return (long long)p.G * p.M <= 8 ? 8 : 16; }
 
-// Blocks that are resident at once, from the kernels' registers (at most 128 a thread for 8 rows, 168 for 16) and rings.
-int blocks_per_sm(const Problem& p) { return rows_per_block(p) == 8 ? 4 : 3; }
+int blocks_per_sm(const Problem& p) { return rows_per_block(p) == 8 ? kBlocks8 : kBlocks16; }
 
 // One block for every place on the GPU, fewer while the longest lengths could not give each kMinTiles tiles.
 int plan_blocks(const Kv4Call& c) {
