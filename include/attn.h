@@ -476,8 +476,8 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  * sums are FP32. Pages need not be clean: rows behind a sequence's end may hold
  * anything. A table entry outside [0, num_pages) reads a page of zeros.
  * D is 32, 64 or 128 (else ATTN_ERR_HEADDIM); B * Hkv <= 65535 and at most
- * 16 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
- * to 8 grouped rows read the cache once, more in blocks of 16 rows; for many
+ * 8 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
+ * to 8 grouped rows read the cache once, more in blocks of 8 rows; for many
  * rows (a prefill over a cached context) attn_kv4_gather and attn_fwd are the
  * faster way.
  *   workspace: device memory of attn_decode_paged_kv4_workspace_bytes(...)

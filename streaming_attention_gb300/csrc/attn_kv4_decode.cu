@@ -1,21 +1,20 @@
 // Decode attention over the 4-bit paged KV cache (format: attn_kv4.h).
 //
-// Work. A segment is the visible keys of one (sequence, KV head, block of 8 * NT
-// grouped query rows), in tiles of 64 keys; query head h = g * G + r / M, row
-// i = r % M. The tiles of all segments in a row are cut into equal ranges, one per
-// block of a grid that fills the GPU once, whatever the lengths are: each block
-// counts the tiles from seq_lens itself. A segment that lies inside a block's range
-// is written to o there; of one that is cut, each block leaves its part's
-// (m, l, acc) in the workspace (at most two parts a block: one begun before it, one
-// that goes on behind it), and a second kernel joins them by the common-maximum
-// rule.
+// Work. A segment is the visible keys of one (sequence, KV head, block of 8 grouped
+// query rows), in tiles of 64 keys; query head h = g * G + r / M, row i = r % M. The
+// tiles of all segments in a row are cut into ranges, one per block of a grid that
+// fills the GPU once, whatever the lengths are: each block counts the tiles from
+// seq_lens itself. A segment that lies inside a block's range is written to o
+// there; of one that is cut, each block leaves its part's (m, l, acc) in the
+// workspace (at most two parts a block: one begun before it, one that goes on
+// behind it), and a second kernel joins them by the common-maximum rule. Ranges
+// depend on the lengths and the grid alone, so the order of all sums does too.
 //
 // In a block, four warps take 16 keys each of a tile and keep their own running
 // (m, l, acc) per row, joined through shared memory at the end of a segment's part.
 // Each warp copies its keys' codes and scales into a ring of its own
-// (cp.async, kStages deep, no barrier between warps): the reading of the cache is
-// what bounds the kernel, and 16 warps with 4 stages in flight keep about 140 KB of
-// it outstanding per SM.
+// (cp.async, a pair of tiles ahead, no barrier between warps); the next part's
+// copies begin before the sums of the last one are joined.
 //
 // A warp's products run transposed, on m16n8k16 matrix instructions with the
 // cache as the left operand, so that a row of the cache is expanded once for all
@@ -56,10 +55,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;  // keys of a tile, 16 per warp
-constexpr int kStages = 5;          // tiles in a warp's ring
-constexpr int kBlocks8 = 4, kBlocks16 = 3;  // blocks per SM, of 8 and of 16 rows
-constexpr int kMinTiles = 2;        // a block's range is at least this long while there are blocks to spare
-constexpr float kPShift = 6.0f;     // probabilities are kept times 2^6
+constexpr int kStages = 4;          // tiles in a warp's ring, two pairs
+constexpr int kBlocksPerSm = 3;     // 12 warps of 168 registers
+constexpr int ROWS = 8;             // query rows of a block
+constexpr int kPartCost = 3;        // what a segment costs beside its tiles, in tiles (see Part)
+constexpr int kMinTiles = 4;        // a block's range is at least this long while there are blocks to spare
+// Probabilities are kept times 2^kPShift relative to a score that the largest one may exceed by kPSlack (base 2): times
+// a scale of at most 448 they stay below 2^7 * 448 = 57344.
+constexpr float kPShift = 3.0f, kPSlack = 4.0f;
 
 struct DecodeArgs {
     const void* q;
@@ -67,7 +70,7 @@ struct DecodeArgs {
     const int* table;
     const int* lens;
     void* o;
-    float *ws_m, *ws_l, *ws_acc;  // [blocks][2][rows], the same, [blocks][2][rows][D]
+    float *ws_m, *ws_l, *ws_acc;  // [blocks][2][ROWS], the same, [blocks][2][ROWS][D]
     int4* cut;                    // [blocks]: segment that a block leaves unfinished (b, head * Z + z), last block of it
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
@@ -124,8 +127,8 @@ __device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
         : "r"(w));
 }
 // pairs of floats in one instruction
-__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
-    ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(x, y), ptx::f2_pack(a, b)), x, y);
+__device__ __forceinline__ void fma2(float& x, float& y, const float (&a)[2], const float (&b)[2]) {
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(x, y), ptx::f2_pack(a[0], a[1]), ptx::f2_pack(b[0], b[1])), x, y);
 }
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
     ptx::f2_unpack(ptx::f2_add(ptx::f2_pack(x, y), ptx::f2_pack(a, b)), x, y);
@@ -192,26 +195,73 @@ __device__ __forceinline__ void put<__half>(void* o, size_t i, float x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// x / n and x % n, in 32 bits where they suffice (a division in 64 takes a hundred instructions)
+__device__ __forceinline__ long long divide(long long x, int n, int* rest) {
+    if ((unsigned long long)x >> 32) {
+        *rest = (int)(x % n);
+        return x / n;
+    }
+    const uint32_t q = (uint32_t)x / (uint32_t)n;
+    *rest = (int)((uint32_t)x - q * (uint32_t)n);
+    return q;
+}
+
+// The tiles are shared out equally: `per` to a block, and one more to the first `more` of them.
+struct Shares {
+    long long per;
+    int more;
+    __device__ __forceinline__ long long begin(int i) const { return per * i + min(i, more); }
+    __device__ __forceinline__ int block_of(long long tile) const {
+        const long long first = (per + 1) * more;
+        if (tile < first) return (int)(tile / (per + 1));
+        return more + (int)((tile - first) / per);
+    }
+};
+
 // The part of a segment that a block is at: tiles [t0, t1) of it. Kept in shared memory, so that what the warps need
 // only before and after a part's tiles takes no registers while they run through them.
+// Every segment counts kPartCost more than its tiles when the tiles are shared out, in front of its first one: that is
+// what a block spends on starting its copies, its query and its sums (measured: with shares by tiles alone, 64 ragged
+// sequences' blocks of ten short segments ended at 150 us and the others at 113).
 struct Part {
-    long long u, rem;    // tiles before the part: of all, and of its sequence
-    long long end, total, blocks;  // the block's range ends at tile `end` of `total`; blocks with a range
-    int b, L, hz, t0, t1;
+    long long u, rem;      // before the part: of all, and of its sequence
+    int b, L, hz, t0, t1;  // t0 == t1: no part
+    int len;               // t1 - t0 and what of kPartCost goes with it
     Tiles tl;
 };
-__device__ __forceinline__ void set_part(Part& p, const DecodeArgs& a) {
+// The part at p.u, p.rem of sequence p.b in a range that ends at `end`.
+__device__ __forceinline__ void set_part(Part& p, const DecodeArgs& a, long long end) {
+    p.t0 = p.t1 = 0;
+    if (p.u >= end) return;
     p.L = length_of(a, p.b);
     p.tl = tiles_of(a, p.L);
-    p.hz = (int)(p.rem / p.tl.n);
-    p.t0 = (int)(p.rem % p.tl.n);
-    p.t1 = (int)min((long long)p.tl.n, p.t0 + (p.end - p.u));
+    const int n = p.tl.n + kPartCost;
+    int from;
+    p.hz = (int)divide(p.rem, n, &from);
+    p.len = (int)min((long long)(n - from), end - p.u);
+    p.t0 = max(from - kPartCost, 0);
+    p.t1 = max(from + p.len - kPartCost, 0);
+}
+__device__ __forceinline__ void next_part(Part& p, const Part& q, const DecodeArgs& a, long long end) {
+    p.t0 = p.t1 = 0;
+    if (q.t0 == q.t1) return;
+    p.u = q.u + q.len;
+    p.rem = q.rem + q.len;
+    p.b = q.b;
+    if (p.rem == (long long)(q.tl.n + kPartCost) * a.Hkv * a.Z) {
+        ++p.b;
+        p.rem = 0;
+    }
+    set_part(p, a, end);
 }
 
 template <bool B>
@@ -235,6 +285,9 @@ struct Stage {
 
     static constexpr int Q = kRow / 16;     // chunks of a row's codes
     static constexpr int S = kScales / 16;  // chunks of 16 rows' scales
+    // at 4 bytes a row the scales that a lane needs are brought together: those of keys j and j + 8, and those of
+    // values j, j + 4, j + 8 and j + 12
+    static constexpr bool kSpread = NG == 4;
 
     // Where a lane reads and writes; the pools' rows come in blocks of 16, numbered in 32 bits.
     const uint8_t *k, *v, *s;
@@ -247,10 +300,17 @@ struct Stage {
         to_k = kK + ((r & 8) | ((r & 3) << 1) | ((r >> 2) & 1)) * kRow + q * 16;
         to_v = kV + r * kRow + (D == 128 ? q ^ (r & 2) : q) * 16;
         codes = lane < kCodes / 16;
-        const bool vs = lane >= S;
-        s = (vs ? c.v_scales : c.k_scales) + (vs ? lane - S : lane) * 16;
-        to_s = vs ? kVs + (lane - S) * 16 : kKs + lane * 16;
-        scales = lane < 2 * S;
+        if (kSpread) {  // one key's or value's scales to a lane
+            const int j = lane & 15;
+            s = (lane < 16 ? c.k_scales : c.v_scales) + j * NG;
+            to_s = lane < 16 ? kKs + ((j & 7) * 2 + (j >> 3)) * NG : kVs + ((j & 3) * 4 + (j >> 2)) * NG;
+            scales = true;
+        } else {
+            const bool vs = lane >= S;
+            s = (vs ? c.v_scales : c.k_scales) + (vs ? lane - S : lane) * 16;
+            to_s = vs ? kVs + (lane - S) * 16 : kKs + lane * 16;
+            scales = lane < 2 * S;
+        }
     }
     // The lane's part of the copy of block `at`; -1, a page outside the pool, reads as zeros: scales of zero.
     __device__ __forceinline__ void load(uint32_t dst, int at) const {
@@ -265,7 +325,12 @@ struct Stage {
                     copy16(dst + to_v + 512, vp + 512);
                 }
             }
-            if (scales) copy16(dst + to_s, row_block(s, (uint32_t)at, kScales));
+            if (kSpread)
+                copy4(dst + to_s, row_block(s, (uint32_t)at, kScales));
+            else if (scales)
+                copy16(dst + to_s, row_block(s, (uint32_t)at, kScales));
+        } else if (kSpread) {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + to_s), "r"(0) : "memory");
         } else if (scales) {
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + to_s), "r"(0) : "memory");
         }
@@ -294,19 +359,18 @@ __device__ __forceinline__ long long block_sum(long long x, long long* part, lon
     return s - x + before;
 }
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_decode_kernel(const DecodeArgs a) {
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(const DecodeArgs a) {
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
-    constexpr int ROWS = 8 * NT;
-    extern __shared__ __align__(16) uint8_t smem[];
-    // the rings, and after them in the same place the warps' sums of a part
-    float* sm_acc = reinterpret_cast<float*>(smem);  // [kWarps][ROWS][D]
+    extern __shared__ __align__(16) uint8_t smem[];  // the rings, then the warps' sums of a part
+    float* sm_acc = reinterpret_cast<float*>(smem + kWarps * kStages * St::kBytes);  // [kWarps][ROWS][D]
     __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-    __shared__ int2 sm_vis[ROWS];  // the visible range of every row
-    __shared__ uint4 sm_q[NT][NG][32];
+    __shared__ int2 sm_vis[2][ROWS];  // the visible range of every row, of this part and of the last or next
     __shared__ long long sums[kWarps];
-    __shared__ Part part;
+    __shared__ Part parts[2];
+    __shared__ Shares shares;
+    __shared__ long long end;  // of the block's range
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, cq = lane & 3;  // the lane's place in a matrix fragment
@@ -314,100 +378,126 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
     const uint32_t ring = ptx::smem_u32(smem) + warp * (kStages * St::kBytes);
     const St from(a.c, lane);
     // where the lane reads in a stage; the values' chunks of every other pair of rows are exchanged
-    const int at_k = St::kK + gq * St::kRow + cq * (4 * NG), at_ks = St::kKs + key_slot * NG;
+    const int at_k = St::kK + gq * St::kRow + cq * (4 * NG), at_ks = St::kKs + key_slot * NG * (St::kSpread ? 2 : 1);
     const int at_v = St::kV + cq * St::kRow + (D == 128 ? (gq * 8) ^ ((cq & 2) * 16) : gq * (2 * NG));
-    const int at_vs = St::kVs + cq * NG;
+    const int at_vs = St::kVs + cq * NG * (St::kSpread ? 4 : 1);
     const int H = a.Hkv * a.Z;
     const int R = a.G * a.M;
     const int ps = a.c.page_size;
 
+    // The join kernel may be launched now (it waits for this one's end); and this kernel may itself have been launched
+    // before the end of the one in front of it, so nothing in memory is touched before that has ended.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- this block's range of the tiles ----
     {
-        long long total = 0;
+        const auto cost_of = [&](int b) {
+            return b < a.B ? (long long)(tiles_of(a, length_of(a, b)).n + kPartCost) * H : 0ll;
+        };
+        long long total = 0, cost = 0, before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
             long long all;
-            block_sum(b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0, sums, &all);
+            cost = cost_of(b0 + threadIdx.x);
+            before = block_sum(cost, sums, &all);
             total += all;
         }
-        const long long want = (total + kMinTiles - 1) / kMinTiles;
-        const long long blocks = want < gridDim.x ? want : gridDim.x;
+        // a grid that is larger than the tiles need uses its first blocks only
+        const int blocks =
+            total >= (long long)kMinTiles * gridDim.x ? (int)gridDim.x : (int)((total + kMinTiles - 1) / kMinTiles);
+        Shares sh;
+        sh.per = divide(total, blocks, &sh.more);
         if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
         if (blockIdx.x >= blocks) return;
-        const long long u0 = total * blockIdx.x / blocks;
-        long long before = 0;
+        const long long u0 = sh.begin(blockIdx.x);
+        if (threadIdx.x == 0) shares = sh;
+        long long behind = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            const long long n = b < a.B ? (long long)tiles_of(a, length_of(a, b)).n * H : 0;
-            long long all;
-            const long long s = before + block_sum(n, sums, &all);
-            if (s <= u0 && u0 < s + n) {
-                part.u = u0;
-                part.rem = u0 - s;
-                part.end = total * (blockIdx.x + 1) / blocks;
-                part.total = total;
-                part.blocks = blocks;
-                part.b = b;
-                set_part(part, a);
+            long long all = total;
+            if (a.B > kThreads) {  // one chunk's sums are still at hand
+                cost = cost_of(b0 + threadIdx.x);
+                before = behind + block_sum(cost, sums, &all);
             }
-            before += all;
-            if (u0 < before) break;
+            if (before <= u0 && u0 < before + cost) {
+                parts[0].u = u0;
+                parts[0].rem = u0 - before;
+                parts[0].b = b0 + threadIdx.x;
+                end = sh.begin(blockIdx.x + 1);
+                set_part(parts[0], a, end);
+            }
+            behind += all;
+            if (u0 < behind) break;
         }
     }
+    __syncthreads();
 
-    for (;;) {
-        __syncthreads();  // the part is set; the last one's sums are read
-        if (part.u >= part.end) return;
-        const int b = part.b, L = part.L, t0 = part.t0, t1 = part.t1;
-        const Tiles tl = part.tl;
-        const int g = part.hz / a.Z, r0 = (part.hz % a.Z) * ROWS;
-
-        // the pool's blocks of this warp's keys, for 32 tiles at a time: lane x has that of tile base + x
-        const int* trow = a.table + (size_t)b * a.max_pages;
-        const auto key_of = [&](int t) { return tl.at(t) * kTile + warp * 16; };
-        const auto page_of = [&](int t) {
-            const int j = key_of(t);
-            return t < t1 && j < L ? __ldg(trow + j / ps) : -1;
-        };
-        const auto block_of = [&](int page, int t) {  // -1: a page outside the pool, or nothing to read
-            return page >= 0 && page < a.c.num_pages ? (page * a.Hkv + g) * (ps / 16) + key_of(t) % ps / 16 : -1;
-        };
-        int base = t0;
-        int next_page = page_of(t0 + lane);
-        int blocks_at = block_of(next_page, t0 + lane);
-        next_page = page_of(t0 + 32 + lane);
-        uint32_t fill = 0, read = 0;  // the ring's places, in bytes
-        const auto issue = [&](int t) {
-            if (t < t1) {
-                if (t - base == 32) {
-                    base = t;
-                    blocks_at = block_of(next_page, t + lane);
-                    next_page = page_of(t + 32 + lane);
-                }
-                from.load(ring + fill, __shfl_sync(0xffffffffu, blocks_at, t - base));
-                fill = fill == (kStages - 1) * St::kBytes ? 0 : fill + St::kBytes;
+    // ---- the copies of a part ----
+    // the pool's blocks of this warp's keys, for 32 tiles at a time: lane x has that of tile base + x
+    int base, blocks_at, next_page, copy_end;
+    uint32_t fill = 0;  // the half of the ring that is filled next, in bytes
+    const auto page_of = [&](const Part& p, int t) {
+        const int j = p.tl.at(t) * kTile + warp * 16;
+        return t < p.t1 && j < p.L ? __ldg(a.table + (size_t)p.b * a.max_pages + j / ps) : -1;
+    };
+    const auto block_of = [&](const Part& p, int page, int t) {  // -1: a page outside the pool, or nothing to read
+        const int j = p.tl.at(t) * kTile + warp * 16, g = p.hz / a.Z;
+        return page >= 0 && page < a.c.num_pages ? (page * a.Hkv + g) * (ps / 16) + j % ps / 16 : -1;
+    };
+    const auto issue = [&](const Part& p, int t) {  // the pair of tiles t, t + 1
+        if (t < copy_end) {
+            if (t - base == 32) {
+                base = t;
+                blocks_at = block_of(p, next_page, t + lane);
+                next_page = page_of(p, t + 32 + lane);
             }
-            copy_commit();
-        };
-#pragma unroll
-        for (int x = 0; x < kStages - 1; ++x) issue(t0 + x);
+            from.load(ring + fill, __shfl_sync(0xffffffffu, blocks_at, t - base));
+            if (t + 1 < copy_end) from.load(ring + fill + St::kBytes, __shfl_sync(0xffffffffu, blocks_at, t + 1 - base));
+            fill ^= 2 * St::kBytes;
+        }
+        copy_commit();
+    };
+    // begins the copies of part p, whose first 64 tiles' pages are at hand
+    const auto begin_copies = [&](const Part& p, int page0, int page1) {
+        base = p.t0;
+        copy_end = p.t1;
+        blocks_at = block_of(p, page0, p.t0 + lane);
+        next_page = page1;
+        issue(p, p.t0);
+    };
+    begin_copies(parts[0], page_of(parts[0], parts[0].t0 + lane), page_of(parts[0], parts[0].t0 + 32 + lane));
+    if (threadIdx.x == 0) next_part(parts[1], parts[0], a, end);
+    __syncthreads();
 
-        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that). Every
-        // warp writes the same ones: a warp reads what it wrote itself, without waiting for the others.
+    for (int turn = 0;; turn ^= 1) {
+        const Part& part = parts[turn];
+        if (part.t0 == part.t1) return;
+        const int t1 = part.t1, L = part.L;
+        const Tiles tl = part.tl;
+        // rows of q and o are [b][g][row of the group]: query head g * G + r / M, row r % M
+        const int r0 = (part.hz % a.Z) * ROWS;
+        const size_t first_row = ((size_t)part.b * a.Hq + part.hz / a.Z * a.G) * a.M;
+        // what the next part begins with, asked for now: its pages, and its query rows into L1
+        const Part& ahead = parts[turn ^ 1];
+        const int page0 = page_of(ahead, ahead.t0 + lane), page1 = page_of(ahead, ahead.t0 + 32 + lane);
+        if (ahead.t0 < ahead.t1) {
+            const int r = (ahead.hz % a.Z) * ROWS + gq;
+            const size_t row = ((size_t)ahead.b * a.Hq + ahead.hz / a.Z * a.G) * a.M + r;
+            if (r < R && cq * 128 < 2 * D)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(a.q) + row * (2 * D) +
+                                                           cq * 128));
+        }
+
+        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that), negated
+        // if the logit scale is negative.
         // start: minus 8 times the rows' sums by group, each as the sum of four halves, as the right operand of a
         // product with the keys' scales (column k of that product's left operand is the scale of group k % 4).
-        uint32_t start[NT][2];
-        float sc[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = r0 + nt * 8 + gq;
+        uint32_t qf[NG][2][2], start[2];
+        float sc[2];
+{
+            const int r = r0 + gq;
             float x[NG][8], top = 0.f;
             const bool row = r < R;
-            const int h = g * a.G + (row ? r / a.M : 0), i = row ? r % a.M : 0;
-            const uint32_t* qrow =
-                reinterpret_cast<const uint32_t*>(a.q) + (((size_t)b * a.Hq + h) * a.M + i) * (D / 2) + cq * 4;
+            const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q) + (first_row + (row ? r : 0)) * (D / 2) + cq * 4;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const uint4 w = row ? __ldg(reinterpret_cast<const uint4*>(qrow + n * 16)) : make_uint4(0, 0, 0, 0);
@@ -424,22 +514,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
             // biased exponent of the row's maximum, kept where 2^e and 2^-e are both normal
             int e = (int)(__float_as_uint(top) >> 23);
             e = top == 0.f ? 127 : min(max(e, 1), 253);
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-            const float up = __uint_as_float((uint32_t)e << 23) * a.scale_log2 * (0x1p-14f / kLowUnit);
+            const float down = copysignf(__uint_as_float((uint32_t)(254 - e) << 23), a.scale_log2);
+            const float up =
+                fmaxf(__uint_as_float((uint32_t)e << 23) * fabsf(a.scale_log2) * (0x1p-14f / kLowUnit), FLT_MIN);
             float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                uint32_t w[2][2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const float unit = t == 0 ? 0x1p14f : 0x1p14f * (kLowUnit / kHighUnit);
-                        w[s][t] = ptx::pack_f16(x[n][2 * s + t] * down * unit, x[n][4 + 2 * s + t] * down * unit);
-                        const float2 y = halves(w[s][t]);
+                        qf[n][s][t] =
+                            ptx::pack_f16(x[n][2 * s + t] * down * unit, x[n][4 + 2 * s + t] * down * unit);
+                        const float2 y = halves(qf[n][s][t]);
                         sums[n] += (y.x + y.y) * (t == 0 ? kLowUnit : kHighUnit);
                     }
-                sm_q[nt][n][lane] = make_uint4(w[0][0], w[0][1], w[1][0], w[1][1]);
                 sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], 1);
                 sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], 2);
             }
@@ -451,16 +541,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
                 const float2 y = halves(w);
                 two[0] -= y.x;
                 two[1] -= y.y;
-                if ((term & 1) == (cq >> 1)) start[nt][term >> 1] = w;
+                if ((term & 1) == (cq >> 1)) start[term >> 1] = w;
             }
 #pragma unroll
-            for (int t = 0; t < 2; ++t) sc[nt][t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
+            for (int t = 0; t < 2; ++t) sc[t] = __shfl_sync(0xffffffffu, up, (2 * cq + t) * 4);
         }
         if (lane < ROWS) {  // every warp writes the same
             const int p = r0 + lane < R ? (r0 + lane) % a.M + L - a.M : L - 1;
             int2 v;
             key_range(p, L, a.causal, a.window, &v.x, &v.y);
-            sm_vis[lane] = v;
+            sm_vis[turn][lane] = v;
         }
         __syncwarp();
         // keys [all_lo, all_hi) are visible to every row
@@ -468,117 +558,112 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
         key_range(L - 1, L, a.causal, a.window, &all_lo, &skip);
         key_range(L - a.M, L, a.causal, a.window, &skip, &all_hi);
 
-        float m[NT][2], l[NT][2], acc[NT][2 * NG][4];
-        float psum[NT][NG][2];  // of the probabilities times a group's scales, as rounded for the products
+        // m: the score that stands for the largest one so far, in units of sc: it is set anew only when a score exceeds it
+        // by kPSlack in base 2 (else every few steps some row's would be); limit: that border; mu: kPShift less m in base 2
+        float m[2], limit[2], mu[2], l[2], acc[2 * NG][4];
+        float psum[NG][2];  // of the probabilities times a group's scales, as rounded for the products
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                m[nt][t] = -FLT_MAX;  // finite: a masked key's -inf less it is -inf, never NaN
-                l[nt][t] = 0.f;
-            }
-#pragma unroll
-            for (int n = 0; n < 2 * NG; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][n][e] = 0.f;
-#pragma unroll
-            for (int n = 0; n < NG; ++n) psum[nt][n][0] = psum[nt][n][1] = 0.f;
+        for (int t = 0; t < 2; ++t) {
+            m[t] = limit[t] = -FLT_MAX;  // finite: a masked key's -inf less it is -inf, never NaN
+            mu[t] = kPShift;
+            l[t] = 0.f;
         }
+#pragma unroll
+        for (int n = 0; n < 2 * NG; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) psum[n][0] = psum[n][1] = 0.f;
 
         // One step: the 16 keys at j0, from the stage at st. `edge`: some row does not see some of them.
         const auto step = [&](uint32_t st, int j0, auto edge_tag) {
             constexpr bool edge = decltype(edge_tag)::value;
-            // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
-            float s[NT][4];
-            {
-                uint32_t k0[NG], k1[NG], e0[2], e1[2];
-                load_shared(k0, st + at_k);
-                load_shared(k1, st + at_k + 8 * St::kRow);
-                e4m3x4(load_shared_small<NG>(st + at_ks), e0[0], e0[1]);
-                e4m3x4(load_shared_small<NG>(st + at_ks + 8 * NG), e1[0], e1[1]);
-                const float2 f0[2] = {halves(e0[0]), halves(e0[1])}, f1[2] = {halves(e1[0]), halves(e1[1])};
-                const uint32_t g0 = cq & 1 ? e0[1] : e0[0], g1 = cq & 1 ? e1[1] : e1[0];
-                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], g0, g1, g0, g1, start[nt][0], start[nt][1], zero);
-#pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const uint32_t h0 = k0[n] >> 8, h1 = k1[n] >> 8;
-                    const float y0 = n & 1 ? f0[n / 2].y : f0[n / 2].x, y1 = n & 1 ? f1[n / 2].y : f1[n / 2].x;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 qf = sm_q[nt][n][lane];
-                        float x[4];
-                        mma_16816(x, k0[n] & kLow, k1[n] & kLow, k0[n] & kHigh, k1[n] & kHigh, qf.x, qf.y, zero);
-                        mma_16816(x, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qf.z, qf.w, x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(x[e], e < 2 ? y0 : y1, s[nt][e]);
-                    }
-                }
-            }
-
-            // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
-            bool rises = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mul2(s[nt][0], s[nt][1], sc[nt][0], sc[nt][1]);
-                mul2(s[nt][2], s[nt][3], sc[nt][0], sc[nt][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (edge) {
-                        const int j = j0 + key_slot + 8 * (e >> 1);
-                        const int2 vis = sm_vis[nt * 8 + 2 * cq + (e & 1)];
-                        if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[nt][e] = -INFINITY;  // a masked key scores -inf
-                    }
-                    rises |= s[nt][e] > m[nt][e & 1];
-                }
-            }
-            if (__any_sync(0xffffffffu, rises)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(m[nt][e], fmaxf(s[nt][e], s[nt][2 + e]));
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        const float alpha = ptx::ex2(m[nt][e] - mx);
-                        m[nt][e] = mx;
-                        l[nt][e] *= alpha;
-#pragma unroll
-                        for (int n = 0; n < 2 * NG; ++n) {
-                            acc[nt][n][e] *= alpha;
-                            acc[nt][n][2 + e] *= alpha;
-                        }
-#pragma unroll
-                        for (int n = 0; n < NG; ++n) psum[nt][n][e] *= alpha;
-                    }
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float mu0 = kPShift - m[nt][0], mu1 = kPShift - m[nt][1];
-                add2(s[nt][0], s[nt][1], mu0, mu1);
-                add2(s[nt][2], s[nt][3], mu0, mu1);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = ptx::ex2(s[nt][e]);
-                pb[nt][0] = transpose8(ptx::pack_f16(s[nt][0], s[nt][1]));
-                pb[nt][1] = transpose8(ptx::pack_f16(s[nt][2], s[nt][3]));
-                add2(l[nt][0], l[nt][1], s[nt][0], s[nt][1]);
-                add2(l[nt][0], l[nt][1], s[nt][2], s[nt][3]);
-            }
-
-            // ---- O^T += V^T (P s)^T: the lane's keys are cq + 4 e ----
+            // the values' codes and scales are loaded with the keys', ahead of the branch below: the lane's are cq + 4 e
             uint32_t v[4][(NG + 1) / 2], vs[4];
+            if constexpr (St::kSpread) load_shared(vs, st + at_vs);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (NG == 1)
                     v[e][0] = load_shared_small<2>(st + at_v + 4 * e * St::kRow);
                 else
                     load_shared(v[e], st + at_v + 4 * e * St::kRow);
-                vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
+                if constexpr (!St::kSpread) vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
                 // whatever stands behind the sequence counts as zero
                 if (edge && j0 + cq + 4 * e >= L) vs[e] = 0;
             }
+            // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
+            float s[4];
+            {
+                uint32_t k0[NG], k1[NG], e0[2], e1[2];
+                load_shared(k0, st + at_k);
+                load_shared(k1, st + at_k + 8 * St::kRow);
+                uint32_t ks[2];
+                if constexpr (St::kSpread) {
+                    load_shared(ks, st + at_ks);
+                } else {
+                    ks[0] = load_shared_small<NG>(st + at_ks);
+                    ks[1] = load_shared_small<NG>(st + at_ks + 8 * NG);
+                }
+                e4m3x4(ks[0], e0[0], e0[1]);
+                e4m3x4(ks[1], e1[0], e1[1]);
+                const float2 f0[2] = {halves(e0[0]), halves(e0[1])}, f1[2] = {halves(e1[0]), halves(e1[1])};
+                const uint32_t g0 = cq & 1 ? e0[1] : e0[0], g1 = cq & 1 ? e1[1] : e1[0];
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(s, g0, g1, g0, g1, start[0], start[1], zero);
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const uint32_t h0 = k0[n] >> 8, h1 = k1[n] >> 8;
+                    const float y0 = n & 1 ? f0[n / 2].y : f0[n / 2].x, y1 = n & 1 ? f1[n / 2].y : f1[n / 2].x;
+                    float x[4];
+                    mma_16816(x, k0[n] & kLow, k1[n] & kLow, k0[n] & kHigh, k1[n] & kHigh, qf[n][0][0], qf[n][0][1], zero);
+                    mma_16816(x, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qf[n][1][0], qf[n][1][1], x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = fmaf(x[e], e < 2 ? y0 : y1, s[e]);
+                }
+            }
+
+            // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
+            bool rises = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (edge) {
+                    const int j = j0 + key_slot + 8 * (e >> 1);
+                    const int2 vis = sm_vis[turn][2 * cq + (e & 1)];
+                    if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[e] = -INFINITY;  // a masked key scores -inf
+                }
+                rises |= s[e] > limit[e & 1];
+            }
+            if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(m[e], fmaxf(s[e], s[2 + e]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    const float alpha = ptx::ex2((m[e] - mx) * sc[e]);
+                    m[e] = mx;
+                    if (mx > -FLT_MAX) {
+                        limit[e] = mx + kPSlack / sc[e];
+                        mu[e] = fmaf(-mx, sc[e], kPShift);
+                    }
+                    l[e] *= alpha;
+#pragma unroll
+                    for (int n = 0; n < 2 * NG; ++n) {
+                        acc[n][e] *= alpha;
+                        acc[n][2 + e] *= alpha;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) psum[n][e] *= alpha;
+                }
+            }
+            fma2(s[0], s[1], sc, mu);
+            fma2(s[2], s[3], sc, mu);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = ptx::ex2(s[e]);
+            const uint32_t pb0 = transpose8(ptx::pack_f16(s[0], s[1])), pb1 = transpose8(ptx::pack_f16(s[2], s[3]));
+            add2(l[0], l[1], s[0], s[1]);
+            add2(l[0], l[1], s[2], s[3]);
+
+            // ---- O^T += V^T (P s)^T ----
             // the scales as halves, those of a pair of keys side by side
             uint32_t f0[4], f1[4];
             e4m3x4(__byte_perm(vs[0], vs[1], 0x5140u), f0[0], f0[1]);
@@ -591,69 +676,64 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
                 const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
                 const uint32_t u0 = __byte_perm(v[0][n / 2], v[1][n / 2], lo), u1 = __byte_perm(v[2][n / 2], v[3][n / 2], lo);
                 const uint32_t h0 = __byte_perm(v[0][n / 2], v[1][n / 2], hi), h1 = __byte_perm(v[2][n / 2], v[3][n / 2], hi);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t p0 = hmul2(pb[nt][0], f0[n]), p1 = hmul2(pb[nt][1], f1[n]);
-                    float (&lo_acc)[4] = acc[nt][2 * n], (&hi_acc)[4] = acc[nt][2 * n + 1];
-                    mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
-                    mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
-                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                    float x[4];
-                    mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, zero);
-                    add2(psum[nt][n][0], psum[nt][n][1], x[0], x[1]);
-                }
+                const uint32_t p0 = hmul2(pb0, f0[n]), p1 = hmul2(pb1, f1[n]);
+                float (&lo_acc)[4] = acc[2 * n], (&hi_acc)[4] = acc[2 * n + 1];
+                mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
+                mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                float x[4];
+                mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, zero);
+                add2(psum[n][0], psum[n][1], x[0], x[1]);
             }
         };
 
-        int j0 = key_of(t0);
-        const int after_sink = tl.sink - 1;
-        const int jump = (tl.win - tl.sink + 1) * kTile;  // from the last tile of the sinks to the window's first
-        for (int t = t0; t < t1; ++t, j0 += t - 1 == after_sink ? jump : kTile) {
-            copy_wait<kStages - 2>();
-            __syncwarp();
-            issue(t + kStages - 1);  // into the place that was read in the last step
-            const uint32_t st = ring + read;
-            read = read == (kStages - 1) * St::kBytes ? 0 : read + St::kBytes;
+        const auto any_step = [&](uint32_t st, int j0) {
             if (j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks))
                 step(st, j0, Flag<false>());
             else if (j0 < L)
                 step(st, j0, Flag<true>());
+        };
+        for (int t = part.t0; t < t1; t += 2) {
+            const uint32_t st = ring + (fill ^ 2 * St::kBytes);  // the pair of tiles t, t + 1
+            __syncwarp();
+            issue(part, t + 2);  // into the half that was read in the last turn
+            copy_wait<1>();
+            __syncwarp();
+            any_step(st, tl.at(t) * kTile + warp * 16);
+            if (t + 1 < t1) any_step(st + St::kBytes, tl.at(t + 1) * kTile + warp * 16);
         }
 
-        // ---- join the warps ----
-        copy_wait<0>();
-        __syncthreads();  // every warp is done with the rings
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        // ---- the next part's copies begin; then the warps' sums are joined ----
+        begin_copies(ahead, page0, page1);
+{
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[nt][t] += __shfl_xor_sync(0xffffffffu, l[nt][t], d);
-                const int r = nt * 8 + 2 * cq + t;
+                for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
+                const int r = 2 * cq + t;
                 if (gq == 0) {
-                    sm_m[warp][r] = m[nt][t];
-                    sm_l[warp][r] = l[nt][t];
+                    sm_m[warp][r] = m[t] * sc[t];
+                    sm_l[warp][r] = l[t];
                 }
                 // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even: low nibbles) or gq + 8
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    const float off = -8.f * psum[nt][n][t];
+                    const float off = -8.f * psum[n][t];
                     *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) =
-                        make_float4(fmaf(acc[nt][2 * n][t], 1.f / kLowUnit, off),
-                                    fmaf(acc[nt][2 * n][2 + t], 1.f / kHighUnit, off),
-                                    fmaf(acc[nt][2 * n + 1][t], 1.f / kLowUnit, off),
-                                    fmaf(acc[nt][2 * n + 1][2 + t], 1.f / kHighUnit, off));
+                        make_float4(fmaf(acc[2 * n][t], 1.f / kLowUnit, off),
+                                    fmaf(acc[2 * n][2 + t], 1.f / kHighUnit, off),
+                                    fmaf(acc[2 * n + 1][t], 1.f / kLowUnit, off),
+                                    fmaf(acc[2 * n + 1][2 + t], 1.f / kHighUnit, off));
                 }
             }
         }
         __syncthreads();
         {
-            const int pb = part.b, ph = part.hz / a.Z, pr0 = (part.hz % a.Z) * ROWS;
-            const bool begun = part.t0 == 0, done = begun && part.t1 == part.tl.n;
+            const bool begun = part.t0 == 0, done = begun && t1 == tl.n;
             const size_t part_row = ((size_t)blockIdx.x * 2 + begun) * ROWS;
             for (int x = threadIdx.x; x < ROWS * D; x += kThreads) {
                 const int r = x / D, d = x % D;
-                if (pr0 + r >= R) break;
+                if (r0 + r >= R) break;
                 float mx = -FLT_MAX;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
@@ -665,8 +745,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
                     y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
                 }
                 if (done) {
-                    const int h = ph * a.G + (pr0 + r) / a.M, i = (pr0 + r) % a.M;
-                    put<T>(a.o, (((size_t)pb * a.Hq + h) * a.M + i) * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
+                    put<T>(a.o, (first_row + r0 + r) * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
                 } else {
                     a.ws_acc[(part_row + r) * D + d] = y;
                     if (d == 0) {
@@ -675,67 +754,93 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kBlocks8 : kBlocks16) kv4_
                     }
                 }
             }
-            __syncthreads();  // the part is read
-            if (threadIdx.x == 0) {
-                if (begun && !done) {
-                    // the block that holds the segment's last tile: the last one that starts at or before it
-                    const long long e = part.u + part.tl.n;
-                    a.cut[blockIdx.x] =
-                        make_int4(pb, part.hz, (int)((e * part.blocks + part.total - 1) / part.total - 1), 0);
-                }
-                part.u += part.t1 - part.t0;
-                part.rem += part.t1 - part.t0;
-                if (part.rem == (long long)part.tl.n * H) {
-                    ++part.b;
-                    part.rem = 0;
-                }
-                if (part.u < part.end) set_part(part, a);
+            if (threadIdx.x == 0 && begun && !done) {
+                const int n = tl.n + kPartCost;
+                a.cut[blockIdx.x] = make_int4(part.b, part.hz, shares.block_of(part.u - part.rem % n + n - 1), 0);
             }
+            __syncthreads();  // the part and the sums are read
+            if (threadIdx.x == 0) next_part(parts[turn], parts[turn ^ 1], a, end);
+            __syncthreads();
         }
     }
 }
 
-// Joins the parts of the segment that block `blockIdx.x` of the decode kernel left unfinished, one row per block: the
-// part in that block's second place and those in the first places of the blocks behind it. Four warps share the parts.
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const DecodeArgs a) {
-    __shared__ float sm_l[kWarps];
-    __shared__ float4 sm_y[kWarps][D / 4];
+// Joins the parts of the segment that block blockIdx.x left unfinished: the part in that block's second slot and those
+// in the first slots of the blocks behind it. kJoinWarps / rows of the warps share the parts of a row,
+// eight at a time: what bounds this kernel is the chain of loads (cut, then parts).
+constexpr int kJoinWarps = 16, kJoinBatch = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const DecodeArgs a) {
+    __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
+    __shared__ float4 sm_y[kJoinWarps][D / 4];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 cut = a.cut[blockIdx.x];
-    const int r = blockIdx.y, r0 = (cut.y % a.Z) * ROWS, R = a.G * a.M;
-    if (cut.x < 0 || r0 + r >= R) return;
+    if (cut.x < 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r0 = (cut.y % a.Z) * ROWS, rows = min(ROWS, a.G * a.M - r0);
+    const int team = rows <= 1 ? 16 : rows <= 2 ? 8 : rows <= 4 ? 4 : 2;  // warps of a row
+    const int r = warp / team, share = warp % team;
     const int parts = cut.z - (int)blockIdx.x + 1;
-    const auto row_of = [&](int x) { return ((size_t)(blockIdx.x + x) * 2 + (x == 0)) * ROWS + r; };
-    float mx = -FLT_MAX;
-    for (int x = lane; x < parts; x += 32) mx = fmaxf(mx, a.ws_m[row_of(x)]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    float l = 0.f;
+    const bool has = lane < D / 4;
+    float mx = -FLT_MAX, l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = warp; x < parts; x += kWarps) {
-        const size_t row = row_of(x);
-        const float f = ptx::ex2(a.ws_m[row] - mx);
-        l = fmaf(f, a.ws_l[row], l);
-        if (lane < D / 4) {
-            const float4 v = reinterpret_cast<const float4*>(a.ws_acc + row * D)[lane];
-            y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+    if (r < rows) {
+        for (int x0 = share; x0 < parts; x0 += kJoinBatch * team) {
+            float m[kJoinBatch], s[kJoinBatch];
+            float4 v[kJoinBatch];
+#pragma unroll
+            for (int e = 0; e < kJoinBatch; ++e) {
+                const int x = x0 + e * team;
+                m[e] = -FLT_MAX;
+                s[e] = 0.f;
+                v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x < parts) {
+                    const size_t row = ((size_t)(blockIdx.x + x) * 2 + (x == 0)) * ROWS + r;
+                    m[e] = a.ws_m[row];
+                    s[e] = a.ws_l[row];
+                    if (has) v[e] = reinterpret_cast<const float4*>(a.ws_acc + row * D)[lane];
+                }
+            }
+            float top = mx;
+#pragma unroll
+            for (int e = 0; e < kJoinBatch; ++e) top = fmaxf(top, m[e]);
+            const float f0 = ptx::ex2(mx - top);
+            l *= f0;
+            y = make_float4(y.x * f0, y.y * f0, y.z * f0, y.w * f0);
+            mx = top;
+#pragma unroll
+            for (int e = 0; e < kJoinBatch; ++e) {
+                const float f = ptx::ex2(m[e] - top);
+                l = fmaf(f, s[e], l);
+                y = make_float4(fmaf(f, v[e].x, y.x), fmaf(f, v[e].y, y.y), fmaf(f, v[e].z, y.z), fmaf(f, v[e].w, y.w));
+            }
         }
     }
-    if (lane == 0) sm_l[warp] = l;
-    if (lane < D / 4) sm_y[warp][lane] = y;
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    float lt = 0.f, yt = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        lt += sm_l[w];
-        yt += reinterpret_cast<const float*>(sm_y[w])[threadIdx.x];
+    if (lane == 0) {
+        sm_m[warp] = mx;
+        sm_l[warp] = l;
     }
-    const int h = (cut.y / a.Z) * a.G + (r0 + r) / a.M, i = (r0 + r) % a.M;
-    put<T>(a.o, (((size_t)cut.x * a.Hq + h) * a.M + i) * D + threadIdx.x, lt > 0.f ? yt * (a.v_scale / lt) : 0.f);
+    if (has) sm_y[warp][lane] = y;
+    __syncthreads();
+    if (share != 0 || r >= rows || !has) return;
+    float top = mx;
+    for (int w = warp + 1; w < warp + team; ++w) top = fmaxf(top, sm_m[w]);
+    l = 0.f;
+    y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = warp; w < warp + team; ++w) {
+        const float f = ptx::ex2(sm_m[w] - top);
+        const float4 v = sm_y[w][lane];
+        l = fmaf(f, sm_l[w], l);
+        y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+    }
+    const size_t at = (((size_t)cut.x * a.Hq + cut.y / a.Z * a.G) * a.M + r0 + r) * D + 4 * lane;
+    const float f = l > 0.f ? a.v_scale / l : 0.f;
+    put<T>(a.o, at, y.x * f);
+    put<T>(a.o, at + 1, y.y * f);
+    put<T>(a.o, at + 2, y.z * f);
+    put<T>(a.o, at + 3, y.w * f);
 }
 
 struct Kv4Call {
@@ -745,9 +850,12 @@ struct Kv4Call {
     float k_descale, v_descale;
 };
 
-int rows_per_block(const Problem& p) { return (long long)p.G * p.M <= 8 ? 8 : 16; }
+int sm_count() {
+    const int n = device_sm_count();
+    return n > 0 ? n : 148;
+}
 
-int blocks_per_sm(const Problem& p) { return rows_per_block(p) == 8 ? kBlocks8 : kBlocks16; }
+int row_blocks(const Problem& p) { return (int)(((long long)p.G * p.M + ROWS - 1) / ROWS); }
 
 // One block for every place on the GPU, fewer while the longest lengths could not give each kMinTiles tiles.
 int plan_blocks(const Kv4Call& c) {
@@ -759,49 +867,43 @@ int plan_blocks(const Kv4Call& c) {
         if (wt < tiles) tiles = wt;
     }
     if (tiles < 1) tiles = 1;
-    const int rows = rows_per_block(p);
-    tiles *= (long long)p.B * p.Hkv * (((long long)p.G * p.M + rows - 1) / rows);
-    int sms = device_sm_count();
-    if (sms <= 0) sms = 148;
-    const long long most = (long long)sms * blocks_per_sm(p), want = (tiles + kMinTiles - 1) / kMinTiles;
+    tiles = (tiles + kPartCost) * p.B * p.Hkv * row_blocks(p);
+    const long long most = (long long)sm_count() * kBlocksPerSm, want = (tiles + kMinTiles - 1) / kMinTiles;
     return (int)(want < most ? want : most);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D>
 cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
-    constexpr int kRing = kWarps * kStages * Stage<D>::kBytes, kSums = kWarps * 8 * NT * D * (int)sizeof(float);
-    constexpr int kSmem = kRing > kSums ? kRing : kSums;
+    constexpr int kSmem = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
     static PerDeviceOnce once;
-    cudaError_t e = once_per_device(once, [] {
-        return cudaFuncSetAttribute(kv4_decode_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = once_per_device(once, [] {
+        return cudaFuncSetAttribute(kv4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (e != cudaSuccess) return e;
-    kv4_decode_kernel<T, D, NT><<<(unsigned)blocks, kThreads, kSmem, s>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || blocks == 1) return e;
-    // launched while the decode kernel runs; waits for its end before it reads
-    const int rows = a.G * a.M < 8 * NT ? a.G * a.M : 8 * NT;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)rows);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
+    // each may be launched while the kernel in front of it runs, and waits for its end
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D, 8 * NT>, a);
+    const cudaError_t r = cudaLaunchKernelEx(&cfg, kv4_decode_kernel<T, D>, a);
+    if (r != cudaSuccess || blocks == 1) return r;
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, a);
 }
 
 template <typename T>
-cudaError_t launch_d(const DecodeArgs& a, int D, int rows, int blocks, cudaStream_t s) {
-    switch (D + (rows == 16)) {
-        case 32: return launch_t<T, 32, 1>(a, blocks, s);
-        case 33: return launch_t<T, 32, 2>(a, blocks, s);
-        case 64: return launch_t<T, 64, 1>(a, blocks, s);
-        case 65: return launch_t<T, 64, 2>(a, blocks, s);
-        case 128: return launch_t<T, 128, 1>(a, blocks, s);
-        default: return launch_t<T, 128, 2>(a, blocks, s);
+cudaError_t launch_d(const DecodeArgs& a, int D, int blocks, cudaStream_t s) {
+    switch (D) {
+        case 32: return launch_t<T, 32>(a, blocks, s);
+        case 64: return launch_t<T, 64>(a, blocks, s);
+        default: return launch_t<T, 128>(a, blocks, s);
     }
 }
 
@@ -822,7 +924,7 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
     const int64_t nq = (int64_t)B * Hq * M * D, ntab = (int64_t)B * max_pages;
     const int64_t cover = (int64_t)max_pages * cache.page_size;
     const int64_t longest = cover < max_seq_len ? cover : max_seq_len;
-    if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + 15) / 16 > 65535 ||
+    if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + ROWS - 1) / ROWS > 65535 ||
         longest > kI32Max - kTile || (int64_t)cache.num_pages * (cache.page_size / 16) * Hkv > kI32Max)
         return ATTN_ERR_OVERFLOW;
     if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
@@ -857,26 +959,23 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
 
 bool nothing_to_attend(const Kv4Call& c) { return c.max_len == 0 || c.c.num_pages == 0; }
 
-// Parts of cut segments, two per block, and the cut segments: [blocks] int4, then m, l and acc.
-size_t workspace_bytes(const Kv4Call& c) {
-    const size_t rows = (size_t)plan_blocks(c) * 2 * rows_per_block(c.p);
-    return plan_blocks(c) * sizeof(int4) + rows * (2 + c.p.D) * sizeof(float);
+// Cut segments and their parts, two per block: [blocks] int4, then m, l and acc.
+size_t workspace_bytes(int blocks, int D) {
+    return blocks * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
 }
 
 int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void* o, void* ws, size_t ws_bytes,
-        cudaStream_t s) {
+        int blocks, cudaStream_t s) {
     const Problem& p = c.p;
-    if (!ws || ws_bytes < workspace_bytes(c)) return ATTN_ERR_WORKSPACE;
+    if (!ws || ws_bytes < workspace_bytes(blocks, p.D)) return ATTN_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
-    const int blocks = plan_blocks(c), rows = rows_per_block(p);
-    const size_t n = (size_t)blocks * 2 * rows;
+    const size_t n = (size_t)blocks * 2 * ROWS;
     int4* cut = static_cast<int4*>(ws);
     float* wm = reinterpret_cast<float*>(cut + blocks);
-    const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G,
-                       (p.G * p.M + rows - 1) / rows, c.max_pages, c.max_len, p.causal, p.window, c.sinks,
-                       p.scale_log2, c.v_descale};
-    const cudaError_t e = p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, rows, blocks, s)
-                                               : launch_d<__half>(a, p.D, rows, blocks, s);
+    const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
+                       c.max_pages, c.max_len, p.causal, p.window, c.sinks, p.scale_log2, c.v_descale};
+    const cudaError_t e =
+        p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, blocks, s) : launch_d<__half>(a, p.D, blocks, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -897,7 +996,7 @@ size_t attn_decode_paged_kv4_workspace_bytes(int B, int Hq, int Hkv, int M, int 
                  0.f, 1.f, 1.f, ATTN_BF16, &c) != ATTN_OK)
         return 0;
     if ((int64_t)B * Hq * M == 0 || nothing_to_attend(c)) return 0;
-    return workspace_bytes(c);
+    return workspace_bytes(plan_blocks(c), D);
 }
 
 int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
@@ -915,11 +1014,12 @@ int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scal
     if ((int64_t)B * Hq * M == 0) return ATTN_OK;
     if (nothing_to_attend(c))  // no sequence can hold a key: every row outputs 0
         return cudaMemsetAsync(o, 0, (size_t)B * Hq * M * D * 2, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-    const size_t bytes = workspace ? 0 : workspace_bytes(c);
-    if (workspace) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, s);
+    const int blocks = plan_blocks(c);
+    if (workspace) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, blocks, s);
+    const size_t bytes = workspace_bytes(blocks, D);
     void* ws = nullptr;
     if (cudaMallocAsync(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    rc = run(c, q, block_table, seq_lens, o, ws, bytes, s);
+    rc = run(c, q, block_table, seq_lens, o, ws, bytes, blocks, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
     return rc;
 }

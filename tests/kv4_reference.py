@@ -88,11 +88,11 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype, ku=None, vu=None
     the unit, whose difference is the value: sums of them are up to 23 units large, whatever the values are. The
     bound per element counts
       the output's rounding                            eps/2 |o|
-      two roundings to FP16, of the probability p (times 2^6, at most 2^6) and of its product with the
-      value's scale                                    2 * 2^-11 A,        A = sum w |v|
+      two roundings to FP16, of the probability p (times 2^3 or more at the largest score) and of its product
+      with the value's scale                           2 * 2^-11 A,        A = sum w |v|
       such products below FP16's normal range: each is off by at most 2^-25, times a code of at most 8 and
-      the factor vd, over a sum of p that is at least 2^6; the same again for p itself
-                                                       L 2 * 2^-25 8 vd / 2^6 max(1, s)
+      the factor vd, over a sum of p that is at least 2^3; the same again for p itself
+                                                       L 2 * 2^-25 8 vd / 2^3 max(1, s)
       FP32 sums over the keys, 16 a matrix instruction (L/16 + 64) 2^-23 23 sum w vu
       the logits: the query's small elements (2^-25 of the row's largest), FP32 sums over D (truncating
       adders counted: 2^-23 a term) of up to 23 ku |q| each, and the exponent's argument; a logit's error
@@ -120,7 +120,7 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype, ku=None, vu=None
             logit = (D + 8) * 2.0 ** -23 * size + 2.0 ** -25 * np.abs(qq).max() * abs(scale) * np.abs(kk).sum(1)
             logit = (logit + 4 * 2.0 ** -24 * (np.abs(s) + abs(s.max()))).max()
             n = len(s)
-            small = n * 2.0 ** -27 * max(vd, np.abs(vv).max())  # 8 vd s is at most the largest value and more
+            small = n * 2.0 ** -24 * max(vd, np.abs(vv).max())  # 8 vd s is at most the largest value and more
             bound[h, i] = (half * np.abs(o[h, i]) + A * (2.0 ** -10 + 2 * logit) + U * (n / 16 + 64) * 2.0 ** -23
                            + small + 1e-30)
             if out_dtype == torch.float16:
