@@ -2,19 +2,21 @@
 //
 // Work. A segment is the visible keys of one (sequence, KV head, block of 8 grouped
 // query rows), in tiles of 64 keys; query head h = g * G + r / M, row i = r % M. The
-// tiles of all segments in a row are cut into ranges, one per block of a grid that
-// fills the GPU once, whatever the lengths are: each block counts the tiles from
-// seq_lens itself. A segment that lies inside a block's range is written to o
-// there; of one that is cut, each block leaves its part's (m, l, acc) in the
-// workspace (at most two parts a block: one begun before it, one that goes on
-// behind it), and a second kernel joins them by the common-maximum rule. Ranges
-// depend on the lengths and the grid alone, so the order of all sums does too.
+// tiles of all segments in a row are cut into equal ranges, one per team of four
+// warps; a block of three teams fills an SM, and the grid the GPU, once, whatever the
+// lengths are: each team counts the tiles from seq_lens itself. A segment that lies
+// inside a team's range is written to o there; of one that is cut, each team leaves
+// its part's (m, l, acc) in the workspace (at most two parts a team: one begun before
+// it, one that goes on behind it), and a second kernel joins them by the
+// common-maximum rule. Ranges depend on the lengths and the grid alone, so the order
+// of all sums does too. (Three teams in one block and not in three: the schedulers
+// then serve them alike; as blocks they ended one after the other, 135 us for 129.)
 //
-// In a block, four warps take 16 keys each of a tile and keep their own running
+// The warps of a team take 16 keys each of a tile and keep their own running
 // (m, l, acc) per row, joined through shared memory at the end of a segment's part.
-// Each warp copies its keys' codes and scales into a ring of its own
-// (cp.async, a pair of tiles ahead, no barrier between warps); the next part's
-// copies begin before the sums of the last one are joined.
+// Each warp copies its keys' codes and scales into a ring of its own (cp.async, a
+// pair of tiles ahead, no barrier between warps); the next part's copies begin
+// before the sums of the last one are joined.
 //
 // A warp's products run transposed, on m16n8k16 matrix instructions with the
 // cache as the left operand, so that a row of the cache is expanded once for all
@@ -32,6 +34,12 @@
 // keys.) The scales are applied where there are fewer numbers than elements: a
 // key's to the sum of a group's 32 products, a value's to the probabilities, once
 // per group.
+// What bounds it: the expansion, 320 instructions of a warp per 16 keys of D = 128 on
+// pipes that the 21 matrix instructions among them share. 64 sequences of 8192 keys,
+// 8 KV heads (570 MB): 122 us, 4.7 TB/s, 69 % of the measured copy bandwidth; with
+// the copies left out 115 us. 12 warps of 168 registers beat 16 of 128 (139 us), 20 of
+// 96 and 24 of 80: fewer registers leave the compiler less to overlap in a warp.
+// FP8 products (half the expansion) run at a quarter of the rate and lose (144 us).
 // Rounded below 32 bits: Q to FP16 after scaling each row by a power of two to
 // maximum 2^14..2^15 (exact for elements above 2^-20 of the maximum), the
 // probabilities to FP16, kept 64 times too large to stay clear of its small numbers
@@ -52,14 +60,14 @@
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kTeams = 3;            // of a block; one block per SM: 12 warps of 168 registers
+constexpr int kWarps = 4;            // of a team
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16 * kWarps;  // keys of a tile, 16 per warp
-constexpr int kStages = 4;          // tiles in a warp's ring, two pairs
-constexpr int kBlocksPerSm = 3;     // 12 warps of 168 registers
-constexpr int ROWS = 8;             // query rows of a block
-constexpr int kPartCost = 3;        // what a segment costs beside its tiles, in tiles (see Part)
-constexpr int kMinTiles = 4;        // a block's range is at least this long while there are blocks to spare
+constexpr int kTile = 16 * kWarps;   // keys of a tile, 16 per warp
+constexpr int kStages = 4;           // tiles in a warp's ring, two pairs
+constexpr int ROWS = 8;              // query rows of a team
+constexpr int kPartCost = 3;         // what a segment costs beside its tiles, in tiles (see Part)
+constexpr int kMinTiles = 4;         // a team's range is at least this long while there are teams to spare
 // Probabilities are kept times 2^kPShift relative to a score that the largest one may exceed by kPSlack (base 2): times
 // a scale of at most 448 they stay below 2^7 * 448 = 57344.
 constexpr float kPShift = 3.0f, kPSlack = 4.0f;
@@ -70,8 +78,8 @@ struct DecodeArgs {
     const int* table;
     const int* lens;
     void* o;
-    float *ws_m, *ws_l, *ws_acc;  // [blocks][2][ROWS], the same, [blocks][2][ROWS][D]
-    int4* cut;                    // [blocks]: segment that a block leaves unfinished (b, head * Z + z), last block of it
+    float *ws_m, *ws_l, *ws_acc;  // [places][2][ROWS], the same, [places][2][ROWS][D]
+    int4* cut;                    // [places]: segment that a team leaves unfinished (b, head * Z + z), last place of it
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
     int causal, window, sinks;
@@ -215,15 +223,15 @@ __device__ __forceinline__ long long divide(long long x, int n, int* rest) {
     return q;
 }
 
-// The tiles are shared out equally: `per` to a block, and one more to the first `more` of them.
+// The tiles are shared out equally: `per` to a place, and one more to the first `more` of them. (Larger shares for the
+// warps of a block that come first measured slower.)
 struct Shares {
     long long per;
     int more;
     __device__ __forceinline__ long long begin(int i) const { return per * i + min(i, more); }
-    __device__ __forceinline__ int block_of(long long tile) const {
+    __device__ __forceinline__ int place_of(long long tile) const {
         const long long first = (per + 1) * more;
-        if (tile < first) return (int)(tile / (per + 1));
-        return more + (int)((tile - first) / per);
+        return (int)(tile < first ? tile / (per + 1) : more + (tile - first) / per);
     }
 };
 
@@ -337,18 +345,20 @@ struct Stage {
     }
 };
 
-// Exclusive sum over the block's threads, and the total.
-__device__ __forceinline__ long long block_sum(long long x, long long* part, long long* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Exclusive sum over a team's threads, and the total.
+template <class Sync>
+__device__ __forceinline__ long long team_sum(long long x, int thread, long long* part, const Sync& sync,
+                                              long long* total) {
+    const int lane = thread & 31, warp = thread >> 5;
     long long s = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += y;
     }
-    __syncthreads();  // the last use of `part` is done
+    sync();  // the last use of `part` is done
     if (lane == 31) part[warp] = s;
-    __syncthreads();
+    sync();
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -359,20 +369,31 @@ __device__ __forceinline__ long long block_sum(long long x, long long* part, lon
     return s - x + before;
 }
 
+template <int D>
+constexpr int kTeamBytes = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const DecodeArgs a) {
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
-    extern __shared__ __align__(16) uint8_t smem[];  // the rings, then the warps' sums of a part
+    extern __shared__ __align__(16) uint8_t smem_of_block[];
+    struct Shared {
+        float m[kWarps][ROWS], l[kWarps][ROWS];  // of a part, by warp
+        int2 vis[2][ROWS];                       // the visible range of every row, of this part and of the last or next
+        long long sums[kWarps];
+        long long end;  // of the team's range
+        Part parts[2];
+        Shares shares;
+    };
+    __shared__ Shared shared_of_block[kTeams];
+    const int team = threadIdx.x / kThreads, thread = threadIdx.x % kThreads;
+    Shared& sh = shared_of_block[team];
+    uint8_t* smem = smem_of_block + team * kTeamBytes<D>;  // the rings, then the warps' sums of a part
     float* sm_acc = reinterpret_cast<float*>(smem + kWarps * kStages * St::kBytes);  // [kWarps][ROWS][D]
-    __shared__ float sm_m[kWarps][ROWS], sm_l[kWarps][ROWS];
-    __shared__ int2 sm_vis[2][ROWS];  // the visible range of every row, of this part and of the last or next
-    __shared__ long long sums[kWarps];
-    __shared__ Part parts[2];
-    __shared__ Shares shares;
-    __shared__ long long end;  // of the block's range
+    const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kThreads) : "memory"); };
+    const int place = team * (int)gridDim.x + (int)blockIdx.x;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = thread >> 5, lane = thread & 31;
     const int gq = lane >> 2, cq = lane & 3;  // the lane's place in a matrix fragment
     const int key_slot = (gq >> 1) + 4 * (gq & 1);  // the key of slot gq; slot gq + 8: 8 more
     const uint32_t ring = ptx::smem_u32(smem) + warp * (kStages * St::kBytes);
@@ -398,38 +419,39 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
         long long total = 0, cost = 0, before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             long long all;
-            cost = cost_of(b0 + threadIdx.x);
-            before = block_sum(cost, sums, &all);
+            cost = cost_of(b0 + thread);
+            before = team_sum(cost, thread, sh.sums, team_sync, &all);
             total += all;
         }
-        // a grid that is larger than the tiles need uses its first blocks only
-        const int blocks =
-            total >= (long long)kMinTiles * gridDim.x ? (int)gridDim.x : (int)((total + kMinTiles - 1) / kMinTiles);
-        Shares sh;
-        sh.per = divide(total, blocks, &sh.more);
-        if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        if (blockIdx.x >= blocks) return;
-        const long long u0 = sh.begin(blockIdx.x);
-        if (threadIdx.x == 0) shares = sh;
+        // a grid that is larger than the tiles need uses its first places only
+        const int all_places = (int)gridDim.x * kTeams;
+        const int places =
+            total >= (long long)kMinTiles * all_places ? all_places : (int)((total + kMinTiles - 1) / kMinTiles);
+        Shares shares;
+        shares.per = divide(total, places, &shares.more);
+        if (thread == 0) a.cut[place] = make_int4(-1, 0, 0, 0);
+        if (place >= places) return;
+        if (thread == 0) sh.shares = shares;
+        const long long u0 = shares.begin(place);
         long long behind = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             long long all = total;
             if (a.B > kThreads) {  // one chunk's sums are still at hand
-                cost = cost_of(b0 + threadIdx.x);
-                before = behind + block_sum(cost, sums, &all);
+                cost = cost_of(b0 + thread);
+                before = behind + team_sum(cost, thread, sh.sums, team_sync, &all);
             }
             if (before <= u0 && u0 < before + cost) {
-                parts[0].u = u0;
-                parts[0].rem = u0 - before;
-                parts[0].b = b0 + threadIdx.x;
-                end = sh.begin(blockIdx.x + 1);
-                set_part(parts[0], a, end);
+                sh.parts[0].u = u0;
+                sh.parts[0].rem = u0 - before;
+                sh.parts[0].b = b0 + thread;
+                sh.end = shares.begin(place + 1);
+                set_part(sh.parts[0], a, sh.end);
             }
             behind += all;
             if (u0 < behind) break;
         }
     }
-    __syncthreads();
+    team_sync();
 
     // ---- the copies of a part ----
     // the pool's blocks of this warp's keys, for 32 tiles at a time: lane x has that of tile base + x
@@ -464,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
         next_page = page1;
         issue(p, p.t0);
     };
-    begin_copies(parts[0], page_of(parts[0], parts[0].t0 + lane), page_of(parts[0], parts[0].t0 + 32 + lane));
-    if (threadIdx.x == 0) next_part(parts[1], parts[0], a, end);
-    __syncthreads();
+    begin_copies(sh.parts[0], page_of(sh.parts[0], sh.parts[0].t0 + lane), page_of(sh.parts[0], sh.parts[0].t0 + 32 + lane));
+    if (thread == 0) next_part(sh.parts[1], sh.parts[0], a, sh.end);
+    team_sync();
 
     for (int turn = 0;; turn ^= 1) {
-        const Part& part = parts[turn];
+        const Part& part = sh.parts[turn];
         if (part.t0 == part.t1) return;
         const int t1 = part.t1, L = part.L;
         const Tiles tl = part.tl;
@@ -477,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
         const int r0 = (part.hz % a.Z) * ROWS;
         const size_t first_row = ((size_t)part.b * a.Hq + part.hz / a.Z * a.G) * a.M;
         // what the next part begins with, asked for now: its pages, and its query rows into L1
-        const Part& ahead = parts[turn ^ 1];
+        const Part& ahead = sh.parts[turn ^ 1];
         const int page0 = page_of(ahead, ahead.t0 + lane), page1 = page_of(ahead, ahead.t0 + 32 + lane);
         if (ahead.t0 < ahead.t1) {
             const int r = (ahead.hz % a.Z) * ROWS + gq;
@@ -550,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
             const int p = r0 + lane < R ? (r0 + lane) % a.M + L - a.M : L - 1;
             int2 v;
             key_range(p, L, a.causal, a.window, &v.x, &v.y);
-            sm_vis[turn][lane] = v;
+            sh.vis[turn][lane] = v;
         }
         __syncwarp();
         // keys [all_lo, all_hi) are visible to every row
@@ -628,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
             for (int e = 0; e < 4; ++e) {
                 if (edge) {
                     const int j = j0 + key_slot + 8 * (e >> 1);
-                    const int2 vis = sm_vis[turn][2 * cq + (e & 1)];
+                    const int2 vis = sh.vis[turn][2 * cq + (e & 1)];
                     if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[e] = -INFINITY;  // a masked key scores -inf
                 }
                 rises |= s[e] > limit[e & 1];
@@ -712,8 +734,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
                 for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
                 const int r = 2 * cq + t;
                 if (gq == 0) {
-                    sm_m[warp][r] = m[t] * sc[t];
-                    sm_l[warp][r] = l[t];
+                    sh.m[warp][r] = m[t] * sc[t];
+                    sh.l[warp][r] = l[t];
                 }
                 // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even: low nibbles) or gq + 8
 #pragma unroll
@@ -727,21 +749,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
                 }
             }
         }
-        __syncthreads();
+        team_sync();
         {
             const bool begun = part.t0 == 0, done = begun && t1 == tl.n;
-            const size_t part_row = ((size_t)blockIdx.x * 2 + begun) * ROWS;
-            for (int x = threadIdx.x; x < ROWS * D; x += kThreads) {
+            const size_t part_row = ((size_t)place * 2 + begun) * ROWS;
+            for (int x = thread; x < ROWS * D; x += kThreads) {
                 const int r = x / D, d = x % D;
                 if (r0 + r >= R) break;
                 float mx = -FLT_MAX;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][r]);
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.m[w][r]);
                 float lt = 0.f, y = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float f = ptx::ex2(sm_m[w][r] - mx);  // a warp that saw no key has sums of zero
-                    lt = fmaf(f, sm_l[w][r], lt);
+                    const float f = ptx::ex2(sh.m[w][r] - mx);  // a warp that saw no key has sums of zero
+                    lt = fmaf(f, sh.l[w][r], lt);
                     y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
                 }
                 if (done) {
@@ -754,19 +776,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_decode_kernel(cons
                     }
                 }
             }
-            if (threadIdx.x == 0 && begun && !done) {
+            if (thread == 0 && begun && !done) {
                 const int n = tl.n + kPartCost;
-                a.cut[blockIdx.x] = make_int4(part.b, part.hz, shares.block_of(part.u - part.rem % n + n - 1), 0);
+                a.cut[place] = make_int4(part.b, part.hz, sh.shares.place_of(part.u - part.rem % n + n - 1), 0);
             }
-            __syncthreads();  // the part and the sums are read
-            if (threadIdx.x == 0) next_part(parts[turn], parts[turn ^ 1], a, end);
-            __syncthreads();
+            team_sync();  // the part and the sums are read
+            if (thread == 0) next_part(sh.parts[turn], sh.parts[turn ^ 1], a, sh.end);
+            team_sync();
         }
     }
 }
 
-// Joins the parts of the segment that block blockIdx.x left unfinished: the part in that block's second slot and those
-// in the first slots of the blocks behind it. kJoinWarps / rows of the warps share the parts of a row,
+// Joins the parts of the segment that the team at place blockIdx.x left unfinished: the part in that place's second
+// slot and those in the first slots of the places behind it. kJoinWarps / rows of the warps share the parts of a row,
 // eight at a time: what bounds this kernel is the chain of loads (cut, then parts).
 constexpr int kJoinWarps = 16, kJoinBatch = 8;
 
@@ -857,7 +879,7 @@ int sm_count() {
 
 int row_blocks(const Problem& p) { return (int)(((long long)p.G * p.M + ROWS - 1) / ROWS); }
 
-// One block for every place on the GPU, fewer while the longest lengths could not give each kMinTiles tiles.
+// One block for every SM, fewer while the longest lengths could not give one team of each kMinTiles tiles.
 int plan_blocks(const Kv4Call& c) {
     const Problem& p = c.p;
     long long tiles = ((long long)c.max_len + kTile - 1) / kTile;
@@ -868,13 +890,13 @@ int plan_blocks(const Kv4Call& c) {
     }
     if (tiles < 1) tiles = 1;
     tiles = (tiles + kPartCost) * p.B * p.Hkv * row_blocks(p);
-    const long long most = (long long)sm_count() * kBlocksPerSm, want = (tiles + kMinTiles - 1) / kMinTiles;
+    const long long most = sm_count(), want = (tiles + kMinTiles - 1) / kMinTiles;
     return (int)(want < most ? want : most);
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
-    constexpr int kSmem = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
+    constexpr int kSmem = kTeams * kTeamBytes<D>;
     static PerDeviceOnce once;
     const cudaError_t e = once_per_device(once, [] {
         return cudaFuncSetAttribute(kv4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -886,13 +908,14 @@ cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kTeams * kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t r = cudaLaunchKernelEx(&cfg, kv4_decode_kernel<T, D>, a);
-    if (r != cudaSuccess || blocks == 1) return r;
+    if (r != cudaSuccess) return r;
+    cfg.gridDim = dim3((unsigned)blocks * kTeams);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, a);
@@ -959,9 +982,9 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
 
 bool nothing_to_attend(const Kv4Call& c) { return c.max_len == 0 || c.c.num_pages == 0; }
 
-// Cut segments and their parts, two per block: [blocks] int4, then m, l and acc.
+// Cut segments and their parts, two per team: [places] int4, then m, l and acc.
 size_t workspace_bytes(int blocks, int D) {
-    return blocks * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
+    return (size_t)blocks * kTeams * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
 }
 
 int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void* o, void* ws, size_t ws_bytes,
@@ -969,9 +992,9 @@ int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void
     const Problem& p = c.p;
     if (!ws || ws_bytes < workspace_bytes(blocks, p.D)) return ATTN_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
-    const size_t n = (size_t)blocks * 2 * ROWS;
+    const size_t n = (size_t)blocks * kTeams * 2 * ROWS;
     int4* cut = static_cast<int4*>(ws);
-    float* wm = reinterpret_cast<float*>(cut + blocks);
+    float* wm = reinterpret_cast<float*>(cut + (size_t)blocks * kTeams);
     const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
                        c.max_pages, c.max_len, p.causal, p.window, c.sinks, p.scale_log2, c.v_descale};
     const cudaError_t e =
