@@ -48,8 +48,13 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 
 // ---------------------------------------------------------------------------
 // append: one thread takes 8 elements of a key row and the same 8 of the value
-// row; the 4 threads of a group share its maximum.
+// row; the 4 threads of a group share its maximum. A thread takes kAppendRows such
+// pieces, a block's width apart, with all their loads in flight at once: the chain
+// slot -> row -> store is what a thread waits for, and with one piece a thread the
+// kernel was bound by it.
 // ---------------------------------------------------------------------------
+constexpr int kAppendRows = 2;
+
 struct AppendArgs {
     const void* k;
     const void* v;
@@ -100,50 +105,60 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
     constexpr int NG = D / kKv4Group;
     constexpr int U = D / 8;  // threads of a row
-    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const long long row = idx / U;  // row of the batch times Hkv plus the head
-    const int u = (int)(idx % U);
-    const long long rows = (long long)a.T * a.Hkv;
-    const bool in = row < rows;
-    const int t = in ? (int)(row / a.Hkv) : 0, h = in ? (int)(row % a.Hkv) : 0;
-    const int slot = in ? __ldg(a.slots + t) : -1;
-    const bool live = slot >= 0 && slot < (long long)a.c.num_pages * a.c.page_size;
-    uint4 wk = make_uint4(0, 0, 0, 0), wv = wk;
-    if (live) {
-        wk = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + h * D + u * 8));
-        wv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + h * D + u * 8));
-    }
-    uint32_t sk, sv;
-    const uint32_t ck = quantize8<T>(wk, a.k_inv, &sk);
-    const uint32_t cv = quantize8<T>(wv, a.v_inv, &sv);
+    const int u = threadIdx.x % U;
     const int i = u / 4, c = u % 4;  // group, and which 8 of its 32 elements
-    // value units of 4 elements: two groups' units at one position make a word, so
-    // the threads of groups i and i ^ 1 trade one unit each
-    int vword;
-    uint32_t vbits;
-    if (NG > 1) {
-        const bool odd = i & 1;
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? (cv & 0xFFFFu) : (cv >> 16), 4);
-        vbits = odd ? (got | (cv & 0xFFFF0000u)) : ((cv & 0xFFFFu) | (got << 16));
-        vword = ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2;
-    } else {
-        vbits = cv;
-        vword = c;
-    }
-    if (!live) return;
+    const long long rows = (long long)a.T * a.Hkv;  // of the batch times Hkv
+    const long long first = (long long)blockIdx.x * (kAppendRows * (kThreads / U)) + threadIdx.x / U;
     const int ps = a.c.page_size;
-    const size_t at = ((size_t)(slot / ps) * a.Hkv + h) * ps + slot % ps;
-    reinterpret_cast<uint32_t*>(a.c.k_codes + at * (D / 2))[c * NG + i] = ck;
-    reinterpret_cast<uint32_t*>(a.c.v_codes + at * (D / 2))[vword] = vbits;
-    if (c == 0) {
-        a.c.k_scales[at * NG + i] = (uint8_t)sk;
-        a.c.v_scales[at * NG + i] = (uint8_t)sv;
+    int slot[kAppendRows], head[kAppendRows];
+    uint4 wk[kAppendRows], wv[kAppendRows];
+#pragma unroll
+    for (int x = 0; x < kAppendRows; ++x) {
+        const long long row = first + x * (kThreads / U);
+        const bool in = row < rows;
+        const int t = in ? (int)(row / a.Hkv) : 0;
+        head[x] = in ? (int)(row - (long long)t * a.Hkv) : 0;
+        slot[x] = in ? __ldg(a.slots + t) : -1;
+        if (slot[x] >= (long long)a.c.num_pages * ps) slot[x] = -1;
+        // read whether the row has a slot or not: the loads need not wait for it
+        wk[x] = wv[x] = make_uint4(0, 0, 0, 0);
+        if (in) {
+            wk[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + head[x] * D + u * 8));
+            wv[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + head[x] * D + u * 8));
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < kAppendRows; ++x) {
+        uint32_t sk, sv;
+        const uint32_t ck = quantize8<T>(wk[x], a.k_inv, &sk);
+        const uint32_t cv = quantize8<T>(wv[x], a.v_inv, &sv);
+        // value units of 4 elements: two groups' units at one position make a word, so
+        // the threads of groups i and i ^ 1 trade one unit each
+        int vword = c;
+        uint32_t vbits = cv;
+        if (NG > 1) {
+            const bool odd = i & 1;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? (cv & 0xFFFFu) : (cv >> 16), 4);
+            vbits = odd ? (got | (cv & 0xFFFF0000u)) : ((cv & 0xFFFFu) | (got << 16));
+            vword = ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2;
+        }
+        if (slot[x] < 0) continue;
+        const size_t at = ((size_t)(slot[x] / ps) * a.Hkv + head[x]) * ps + slot[x] % ps;
+        reinterpret_cast<uint32_t*>(a.c.k_codes + at * (D / 2))[c * NG + i] = ck;
+        reinterpret_cast<uint32_t*>(a.c.v_codes + at * (D / 2))[vword] = vbits;
+        if (c == 0) {
+            a.c.k_scales[at * NG + i] = (uint8_t)sk;
+            a.c.v_scales[at * NG + i] = (uint8_t)sv;
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// gather: one thread writes 8 elements of a key row and the same 8 of the value row
+// gather: one thread writes 8 elements of a key row and the same 8 of the value row,
+// for kGatherRows rows a block's width apart, all their loads in flight at once.
 // ---------------------------------------------------------------------------
+constexpr int kGatherRows = 4;
+
 struct GatherArgs {
     Kv4Cache c;
     const int* table;
@@ -154,13 +169,14 @@ struct GatherArgs {
     float k_scale, v_scale;
 };
 
+// s (n - 8) of eight codes, exact in 32 bits: 2^23 + n as a float is n under the exponent of 2^23
 template <typename T>
 __device__ __forceinline__ uint4 expand8(uint32_t codes, float s) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = (float)(int)((codes >> (8 * i)) & 15u) - 8.0f;
-        const float hi = (float)(int)((codes >> (8 * i + 4)) & 15u) - 8.0f;
+        const float lo = __uint_as_float(((codes >> (8 * i)) & 15u) | 0x4B000000u) - 8388616.0f;
+        const float hi = __uint_as_float(((codes >> (8 * i + 4)) & 15u) | 0x4B000000u) - 8388616.0f;
         w[i] = from_float2<T>(lo * s, hi * s);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -170,40 +186,52 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a) {
     constexpr int NG = D / kKv4Group;
     constexpr int U = D / 8;
-    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const int j = (int)(idx / U), u = (int)(idx % U);
-    const int h = blockIdx.y, b = blockIdx.z;
+    const int u = threadIdx.x % U;
     const int i = u / 4, c = u % 4;
     const bool odd = i & 1;
-    const bool in = idx < (long long)a.N * U;
-    uint32_t ck = 0, cv = 0;
-    float sk = 0.f, sv = 0.f;  // a row behind the sequence, or on a page outside the pool, is zeros
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int first = (int)blockIdx.x * (kGatherRows * (kThreads / U)) + (int)threadIdx.x / U;
     const int ps = a.c.page_size;
-    if (in && j < __ldg(a.lens + b) && j / ps < a.max_pages) {
-        const int page = __ldg(a.table + (size_t)b * a.max_pages + j / ps);
-        if (page >= 0 && page < a.c.num_pages) {
-            const size_t at = ((size_t)page * a.Hkv + h) * ps + j % ps;
-            ck = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_codes + at * (D / 2)) + c * NG + i);
-            const int vword = NG > 1 ? ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2 : c;
-            cv = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_codes + at * (D / 2)) + vword);
-            sk = e4m3_value(__ldg(a.c.k_scales + at * NG + i)) * a.k_scale;
-            sv = e4m3_value(__ldg(a.c.v_scales + at * NG + i)) * a.v_scale;
+    const int vword = NG > 1 ? ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2 : c;
+    const int L = min(__ldg(a.lens + b), a.N);
+    int page[kGatherRows];
+#pragma unroll
+    for (int x = 0; x < kGatherRows; ++x) {
+        const int j = first + x * (kThreads / U);
+        page[x] = j < L && j / ps < a.max_pages ? __ldg(a.table + (size_t)b * a.max_pages + j / ps) : -1;
+        if (page[x] >= a.c.num_pages) page[x] = -1;
+    }
+    // a row behind the sequence, or on a page outside the pool, is zeros
+    uint32_t ck[kGatherRows], cv[kGatherRows], sk[kGatherRows], sv[kGatherRows];
+#pragma unroll
+    for (int x = 0; x < kGatherRows; ++x) {
+        ck[x] = cv[x] = sk[x] = sv[x] = 0;
+        if (page[x] >= 0) {
+            const size_t at = ((size_t)page[x] * a.Hkv + h) * ps + (first + x * (kThreads / U)) % ps;
+            ck[x] = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_codes + at * (D / 2)) + c * NG + i);
+            cv[x] = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_codes + at * (D / 2)) + vword);
+            sk[x] = __ldg(a.c.k_scales + at * NG + i);
+            sv[x] = __ldg(a.c.v_scales + at * NG + i);
         }
     }
-    if (NG > 1) {  // the inverse of the append kernel's trade
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? (cv & 0xFFFFu) : (cv >> 16), 4);
-        cv = odd ? (got | (cv & 0xFFFF0000u)) : ((cv & 0xFFFFu) | (got << 16));
+#pragma unroll
+    for (int x = 0; x < kGatherRows; ++x) {
+        if (NG > 1) {  // the inverse of the append kernel's trade
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? (cv[x] & 0xFFFFu) : (cv[x] >> 16), 4);
+            cv[x] = odd ? (got | (cv[x] & 0xFFFF0000u)) : ((cv[x] & 0xFFFFu) | (got << 16));
+        }
+        const int j = first + x * (kThreads / U);
+        if (j >= a.N) continue;
+        const size_t out = (((size_t)b * a.Hkv + h) * a.N + j) * U + u;
+        reinterpret_cast<uint4*>(a.k)[out] = expand8<T>(ck[x], e4m3_value(sk[x]) * a.k_scale);
+        reinterpret_cast<uint4*>(a.v)[out] = expand8<T>(cv[x], e4m3_value(sv[x]) * a.v_scale);
     }
-    if (!in) return;
-    const size_t out = (((size_t)b * a.Hkv + h) * a.N + j) * U + u;
-    reinterpret_cast<uint4*>(a.k)[out] = expand8<T>(ck, sk);
-    reinterpret_cast<uint4*>(a.v)[out] = expand8<T>(cv, sv);
 }
 
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
-    const long long n = (long long)a.T * a.Hkv * (D / 8);
-    const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads);
+    const long long rows = (long long)a.T * a.Hkv, per = kAppendRows * (kThreads / (D / 8));
+    const unsigned grid = (unsigned)((rows + per - 1) / per);
     switch (D) {
         case 32: kv4_append_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
         case 64: kv4_append_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;
@@ -214,8 +242,8 @@ cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_gather(const GatherArgs& a, int B, int D, cudaStream_t s) {
-    const long long n = (long long)a.N * (D / 8);
-    const dim3 grid((unsigned)((n + kThreads - 1) / kThreads), (unsigned)a.Hkv, (unsigned)B);
+    const int per = kGatherRows * (kThreads / (D / 8));
+    const dim3 grid((unsigned)(((long long)a.N + per - 1) / per), (unsigned)a.Hkv, (unsigned)B);
     switch (D) {
         case 32: kv4_gather_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
         case 64: kv4_gather_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;

@@ -66,7 +66,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;   // keys of a tile, 16 per warp
 constexpr int kStages = 4;           // tiles in a warp's ring, two pairs
 constexpr int ROWS = 8;              // query rows of a team
-constexpr int kPartCost = 3;         // what a segment costs beside its tiles, in tiles (see Part)
+constexpr int kPartCost = 6;         // what a segment costs beside its tiles, in tiles (see Part)
 constexpr int kMinTiles = 4;         // a team's range is at least this long while there are teams to spare
 // Probabilities are kept times 2^kPShift relative to a score that the largest one may exceed by kPSlack (base 2): times
 // a scale of at most 448 they stay below 2^7 * 448 = 57344.
@@ -238,8 +238,8 @@ struct Shares {
 // The part of a segment that a block is at: tiles [t0, t1) of it. Kept in shared memory, so that what the warps need
 // only before and after a part's tiles takes no registers while they run through them.
 // Every segment counts kPartCost more than its tiles when the tiles are shared out, in front of its first one: that is
-// what a block spends on starting its copies, its query and its sums (measured: with shares by tiles alone, 64 ragged
-// sequences' blocks of ten short segments ended at 150 us and the others at 113).
+// what a team spends on starting its copies, its query and its sums. 64 ragged sequences of up to 16384 keys: 129 us
+// at a cost of 3, 122 at 5, 123 at 7; 256 of up to 1000 keys, D = 64: 32, 28.8 and 28.1.
 struct Part {
     long long u, rem;      // before the part: of all, and of its sequence
     int b, L, hz, t0, t1;  // t0 == t1: no part
