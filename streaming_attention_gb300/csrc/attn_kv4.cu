@@ -65,40 +65,62 @@ struct AppendArgs {
     float k_inv, v_inv;  // 1 / descale (a power of two)
 };
 
+// max |x| of the 8 elements of four words, two halves at a time
+template <typename T2>
+__device__ __forceinline__ T2 as_pair(uint32_t w) {
+    return *reinterpret_cast<const T2*>(&w);
+}
+template <typename T>
+__device__ __forceinline__ float largest(const uint32_t (&w)[4]);
+template <>
+__device__ __forceinline__ float largest<__nv_bfloat16>(const uint32_t (&w)[4]) {
+    using P = __nv_bfloat162;
+    const P m = __hmax2(__hmax2(__habs2(as_pair<P>(w[0])), __habs2(as_pair<P>(w[1]))),
+                        __hmax2(__habs2(as_pair<P>(w[2])), __habs2(as_pair<P>(w[3]))));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+template <>
+__device__ __forceinline__ float largest<__half>(const uint32_t (&w)[4]) {
+    using P = __half2;
+    const P m = __hmax2(__hmax2(__habs2(as_pair<P>(w[0])), __habs2(as_pair<P>(w[1]))),
+                        __hmax2(__habs2(as_pair<P>(w[2])), __habs2(as_pair<P>(w[3]))));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
 // 8 elements -> 8 codes in one word (lowest element in the lowest bits) and the
-// group's scale byte. Exact with respect to the format's definition: the quotient
-// x / s is taken as x * r with r = (1 / s)(1 + 2^-16). A tie between two codes is
-// pushed to the larger magnitude (r exceeds 1 / s by 2^-16 and rounding errs by
-// less than 2^-22), and nothing else crosses a border: x has 11 significant bits
-// and s times a border 8, so a quotient that is not on a border is at least 2^-11
-// of it away.
+// group's scale byte. Exact with respect to the format's definition:
+//   max / 7.5 is one product and one correction by its remainder, which leaves a
+//   quotient that lies on a border between two scales (5 bits) exactly there, and
+//   others (the maximum has 11 bits) on their side of it.
+//   x / s is x * r with r = (1 / s)(1 + 2^-16). A tie between two codes is pushed to
+//   the larger magnitude (r exceeds 1 / s by 2^-16, rounding errs by less than
+//   2^-21), and nothing else crosses a border: x has 11 significant bits and s times
+//   a border 8, so a quotient that is not on a border is at least 2^-11 of it away.
+// inv, 1 / descale, is a power of two: x is scaled by way of r.
 template <typename T>
 __device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_t* scale) {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    float x[8];
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 t = to_float2<T>(words[i]);
-        x[2 * i] = t.x * inv;
-        x[2 * i + 1] = t.y * inv;
-        top = fmaxf(top, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-    }
+    float top = largest<T>(words);
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // division rounds correctly, so a maximum that lies on a border between two scales is seen there
-    const uint32_t s = __nv_cvt_float_to_fp8(__fdiv_rn(top, 7.5f), __NV_SATFINITE, __NV_E4M3);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * inv;
+    const float q = top * (1.0f / 7.5f);
+    const uint32_t s =
+        __nv_cvt_float_to_fp8(fmaf(fmaf(-7.5f, q, top), 1.0f / 7.5f, q), __NV_SATFINITE, __NV_E4M3);
     const float sf = e4m3_value(s);
-    const float r = sf > 0.f ? __fdiv_rn(1.0f, sf) * (1.0f + 0x1p-16f) : 0.f;
+    const float r = sf > 0.f ? __fdividef(1.0f, sf) * (1.0f + 0x1p-16f) * inv : 0.f;
+    // 1.5 * 2^23 + 8 + n has 8 + n in its low bits, under bits that are always the same
+    constexpr float kMagic = 12582920.0f;
+    constexpr uint32_t kUnder = 0x4B400000u * 0x11111111u;
     uint32_t codes = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = fminf(fmaxf(x[i] * r, -8.0f), 7.0f);
-        // 1.5 * 2^23 + 8: the integer part of the sum sits in its low bits
-        codes |= (__float_as_uint(t + 12582920.0f) & 15u) << (4 * i);
+    for (int i = 3; i >= 0; --i) {
+        const float2 x = to_float2<T>(words[i]);
+        const float hi = fminf(fmaxf(x.y * r, -8.0f), 7.0f) + kMagic, lo = fminf(fmaxf(x.x * r, -8.0f), 7.0f) + kMagic;
+        codes = codes * 16 + __float_as_uint(hi);
+        codes = codes * 16 + __float_as_uint(lo);
     }
     *scale = s;
-    return codes;
+    return codes - kUnder;
 }
 
 template <typename T, int D>

@@ -9,7 +9,7 @@
 // the batch, first_b = sum need its pages in the free list. The sums run over
 // at most a few thousand requests, which one block does in a microsecond or
 // two, so there is one launch: every block computes them for itself, a chunk of
-// one request per thread at a time, and takes its share of the chunk's rows and
+// one or two requests per thread at a time, and takes its share of the chunk's rows and
 // pages, whose request it finds by bisection in shared memory. No block reads a
 // table entry that another one writes: entries below old_b are only read, the
 // others only written (their page is computed from the free list instead).
@@ -23,8 +23,8 @@
 namespace attn {
 namespace {
 
-constexpr int kPlanMost = 1024;  // threads of a block, and requests of a chunk
-constexpr int64_t kI32Max = 2147483647LL;
+constexpr int kPlanMost = 2048;  // requests of a chunk, at most
+constexpr long long kI32Max = 2147483647LL;
 
 struct PlanArgs {
     const int* cached;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void block_sums(long long& x, long long& y, longlong2
 }
 
 // The last entry e of the ascending a[0..n) with a[e] <= x; a[0] <= x.
-__device__ __forceinline__ int last_not_above(const long long* a, int n, long long x) {
+__device__ __forceinline__ int last_not_above(const int* a, int n, int x) {
     int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -87,62 +87,83 @@ __device__ __forceinline__ int last_not_above(const long long* a, int n, long lo
     return lo;
 }
 
-template <int N>
+// Pages of x keys, x below 2^32, at most `most`.
+__device__ __forceinline__ int pages_of(uint32_t x, uint32_t page_size, int most) {
+    const uint32_t n = x / page_size + (x % page_size != 0);
+    return (int)min(n, (uint32_t)most);
+}
+
+// N threads, K requests of a chunk to a thread.
+template <int N, int K>
 __global__ void __launch_bounds__(N) page_plan_kernel(const PlanArgs a) {
-    __shared__ long long start[N], first[N];
+    // a request's first row of the batch and first page of the free list (2^31 - 1 for all behind that), its keys in
+    // the cache and its pages
+    __shared__ int start[N * K], first[N * K], have[N * K], old[N * K];
     __shared__ longlong2 part[N / 32];
-    __shared__ int have[N], old[N];
     const long long mine = (long long)blockIdx.x * N + threadIdx.x;
     const long long step = (long long)gridDim.x * N;
     long long rows = 0, pages = 0;  // of the requests before this chunk
     long long lost = 0;             // rows without a place of this thread's requests
-    int c32 = (int)threadIdx.x < a.B ? __ldg(a.cached + threadIdx.x) : 0;
-    int n32 = (int)threadIdx.x < a.B ? __ldg(a.fresh + threadIdx.x) : 0;
-    for (int b0 = 0; b0 < a.B; b0 += N) {
-        const int b = b0 + threadIdx.x;
-        const long long c = max(c32, 0), n = max(n32, 0), ps = a.page_size;
-        if (b0 + N < a.B) {  // the next chunk's lengths are on their way while this one is worked on
-            c32 = b + N < a.B ? __ldg(a.cached + b + N) : 0;
-            n32 = b + N < a.B ? __ldg(a.fresh + b + N) : 0;
+    for (int b0 = 0; b0 < a.B; b0 += N * K) {
+        const int b = b0 + (int)threadIdx.x * K;
+        uint32_t c[K], n[K];
+        int had[K], need[K];
+        long long s = 0, f = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            c[k] = b + k < a.B ? (uint32_t)max(__ldg(a.cached + b + k), 0) : 0;
+            n[k] = b + k < a.B ? (uint32_t)max(__ldg(a.fresh + b + k), 0) : 0;
         }
-        const int had = (int)min((c + ps - 1) / ps, (long long)a.max_pages);
-        const int need = (int)min((c + n + ps - 1) / ps, (long long)a.max_pages) - had;
-        long long s = n, f = need, chunk_rows, chunk_pages;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            had[k] = pages_of(c[k], a.page_size, a.max_pages);
+            need[k] = pages_of(c[k] + n[k], a.page_size, a.max_pages) - had[k];
+            s += n[k];
+            f += need[k];
+        }
+        long long chunk_rows, chunk_pages;
         block_sums<N>(s, f, part, &chunk_rows, &chunk_pages);
         s += rows;
         f += pages;
-        start[threadIdx.x] = s;
-        first[threadIdx.x] = f;
-        have[threadIdx.x] = (int)c;
-        old[threadIdx.x] = had;
-        if (blockIdx.x == 0 && b < a.B) {
-            a.seq_lens[b] = saturate(c + n);
-            a.row_starts[b] = saturate(s);
-            // kept: the rows on pages that this request could get, and not behind slot_map
-            const long long got = had + min(max(a.num_free - f, 0LL), (long long)need);
-            lost += n - min(max(min(c + n, got * ps) - c, 0LL), max(a.num_rows - s, 0LL));
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int e = (int)threadIdx.x * K + k;
+            start[e] = saturate(s);
+            first[e] = saturate(f);
+            have[e] = (int)c[k];
+            old[e] = had[k];
+            if (blockIdx.x == 0 && b + k < a.B) {
+                const long long len = (long long)c[k] + n[k];
+                a.seq_lens[b + k] = saturate(len);
+                a.row_starts[b + k] = saturate(s);
+                // kept: the rows on pages that this request could get, and not behind slot_map
+                const long long got = had[k] + min(max(a.num_free - f, 0LL), (long long)need[k]);
+                lost += n[k] - min(max(min(len, got * a.page_size) - c[k], 0LL), max(a.num_rows - s, 0LL));
+            }
+            s += n[k];
+            f += need[k];
         }
         __syncthreads();
-        const int live = min(a.B - b0, N);
-        for (long long x = pages + mine; x < pages + chunk_pages; x += step) {
-            const int e = last_not_above(first, live, x);
-            const long long k = old[e] + (x - first[e]);
+        const int live = min(a.B - b0, N * K);
+        const long long page_end = min(pages + chunk_pages, kI32Max);
+        for (long long x = pages + mine; x < page_end; x += step) {
+            const int e = last_not_above(first, live, (int)x);
+            const int k = old[e] + ((int)x - first[e]);
             a.table[(size_t)(b0 + e) * a.max_pages + k] = x < a.num_free ? __ldg(a.free_pages + x) : -1;
         }
-        const long long end = min(rows + chunk_rows, (long long)a.num_rows);
-        for (long long r = rows + mine; r < end; r += step) {
-            const int e = last_not_above(start, live, r);
-            const long long pos = have[e] + (r - start[e]);
-            // positions pass 32 bits only where no page is left
-            const int k = pos <= kI32Max ? (int)((uint32_t)pos / (uint32_t)a.page_size) : a.max_pages;
+        const long long row_end = min(rows + chunk_rows, (long long)a.num_rows);
+        for (long long r = rows + mine; r < row_end; r += step) {
+            const int e = last_not_above(start, live, (int)r);
+            const uint32_t pos = (uint32_t)have[e] + (uint32_t)((int)r - start[e]);
+            const uint32_t k = pos / (uint32_t)a.page_size;
             int page = -1;
-            if (k < old[e]) {
+            if (k < (uint32_t)old[e]) {
                 page = a.table[(size_t)(b0 + e) * a.max_pages + k];
-            } else if (k < a.max_pages) {
-                const long long x = first[e] + (k - old[e]);
+            } else if (k < (uint32_t)a.max_pages) {
+                const long long x = (long long)first[e] + (k - (uint32_t)old[e]);
                 if (x < a.num_free) page = __ldg(a.free_pages + x);
             }
-            const long long slot = (long long)page * a.page_size + ((uint32_t)pos - (uint32_t)k * (uint32_t)a.page_size);
+            const long long slot = (long long)page * a.page_size + (pos - k * (uint32_t)a.page_size);
             a.slots[r] = page >= 0 && slot <= kI32Max ? (int)slot : -1;
         }
         rows += chunk_rows;
@@ -198,19 +219,19 @@ int attn_page_plan(const int* cached_lens, const int* new_lens, const int* free_
     }
     const PlanArgs a{cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats,
                      B, page_size, max_pages, num_free, num_rows};
-    // one row per thread, on at most one block per SM. Few requests take smaller blocks, whose sums are quicker (64
-    // requests); many take larger ones, and so fewer chunks one after the other (2000).
+    // one row per thread, on at most one block per SM. Few requests take smaller blocks, whose sums are quicker; many take
+    // larger ones, and so fewer chunks one after the other.
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
-    const int threads = B <= 256 ? 256 : kPlanMost;
+    const int threads = B <= 256 ? 256 : 1024;
     int64_t grid = ((int64_t)(num_rows > B ? num_rows : B) + threads - 1) / threads;
     if (grid > sms) grid = sms;
     if (grid < 1) grid = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (threads == 256)
-        page_plan_kernel<256><<<(unsigned)grid, 256, 0, s>>>(a);
+        page_plan_kernel<256, 1><<<(unsigned)grid, 256, 0, s>>>(a);
     else
-        page_plan_kernel<kPlanMost><<<(unsigned)grid, kPlanMost, 0, s>>>(a);
+        page_plan_kernel<1024, kPlanMost / 1024><<<(unsigned)grid, 1024, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
