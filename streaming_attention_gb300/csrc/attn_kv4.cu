@@ -93,9 +93,12 @@ __device__ __forceinline__ float largest<__half>(const uint32_t (&w)[4]) {
 //   quotient that lies on a border between two scales (5 bits) exactly there, and
 //   others (the maximum has 11 bits) on their side of it.
 //   x / s is x * r with r = (1 / s)(1 + 2^-16). A tie between two codes is pushed to
-//   the larger magnitude (r exceeds 1 / s by 2^-16, rounding errs by less than
-//   2^-21), and nothing else crosses a border: x has 11 significant bits and s times
-//   a border 8, so a quotient that is not on a border is at least 2^-11 of it away.
+//   the larger magnitude (by at least 2^-17; the roundings of what follows add up to
+//   less than 2^-19), and nothing else crosses a border: x has 11 significant bits
+//   and s times a border 8, so a quotient that is not on a border is at least 2^-11
+//   of it away.
+//   The clamp to codes 0..15 is the saturation of (x / s + 8) / 15 to 0..1, which
+//   comes with the multiply-add.
 // inv, 1 / descale, is a power of two: x is scaled by way of r.
 template <typename T>
 __device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_t* scale) {
@@ -107,17 +110,15 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_
     const uint32_t s =
         __nv_cvt_float_to_fp8(fmaf(fmaf(-7.5f, q, top), 1.0f / 7.5f, q), __NV_SATFINITE, __NV_E4M3);
     const float sf = e4m3_value(s);
-    const float r = sf > 0.f ? __fdividef(1.0f, sf) * (1.0f + 0x1p-16f) * inv : 0.f;
-    // 1.5 * 2^23 + 8 + n has 8 + n in its low bits, under bits that are always the same
-    constexpr float kMagic = 12582920.0f;
+    const float r = sf > 0.f ? __fdividef((1.0f + 0x1p-16f) / 15.0f, sf) * inv : 0.f;
+    // 1.5 * 2^23 + code has the code in its low bits, under bits that are always the same
     constexpr uint32_t kUnder = 0x4B400000u * 0x11111111u;
     uint32_t codes = 0;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
         const float2 x = to_float2<T>(words[i]);
-        const float hi = fminf(fmaxf(x.y * r, -8.0f), 7.0f) + kMagic, lo = fminf(fmaxf(x.x * r, -8.0f), 7.0f) + kMagic;
-        codes = codes * 16 + __float_as_uint(hi);
-        codes = codes * 16 + __float_as_uint(lo);
+        codes = codes * 16 + __float_as_uint(fmaf(__saturatef(fmaf(x.y, r, 8.0f / 15.0f)), 15.0f, 12582912.0f));
+        codes = codes * 16 + __float_as_uint(fmaf(__saturatef(fmaf(x.x, r, 8.0f / 15.0f)), 15.0f, 12582912.0f));
     }
     *scale = s;
     return codes - kUnder;
@@ -129,17 +130,17 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     constexpr int U = D / 8;  // threads of a row
     const int u = threadIdx.x % U;
     const int i = u / 4, c = u % 4;  // group, and which 8 of its 32 elements
-    const long long rows = (long long)a.T * a.Hkv;  // of the batch times Hkv
-    const long long first = (long long)blockIdx.x * (kAppendRows * (kThreads / U)) + threadIdx.x / U;
+    const int rows = a.T * a.Hkv;  // of the batch times Hkv: times D it fits 31 bits
+    const int first = (int)blockIdx.x * (kAppendRows * (kThreads / U)) + (int)threadIdx.x / U;
     const int ps = a.c.page_size;
     int slot[kAppendRows], head[kAppendRows];
     uint4 wk[kAppendRows], wv[kAppendRows];
 #pragma unroll
     for (int x = 0; x < kAppendRows; ++x) {
-        const long long row = first + x * (kThreads / U);
+        const int row = first + x * (kThreads / U);
         const bool in = row < rows;
-        const int t = in ? (int)(row / a.Hkv) : 0;
-        head[x] = in ? (int)(row - (long long)t * a.Hkv) : 0;
+        const int t = in ? row / a.Hkv : 0;
+        head[x] = in ? row - t * a.Hkv : 0;
         slot[x] = in ? __ldg(a.slots + t) : -1;
         if (slot[x] >= (long long)a.c.num_pages * ps) slot[x] = -1;
         // read whether the row has a slot or not: the loads need not wait for it
@@ -164,11 +165,20 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
             vbits = odd ? (got | (cv & 0xFFFF0000u)) : ((cv & 0xFFFFu) | (got << 16));
             vword = ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2;
         }
+        if (NG == 4) {  // the row's four scales into one word, of K in its first and of V in its second thread
+            uint32_t two = c == 0 ? sk : sv;
+            two |= __shfl_down_sync(0xffffffffu, two, 4) << 8;
+            two |= __shfl_down_sync(0xffffffffu, two, 8) << 16;
+            sk = two;
+        }
         if (slot[x] < 0) continue;
-        const size_t at = ((size_t)(slot[x] / ps) * a.Hkv + head[x]) * ps + slot[x] % ps;
+        const int page = slot[x] / ps;
+        const size_t at = ((size_t)page * a.Hkv + head[x]) * ps + (slot[x] - page * ps);
         reinterpret_cast<uint32_t*>(a.c.k_codes + at * (D / 2))[c * NG + i] = ck;
         reinterpret_cast<uint32_t*>(a.c.v_codes + at * (D / 2))[vword] = vbits;
-        if (c == 0) {
+        if (NG == 4) {
+            if (u < 2) reinterpret_cast<uint32_t*>(u == 0 ? a.c.k_scales : a.c.v_scales)[at] = sk;
+        } else if (c == 0) {
             a.c.k_scales[at * NG + i] = (uint8_t)sk;
             a.c.v_scales[at * NG + i] = (uint8_t)sv;
         }
@@ -191,20 +201,49 @@ struct GatherArgs {
     float k_scale, v_scale;
 };
 
-// s (n - 8) of eight codes, exact in 32 bits: 2^23 + n as a float is n under the exponent of 2^23
+// s (n - 8) of eight codes. Pairs: a byte b of the word times 0x1001 has its two nibbles at bits 0 and 16, where they
+// are small whole numbers under the exponent of 128 (BF16) or 1024 (FP16); n - 8 and its product with the scale are
+// exact in 16 bits (4 + 4 significant ones) where the scale times the factor is a normal number of T, which the caller
+// has seen to. 5 operations a pair; in 32 bits, for other factors, 10.
 template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+    static constexpr uint32_t kBase = 0x43004300u;  // 128 + n
+    static __device__ __forceinline__ uint32_t value(uint32_t h, uint32_t s2) {
+        const __nv_bfloat162 x = __hsub2(as_pair<__nv_bfloat162>(h), __floats2bfloat162_rn(136.f, 136.f));
+        const __nv_bfloat162 y = __hmul2(x, as_pair<__nv_bfloat162>(s2));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+};
+template <>
+struct Pair<__half> {
+    static constexpr uint32_t kBase = 0x64006400u;  // 1024 + n
+    static __device__ __forceinline__ uint32_t value(uint32_t h, uint32_t s2) {
+        const __half2 x = __hsub2(as_pair<__half2>(h), __floats2half2_rn(1032.f, 1032.f));
+        const __half2 y = __hmul2(x, as_pair<__half2>(s2));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+};
+template <typename T, bool kNarrow>
 __device__ __forceinline__ uint4 expand8(uint32_t codes, float s) {
     uint32_t w[4];
+    const uint32_t s2 = from_float2<T>(s, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(((codes >> (8 * i)) & 15u) | 0x4B000000u) - 8388616.0f;
-        const float hi = __uint_as_float(((codes >> (8 * i + 4)) & 15u) | 0x4B000000u) - 8388616.0f;
-        w[i] = from_float2<T>(lo * s, hi * s);
+        if constexpr (kNarrow) {
+            const uint32_t two = __byte_perm(codes, 0, 0x4440 | i) * 0x1001u;
+            w[i] = Pair<T>::value((two & 0x000F000Fu) | Pair<T>::kBase, s2);
+        } else {
+            const float lo = __uint_as_float(((codes >> (8 * i)) & 15u) | 0x4B000000u) - 8388616.0f;
+            const float hi = __uint_as_float(((codes >> (8 * i + 4)) & 15u) | 0x4B000000u) - 8388616.0f;
+            w[i] = from_float2<T>(lo * s, hi * s);
+        }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kNarrow>
 __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a) {
     constexpr int NG = D / kKv4Group;
     constexpr int U = D / 8;
@@ -245,8 +284,8 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a
         const int j = first + x * (kThreads / U);
         if (j >= a.N) continue;
         const size_t out = (((size_t)b * a.Hkv + h) * a.N + j) * U + u;
-        reinterpret_cast<uint4*>(a.k)[out] = expand8<T>(ck[x], e4m3_value(sk[x]) * a.k_scale);
-        reinterpret_cast<uint4*>(a.v)[out] = expand8<T>(cv[x], e4m3_value(sv[x]) * a.v_scale);
+        reinterpret_cast<uint4*>(a.k)[out] = expand8<T, kNarrow>(ck[x], e4m3_value(sk[x]) * a.k_scale);
+        reinterpret_cast<uint4*>(a.v)[out] = expand8<T, kNarrow>(cv[x], e4m3_value(sv[x]) * a.v_scale);
     }
 }
 
@@ -262,14 +301,35 @@ cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, int D>
+void launch_gather_d(const GatherArgs& a, dim3 grid, bool narrow, cudaStream_t s) {
+    if (narrow)
+        kv4_gather_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
+    else
+        kv4_gather_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
+}
+
+// Whether every scale (2^-9 .. 448) times the factor is a normal number of T.
+template <typename T>
+bool narrow_factor(float f);
+template <>
+bool narrow_factor<__half>(float f) {
+    return f >= 0x1p-5f && f <= 0x1p7f;
+}
+template <>
+bool narrow_factor<__nv_bfloat16>(float f) {
+    return f >= 0x1p-117f && f <= 0x1p119f;
+}
+
 template <typename T>
 cudaError_t launch_gather(const GatherArgs& a, int B, int D, cudaStream_t s) {
     const int per = kGatherRows * (kThreads / (D / 8));
     const dim3 grid((unsigned)(((long long)a.N + per - 1) / per), (unsigned)a.Hkv, (unsigned)B);
+    const bool narrow = narrow_factor<T>(a.k_scale) && narrow_factor<T>(a.v_scale);
     switch (D) {
-        case 32: kv4_gather_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
-        case 64: kv4_gather_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;
-        default: kv4_gather_kernel<T, 128><<<grid, kThreads, 0, s>>>(a); break;
+        case 32: launch_gather_d<T, 32>(a, grid, narrow, s); break;
+        case 64: launch_gather_d<T, 64>(a, grid, narrow, s); break;
+        default: launch_gather_d<T, 128>(a, grid, narrow, s); break;
     }
     return cudaGetLastError();
 }
