@@ -42,6 +42,14 @@ __device__ __forceinline__ uint32_t from_float2<__half>(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
+// log2 of a power of two, else -1
+int shift_of(int ps) {
+    int n = 0;
+    while ((1 << n) < ps && n < 30) ++n;
+    return (1 << n) == ps ? n : -1;
+}
+__device__ __forceinline__ int page_index(int x, int ps, int shift) { return shift >= 0 ? x >> shift : x / ps; }
+
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
 }
@@ -61,7 +69,7 @@ struct AppendArgs {
     const int* slots;
     Kv4Cache c;
     long long k_stride, v_stride;  // elements from one row of the batch to the next
-    int T, Hkv;
+    int T, Hkv, ps_shift;
     float k_inv, v_inv;  // 1 / descale (a power of two)
 };
 
@@ -130,24 +138,23 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     constexpr int U = D / 8;  // threads of a row
     const int u = threadIdx.x % U;
     const int i = u / 4, c = u % 4;  // group, and which 8 of its 32 elements
-    const int rows = a.T * a.Hkv;  // of the batch times Hkv: times D it fits 31 bits
-    const int first = (int)blockIdx.x * (kAppendRows * (kThreads / U)) + (int)threadIdx.x / U;
+    // a block takes one head of consecutive rows, whose keys mostly lie side by side on a page
+    const int h = (int)(blockIdx.x % a.Hkv);
+    const int first = (int)(blockIdx.x / a.Hkv) * (kAppendRows * (kThreads / U)) + (int)threadIdx.x / U;
     const int ps = a.c.page_size;
-    int slot[kAppendRows], head[kAppendRows];
+    int slot[kAppendRows];
     uint4 wk[kAppendRows], wv[kAppendRows];
 #pragma unroll
     for (int x = 0; x < kAppendRows; ++x) {
-        const int row = first + x * (kThreads / U);
-        const bool in = row < rows;
-        const int t = in ? row / a.Hkv : 0;
-        head[x] = in ? row - t * a.Hkv : 0;
+        const int t = first + x * (kThreads / U);
+        const bool in = t < a.T;
         slot[x] = in ? __ldg(a.slots + t) : -1;
         if (slot[x] >= (long long)a.c.num_pages * ps) slot[x] = -1;
         // read whether the row has a slot or not: the loads need not wait for it
         wk[x] = wv[x] = make_uint4(0, 0, 0, 0);
         if (in) {
-            wk[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + head[x] * D + u * 8));
-            wv[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + head[x] * D + u * 8));
+            wk[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + h * D + u * 8));
+            wv[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + h * D + u * 8));
         }
     }
 #pragma unroll
@@ -172,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
             sk = two;
         }
         if (slot[x] < 0) continue;
-        const int page = slot[x] / ps;
-        const size_t at = ((size_t)page * a.Hkv + head[x]) * ps + (slot[x] - page * ps);
+        const int page = page_index(slot[x], ps, a.ps_shift);
+        const size_t at = ((size_t)page * a.Hkv + h) * ps + (slot[x] - page * ps);
         reinterpret_cast<uint32_t*>(a.c.k_codes + at * (D / 2))[c * NG + i] = ck;
         reinterpret_cast<uint32_t*>(a.c.v_codes + at * (D / 2))[vword] = vbits;
         if (NG == 4) {
@@ -197,7 +204,7 @@ struct GatherArgs {
     const int* lens;
     void* k;
     void* v;
-    int Hkv, N, max_pages;
+    int Hkv, N, max_pages, ps_shift;
     float k_scale, v_scale;
 };
 
@@ -259,7 +266,8 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a
 #pragma unroll
     for (int x = 0; x < kGatherRows; ++x) {
         const int j = first + x * (kThreads / U);
-        page[x] = j < L && j / ps < a.max_pages ? __ldg(a.table + (size_t)b * a.max_pages + j / ps) : -1;
+        const int n = page_index(j, ps, a.ps_shift);
+        page[x] = j < L && n < a.max_pages ? __ldg(a.table + (size_t)b * a.max_pages + n) : -1;
         if (page[x] >= a.c.num_pages) page[x] = -1;
     }
     // a row behind the sequence, or on a page outside the pool, is zeros
@@ -268,7 +276,8 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a
     for (int x = 0; x < kGatherRows; ++x) {
         ck[x] = cv[x] = sk[x] = sv[x] = 0;
         if (page[x] >= 0) {
-            const size_t at = ((size_t)page[x] * a.Hkv + h) * ps + (first + x * (kThreads / U)) % ps;
+            const int j = first + x * (kThreads / U);
+            const size_t at = ((size_t)page[x] * a.Hkv + h) * ps + (j - page_index(j, ps, a.ps_shift) * ps);
             ck[x] = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_codes + at * (D / 2)) + c * NG + i);
             cv[x] = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_codes + at * (D / 2)) + vword);
             sk[x] = __ldg(a.c.k_scales + at * NG + i);
@@ -291,8 +300,8 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a
 
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
-    const long long rows = (long long)a.T * a.Hkv, per = kAppendRows * (kThreads / (D / 8));
-    const unsigned grid = (unsigned)((rows + per - 1) / per);
+    const int per = kAppendRows * (kThreads / (D / 8));
+    const unsigned grid = (unsigned)(((long long)a.T + per - 1) / per * a.Hkv);
     switch (D) {
         case 32: kv4_append_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
         case 64: kv4_append_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;
@@ -371,7 +380,7 @@ int attn_kv4_append(const void* k, const void* v, const int* slot_map, void* k_c
     if (!k || !v || !slot_map) return ATTN_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4) || (T > 1 && (k_stride % 8 || v_stride % 8)))
         return ATTN_ERR_ALIGN;
-    const AppendArgs a{k, v, slot_map, c, k_stride, v_stride, T, Hkv, 1.0f / k_descale, 1.0f / v_descale};
+    const AppendArgs a{k, v, slot_map, c, k_stride, v_stride, T, Hkv, shift_of(page_size), 1.0f / k_descale, 1.0f / v_descale};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(dtype == ATTN_BF16 ? launch_append<__nv_bfloat16>(a, D, s) : launch_append<__half>(a, D, s));
 }
@@ -393,7 +402,7 @@ int attn_kv4_gather(const void* k_codes, const void* k_scales, const void* v_cod
     if ((int64_t)B * Hkv * N == 0) return ATTN_OK;
     if (!k || !v || !seq_lens || (max_pages > 0 && !block_table)) return ATTN_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq_lens, 4) || !aligned(block_table, 4)) return ATTN_ERR_ALIGN;
-    const GatherArgs a{c, block_table, seq_lens, k, v, Hkv, N, max_pages, k_descale, v_descale};
+    const GatherArgs a{c, block_table, seq_lens, k, v, Hkv, N, max_pages, shift_of(page_size), k_descale, v_descale};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(dtype == ATTN_BF16 ? launch_gather<__nv_bfloat16>(a, B, D, s)
                                           : launch_gather<__half>(a, B, D, s));
