@@ -401,35 +401,70 @@ def kv4_cache(num_pages, Hkv, page_size, D, device="cuda"):
     return pools() + pools()
 
 
-def _on_current_device(*tensors) -> None:
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors are on {dev} and {t.device}: one device is wanted")
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}: they must be on the current CUDA device")
+# These calls are small on the GPU (a few microseconds), so what surrounds them in Python is kept short: the stream is
+# taken as a number and pointers are passed as numbers.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _int32(**tensors) -> None:
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(device)
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _address(t: torch.Tensor):
+    return t.data_ptr() if t.numel() else None
+
+
+def _device_of(first: torch.Tensor, *others) -> int:
+    """The current CUDA device, where all the tensors have to be."""
+    dev = first.get_device()
+    for t in others:
+        if t.get_device() != dev:
+            raise ValueError(f"tensors are on {first.device} and {t.device}: one device is wanted")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}: they must be on the current CUDA device")
+    return dev
+
+
+def _int32(name: str, t: torch.Tensor) -> None:
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor")
 
 
 def _kv4_dims(k_codes, k_scales, v_codes, v_scales):
-    if k_codes.dim() != 4 or k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
+    shape = k_codes.shape
+    if len(shape) != 4 or k_codes.dtype is not torch.uint8 or v_codes.dtype is not torch.uint8:
         raise ValueError("codes are uint8 [num_pages, Hkv, page_size, D/2]")
-    num_pages, Hkv, page_size, half = k_codes.shape
-    if v_codes.shape != k_codes.shape:
+    num_pages, Hkv, page_size, half = shape
+    if v_codes.shape != shape:
         raise ValueError("k_codes and v_codes must have one shape")
     want = (num_pages, Hkv, page_size, half // 16)
     for t in (k_scales, v_scales):
-        if tuple(t.shape) != want or t.dtype != torch.float8_e4m3fn:
+        if t.dtype is not torch.float8_e4m3fn or t.shape != want:
             raise ValueError(f"scales are float8_e4m3fn [num_pages, Hkv, page_size, D/32] = {want}")
-    for t in (k_codes, k_scales, v_codes, v_scales):
-        if not t.is_contiguous():
-            raise ValueError("the cache's tensors must be contiguous")
+    if not (k_codes.is_contiguous() and k_scales.is_contiguous() and v_codes.is_contiguous()
+            and v_scales.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
     return num_pages, Hkv, page_size, 2 * half
+
+
+def _one_dtype(what: str, x: torch.Tensor, y: torch.Tensor) -> int:
+    if x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16:
+        return ATTN_BF16
+    if x.dtype is torch.float16 and y.dtype is torch.float16:
+        return ATTN_FP16
+    raise ValueError(f"{what} must share one dtype, bfloat16 or float16")
+
+
+def _tables(block_table, seq_lens, B: int) -> int:
+    _int32("block_table", block_table)
+    _int32("seq_lens", seq_lens)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    return block_table.shape[1]
 
 
 def attn_page_plan(cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats, page_size,
@@ -437,20 +472,25 @@ def attn_page_plan(cached_lens, new_lens, free_pages, block_table, seq_lens, row
     """C-ABI ``attn_page_plan``: takes pages for the new keys of every request (``block_table``, updated in
     place) and writes ``seq_lens`` [B], ``row_starts`` [B+1], ``slot_map`` [rows, padding included] and
     ``stats`` [3]: rows, pages taken, rows without a slot. All int32 device tensors."""
-    _int32(cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages, block_table=block_table,
-           seq_lens=seq_lens, row_starts=row_starts, slot_map=slot_map, stats=stats)
+    _int32("cached_lens", cached_lens)
+    _int32("new_lens", new_lens)
+    _int32("free_pages", free_pages)
+    _int32("row_starts", row_starts)
+    _int32("slot_map", slot_map)
+    _int32("stats", stats)
     B = cached_lens.numel()
-    if cached_lens.dim() != 1 or new_lens.shape != (B,) or seq_lens.shape != (B,) or row_starts.shape != (B + 1,):
+    if cached_lens.dim() != 1 or new_lens.shape != (B,) or row_starts.shape != (B + 1,):
         raise ValueError("cached_lens, new_lens and seq_lens are [B], row_starts is [B+1]")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages]")
+    max_pages = _tables(block_table, seq_lens, B)
     if free_pages.dim() != 1 or slot_map.dim() != 1 or stats.shape != (3,):
         raise ValueError("free_pages and slot_map are one-dimensional, stats is [3]")
-    _on_current_device(stats, cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map)
-    st = lib().attn_page_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_pages), _ptr(block_table), _ptr(seq_lens),
-                              _ptr(row_starts), _ptr(slot_map), _ptr(stats), B, int(page_size), block_table.shape[1],
-                              free_pages.numel(), slot_map.numel(), _stream(stream))
-    _check(st, "attn_page_plan")
+    dev = _device_of(stats, cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map)
+    st = (_lib or lib()).attn_page_plan(
+        _address(cached_lens), _address(new_lens), _address(free_pages), _address(block_table), _address(seq_lens),
+        row_starts.data_ptr(), _address(slot_map), stats.data_ptr(), B, int(page_size), max_pages, free_pages.numel(),
+        slot_map.numel(), _raw_stream(stream, dev))
+    if st:
+        _check(st, "attn_page_plan")
 
 
 def attn_kv4_append(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, k_descale=1.0, v_descale=1.0,
@@ -458,22 +498,23 @@ def attn_kv4_append(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, k_desc
     """C-ABI ``attn_kv4_append``: quantizes the rows of ``k`` and ``v`` [T, Hkv, D] (BF16 or FP16; heads
     contiguous, rows any distance apart) into the cache at ``slot_map`` [T] (-1 skips a row)."""
     num_pages, Hkv, page_size, D = _kv4_dims(k_codes, k_scales, v_codes, v_scales)
-    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, D) or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != D or v.shape != shape:
         raise ValueError(f"k and v must be [T, {Hkv}, {D}]")
-    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
-        raise ValueError("k and v must share one dtype, bfloat16 or float16")
-    for t in (k, v):
-        if t.numel() and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D)):
-            raise ValueError("the elements of a head and the heads of a row must be contiguous")
-    T = k.shape[0]
-    _int32(slot_map=slot_map)
+    dtype = _one_dtype("k and v", k, v)
+    T, ks, vs = shape[0], k.stride(), v.stride()
+    if T and Hkv and (ks[2] != 1 or vs[2] != 1 or (Hkv > 1 and (ks[1] != D or vs[1] != D))):
+        raise ValueError("the elements of a head and the heads of a row must be contiguous")
+    _int32("slot_map", slot_map)
     if slot_map.shape != (T,):
         raise ValueError("slot_map must be [T]")
-    _on_current_device(k, v, slot_map, k_codes, k_scales, v_codes, v_scales)
-    st = lib().attn_kv4_append(_ptr(k), _ptr(v), _ptr(slot_map), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
-                               _ptr(v_scales), T, Hkv, D, k.stride(0), v.stride(0), num_pages, page_size,
-                               float(k_descale), float(v_descale), _DTYPES[k.dtype], _stream(stream))
-    _check(st, "attn_kv4_append")
+    dev = _device_of(k, v, slot_map, k_codes, k_scales, v_codes, v_scales)
+    st = (_lib or lib()).attn_kv4_append(
+        _address(k), _address(v), _address(slot_map), _address(k_codes), _address(k_scales), _address(v_codes),
+        _address(v_scales), T, Hkv, D, ks[0], vs[0], num_pages, page_size, k_descale, v_descale, dtype,
+        _raw_stream(stream, dev))
+    if st:
+        _check(st, "attn_kv4_append")
 
 
 def attn_kv4_gather(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens, k, v, k_descale=1.0, v_descale=1.0,
@@ -481,22 +522,20 @@ def attn_kv4_gather(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
     """C-ABI ``attn_kv4_gather``: writes the first N rows of every sequence into ``k`` and ``v``
     [B, Hkv, N, D] (BF16 or FP16) as the values the cache stands for; zeros behind a sequence's end."""
     num_pages, Hkv, page_size, D = _kv4_dims(k_codes, k_scales, v_codes, v_scales)
-    if k.dim() != 4 or k.shape[1] != Hkv or k.shape[3] != D or v.shape != k.shape:
+    shape = k.shape
+    if len(shape) != 4 or shape[1] != Hkv or shape[3] != D or v.shape != shape:
         raise ValueError(f"k and v must be [B, {Hkv}, N, {D}]")
-    if k.dtype not in (torch.bfloat16, torch.float16) or v.dtype != k.dtype:
-        raise ValueError("k and v must share one dtype, bfloat16 or float16")
+    dtype = _one_dtype("k and v", k, v)
     if not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("k and v must be contiguous")
-    B, _, N, _ = k.shape
-    _int32(block_table=block_table, seq_lens=seq_lens)
-    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    _on_current_device(k, v, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
-    st = lib().attn_kv4_gather(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(block_table),
-                               _ptr(seq_lens), _ptr(k), _ptr(v), B, Hkv, N, D, num_pages, page_size,
-                               block_table.shape[1], float(k_descale), float(v_descale), _DTYPES[k.dtype],
-                               _stream(stream))
-    _check(st, "attn_kv4_gather")
+    max_pages = _tables(block_table, seq_lens, shape[0])
+    dev = _device_of(k, v, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
+    st = (_lib or lib()).attn_kv4_gather(
+        _address(k_codes), _address(k_scales), _address(v_codes), _address(v_scales), _address(block_table),
+        _address(seq_lens), _address(k), _address(v), shape[0], Hkv, shape[2], D, num_pages, page_size, max_pages,
+        k_descale, v_descale, dtype, _raw_stream(stream, dev))
+    if st:
+        _check(st, "attn_kv4_gather")
 
 
 def attn_decode_paged_kv4_workspace_bytes(B, Hq, Hkv, M, D, page_size, max_pages, max_seq_len, causal=True, window=0,
@@ -512,27 +551,28 @@ def attn_decode_paged_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
     sliding ``window``, the first ``sinks`` keys of a sequence stay visible. ``workspace`` None lets the
     library allocate it stream-ordered."""
     num_pages, Hkv, page_size, D = _kv4_dims(k_codes, k_scales, v_codes, v_scales)
-    if q.dim() != 4 or q.shape[3] != D or o.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != D or o.shape != shape:
         raise ValueError(f"q and o must be [B, Hq, M, {D}]")
-    if q.dtype not in (torch.bfloat16, torch.float16) or o.dtype != q.dtype:
-        raise ValueError("q and o must share one dtype, bfloat16 or float16")
+    dtype = _one_dtype("q and o", q, o)
     if not q.is_contiguous() or not o.is_contiguous():
         raise ValueError("q and o must be contiguous")
-    B, Hq, M, _ = q.shape
-    _int32(block_table=block_table, seq_lens=seq_lens)
-    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    _on_current_device(q, o, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
-    ws_bytes = 0
-    if workspace is not None:
-        _on_current_device(q, workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    st = lib().attn_decode_paged_kv4(_ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
-                                     _ptr(block_table), _ptr(seq_lens), _ptr(o), B, Hq, Hkv, M, D, num_pages,
-                                     page_size, block_table.shape[1], int(max_seq_len), int(bool(causal)),
-                                     int(window), int(sinks), float(scale or 0.0), float(k_descale), float(v_descale),
-                                     _DTYPES[q.dtype], _ptr(workspace), ws_bytes, _stream(stream))
-    _check(st, "attn_decode_paged_kv4")
+    max_pages = _tables(block_table, seq_lens, shape[0])
+    ws, ws_bytes = None, 0
+    if workspace is None:
+        dev = _device_of(q, o, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
+    else:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        dev = _device_of(q, o, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales, workspace)
+        ws, ws_bytes = _address(workspace), workspace.nbytes
+    st = (_lib or lib()).attn_decode_paged_kv4(
+        _address(q), _address(k_codes), _address(k_scales), _address(v_codes), _address(v_scales),
+        _address(block_table), _address(seq_lens), _address(o), shape[0], shape[1], Hkv, shape[2], D, num_pages,
+        page_size, max_pages, int(max_seq_len), 1 if causal else 0, int(window), int(sinks), scale or 0.0, k_descale,
+        v_descale, dtype, ws, ws_bytes, _raw_stream(stream, dev))
+    if st:
+        _check(st, "attn_decode_paged_kv4")
 
 
 def attn_split_softmax_workspace_bytes(M, N, chunk=1024) -> int:
