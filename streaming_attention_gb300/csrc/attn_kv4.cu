@@ -133,9 +133,12 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(AppendArgs a) {
     constexpr int NG = D / kKv4Group;
     constexpr int U = D / 8;  // threads of a row
+    // launched while the kernel in front of it may still run: nothing in memory is touched before that has ended
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int u = threadIdx.x % U;
     const int i = u / 4, c = u % 4;  // group, and which 8 of its 32 elements
     // a block takes one head of consecutive rows, whose keys mostly lie side by side on a page
@@ -251,9 +254,11 @@ __device__ __forceinline__ uint4 expand8(uint32_t codes, float s) {
 }
 
 template <typename T, int D, bool kNarrow>
-__global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a) {
+__global__ void __launch_bounds__(kThreads) kv4_gather_kernel(GatherArgs a) {
     constexpr int NG = D / kKv4Group;
     constexpr int U = D / 8;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int u = threadIdx.x % U;
     const int i = u / 4, c = u % 4;
     const bool odd = i & 1;
@@ -301,21 +306,18 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(const GatherArgs a
 template <typename T>
 cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
     const int per = kAppendRows * (kThreads / (D / 8));
-    const unsigned grid = (unsigned)(((long long)a.T + per - 1) / per * a.Hkv);
+    const dim3 grid((unsigned)(((long long)a.T + per - 1) / per * a.Hkv));
     switch (D) {
-        case 32: kv4_append_kernel<T, 32><<<grid, kThreads, 0, s>>>(a); break;
-        case 64: kv4_append_kernel<T, 64><<<grid, kThreads, 0, s>>>(a); break;
-        default: kv4_append_kernel<T, 128><<<grid, kThreads, 0, s>>>(a); break;
+        case 32: return launch_programmatic(kv4_append_kernel<T, 32>, grid, kThreads, s, a);
+        case 64: return launch_programmatic(kv4_append_kernel<T, 64>, grid, kThreads, s, a);
+        default: return launch_programmatic(kv4_append_kernel<T, 128>, grid, kThreads, s, a);
     }
-    return cudaGetLastError();
 }
 
 template <typename T, int D>
-void launch_gather_d(const GatherArgs& a, dim3 grid, bool narrow, cudaStream_t s) {
-    if (narrow)
-        kv4_gather_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
-    else
-        kv4_gather_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
+cudaError_t launch_gather_d(const GatherArgs& a, dim3 grid, bool narrow, cudaStream_t s) {
+    return narrow ? launch_programmatic(kv4_gather_kernel<T, D, true>, grid, kThreads, s, a)
+                  : launch_programmatic(kv4_gather_kernel<T, D, false>, grid, kThreads, s, a);
 }
 
 // Whether every scale (2^-9 .. 448) times the factor is a normal number of T.
@@ -336,11 +338,10 @@ cudaError_t launch_gather(const GatherArgs& a, int B, int D, cudaStream_t s) {
     const dim3 grid((unsigned)(((long long)a.N + per - 1) / per), (unsigned)a.Hkv, (unsigned)B);
     const bool narrow = narrow_factor<T>(a.k_scale) && narrow_factor<T>(a.v_scale);
     switch (D) {
-        case 32: launch_gather_d<T, 32>(a, grid, narrow, s); break;
-        case 64: launch_gather_d<T, 64>(a, grid, narrow, s); break;
-        default: launch_gather_d<T, 128>(a, grid, narrow, s); break;
+        case 32: return launch_gather_d<T, 32>(a, grid, narrow, s);
+        case 64: return launch_gather_d<T, 64>(a, grid, narrow, s);
+        default: return launch_gather_d<T, 128>(a, grid, narrow, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

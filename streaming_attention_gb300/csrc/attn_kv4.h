@@ -46,6 +46,24 @@ inline bool kv4_descale(float x) {
     return (b.u & 0x007FFFFFu) == 0 && e >= 1 && e <= 253;  // 2^-126 .. 2^126: its reciprocal is normal too
 }
 
+// Launches a kernel that may start while the one in front of it in the stream runs, and waits for its end itself
+// (griddepcontrol.wait) before it touches memory.
+template <class Args>
+inline cudaError_t launch_programmatic(void (*kernel)(Args), dim3 grid, int threads, cudaStream_t stream, const Args& args,
+                                       size_t smem = 0) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
 // Pools, table and lengths of a call; every pointer may be null only with nothing behind it.
 int kv4_validate_cache(const Kv4Cache& c, int Hkv, int D);
 

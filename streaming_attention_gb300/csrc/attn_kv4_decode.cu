@@ -83,6 +83,7 @@ struct DecodeArgs {
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
     int causal, window, sinks;
+    int whole;         // one segment per place, none cut
     float scale_log2;  // logit scale and K factor, times log2(e)
     float v_scale;
 };
@@ -356,7 +357,6 @@ __device__ __forceinline__ long long team_sum(long long x, int thread, long long
         const long long y = __shfl_up_sync(0xffffffffu, s, d);
         if (lane >= d) s += y;
     }
-    sync();  // the last use of `part` is done
     if (lane == 31) part[warp] = s;
     sync();
     long long before = 0, all = 0;
@@ -373,7 +373,7 @@ template <int D>
 constexpr int kTeamBytes = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(DecodeArgs a) {
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
     extern __shared__ __align__(16) uint8_t smem_of_block[];
@@ -411,18 +411,28 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    // ---- this block's range of the tiles ----
-    {
-        const auto cost_of = [&](int b) {
-            return b < a.B ? (long long)(tiles_of(a, length_of(a, b)).n + kPartCost) * H : 0ll;
-        };
-        long long total = 0, cost = 0, before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            long long all;
-            cost = cost_of(b0 + thread);
-            before = team_sum(cost, thread, sh.sums, team_sync, &all);
-            total += all;
+    // ---- this team's range of the tiles ----
+    if (a.whole) {
+        if (place >= a.B * H) return;
+        if (thread == 0) {
+            Part& p = sh.parts[0];
+            p.u = p.rem = 0;
+            p.b = place / H;
+            p.hz = place % H;
+            p.L = length_of(a, p.b);
+            p.tl = tiles_of(a, p.L);
+            p.t0 = 0;
+            p.t1 = p.tl.n;
+            p.len = 1;
+            sh.end = 1;
         }
+    } else {
+        // each thread sums the costs of a run of sequences
+        const int run = (a.B + kThreads - 1) / kThreads, b0 = min(thread * run, a.B), b1 = min(b0 + run, a.B);
+        const auto cost_of = [&](int b) { return (long long)(tiles_of(a, length_of(a, b)).n + kPartCost) * H; };
+        long long total, cost = 0;
+        for (int b = b0; b < b1; ++b) cost += cost_of(b);
+        long long before = team_sum(cost, thread, sh.sums, team_sync, &total);
         // a grid that is larger than the tiles need uses its first places only
         const int all_places = (int)gridDim.x * kTeams;
         const int places =
@@ -433,22 +443,18 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
         if (place >= places) return;
         if (thread == 0) sh.shares = shares;
         const long long u0 = shares.begin(place);
-        long long behind = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            long long all = total;
-            if (a.B > kThreads) {  // one chunk's sums are still at hand
-                cost = cost_of(b0 + thread);
-                before = behind + team_sum(cost, thread, sh.sums, team_sync, &all);
+        if (before <= u0 && u0 < before + cost) {
+            int b = b0;
+            for (;; ++b) {
+                const long long c = cost_of(b);
+                if (u0 < before + c) break;
+                before += c;
             }
-            if (before <= u0 && u0 < before + cost) {
-                sh.parts[0].u = u0;
-                sh.parts[0].rem = u0 - before;
-                sh.parts[0].b = b0 + thread;
-                sh.end = shares.begin(place + 1);
-                set_part(sh.parts[0], a, sh.end);
-            }
-            behind += all;
-            if (u0 < behind) break;
+            sh.parts[0].u = u0;
+            sh.parts[0].rem = u0 - before;
+            sh.parts[0].b = b;
+            sh.end = shares.begin(place + 1);
+            set_part(sh.parts[0], a, sh.end);
         }
     }
     team_sync();
@@ -793,7 +799,7 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
 constexpr int kJoinWarps = 16, kJoinBatch = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(DecodeArgs a) {
     __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
     __shared__ float4 sm_y[kJoinWarps][D / 4];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -879,8 +885,17 @@ int sm_count() {
 
 int row_blocks(const Problem& p) { return (int)(((long long)p.G * p.M + ROWS - 1) / ROWS); }
 
+// Few short segments are left whole, one to a team: no sums of costs, no second kernel. 2 KV heads of one sequence,
+// D = 64: 300 keys (5 tiles) 5.5 us whole and 8.2 cut, 1000 keys (16 tiles) 9.0 and 8.4, 2000 keys 14.2 and 8.6; 64 KV
+// heads (8 sequences), D = 128: 6.9 and 10.5, 11.3 and 12.4, 17.6 and 14.5.
+struct Plan {
+    int blocks;
+    bool whole;
+};
+constexpr int kWholeTiles = 16;
+
 // One block for every SM, fewer while the longest lengths could not give one team of each kMinTiles tiles.
-int plan_blocks(const Kv4Call& c) {
+Plan plan_blocks(const Kv4Call& c) {
     const Problem& p = c.p;
     long long tiles = ((long long)c.max_len + kTile - 1) / kTile;
     if (p.window > 0) {
@@ -889,9 +904,10 @@ int plan_blocks(const Kv4Call& c) {
         if (wt < tiles) tiles = wt;
     }
     if (tiles < 1) tiles = 1;
-    tiles = (tiles + kPartCost) * p.B * p.Hkv * row_blocks(p);
-    const long long most = sm_count(), want = (tiles + kMinTiles - 1) / kMinTiles;
-    return (int)(want < most ? want : most);
+    const long long segments = (long long)p.B * p.Hkv * row_blocks(p), sms = sm_count();
+    if (tiles <= kWholeTiles && segments <= sms * kTeams) return Plan{(int)(segments < sms ? segments : sms), true};
+    const long long want = ((tiles + kPartCost) * segments + kMinTiles - 1) / kMinTiles;
+    return Plan{(int)(want < sms ? want : sms), false};
 }
 
 template <typename T, int D>
@@ -902,23 +918,10 @@ cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
         return cudaFuncSetAttribute(kv4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (e != cudaSuccess) return e;
-    // each may be launched while the kernel in front of it runs, and waits for its end
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kTeams * kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t r = cudaLaunchKernelEx(&cfg, kv4_decode_kernel<T, D>, a);
-    if (r != cudaSuccess) return r;
-    cfg.gridDim = dim3((unsigned)blocks * kTeams);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, kv4_join_kernel<T, D>, a);
+    const cudaError_t r =
+        launch_programmatic(kv4_decode_kernel<T, D>, dim3((unsigned)blocks), kTeams * kThreads, s, a, kSmem);
+    if (r != cudaSuccess || a.whole) return r;
+    return launch_programmatic(kv4_join_kernel<T, D>, dim3((unsigned)blocks * kTeams), 32 * kJoinWarps, s, a);
 }
 
 template <typename T>
@@ -983,20 +986,23 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
 bool nothing_to_attend(const Kv4Call& c) { return c.max_len == 0 || c.c.num_pages == 0; }
 
 // Cut segments and their parts, two per team: [places] int4, then m, l and acc.
-size_t workspace_bytes(int blocks, int D) {
-    return (size_t)blocks * kTeams * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
+size_t workspace_bytes(const Plan& plan, int D) {
+    return plan.whole ? 0 : (size_t)plan.blocks * kTeams * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
 }
 
 int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void* o, void* ws, size_t ws_bytes,
-        int blocks, cudaStream_t s) {
+        const Plan& plan, cudaStream_t s) {
     const Problem& p = c.p;
-    if (!ws || ws_bytes < workspace_bytes(blocks, p.D)) return ATTN_ERR_WORKSPACE;
-    if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
+    const int blocks = plan.blocks;
+    if (!plan.whole) {
+        if (!ws || ws_bytes < workspace_bytes(plan, p.D)) return ATTN_ERR_WORKSPACE;
+        if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
+    }
     const size_t n = (size_t)blocks * kTeams * 2 * ROWS;
     int4* cut = static_cast<int4*>(ws);
-    float* wm = reinterpret_cast<float*>(cut + (size_t)blocks * kTeams);
+    float* wm = plan.whole ? nullptr : reinterpret_cast<float*>(cut + (size_t)blocks * kTeams);
     const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
-                       c.max_pages, c.max_len, p.causal, p.window, c.sinks, p.scale_log2, c.v_descale};
+                       c.max_pages, c.max_len, p.causal, p.window, c.sinks, plan.whole, p.scale_log2, c.v_descale};
     const cudaError_t e =
         p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, blocks, s) : launch_d<__half>(a, p.D, blocks, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
@@ -1037,12 +1043,12 @@ int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scal
     if ((int64_t)B * Hq * M == 0) return ATTN_OK;
     if (nothing_to_attend(c))  // no sequence can hold a key: every row outputs 0
         return cudaMemsetAsync(o, 0, (size_t)B * Hq * M * D * 2, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-    const int blocks = plan_blocks(c);
-    if (workspace) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, blocks, s);
-    const size_t bytes = workspace_bytes(blocks, D);
+    const Plan plan = plan_blocks(c);
+    const size_t bytes = workspace_bytes(plan, D);
+    if (workspace || bytes == 0) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, plan, s);
     void* ws = nullptr;
     if (cudaMallocAsync(&ws, bytes, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    rc = run(c, q, block_table, seq_lens, o, ws, bytes, blocks, s);
+    rc = run(c, q, block_table, seq_lens, o, ws, bytes, plan, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess && rc == ATTN_OK) rc = ATTN_ERR_CUDA;
     return rc;
 }

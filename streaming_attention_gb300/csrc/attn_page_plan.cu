@@ -19,6 +19,7 @@
 
 #include "attn.h"
 #include "attn_internal.h"
+#include "attn_kv4.h"
 
 namespace attn {
 namespace {
@@ -95,11 +96,14 @@ __device__ __forceinline__ int pages_of(uint32_t x, uint32_t page_size, int most
 
 // N threads, K requests of a chunk to a thread.
 template <int N, int K>
-__global__ void __launch_bounds__(N) page_plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
     // a request's first row of the batch and first page of the free list (2^31 - 1 for all behind that), its keys in
     // the cache and its pages
     __shared__ int start[N * K], first[N * K], have[N * K], old[N * K];
     __shared__ longlong2 part[N / 32];
+    // launched while the kernel in front of it may still run: nothing in memory is touched before that has ended
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long mine = (long long)blockIdx.x * N + threadIdx.x;
     const long long step = (long long)gridDim.x * N;
     long long rows = 0, pages = 0;  // of the requests before this chunk
@@ -228,11 +232,11 @@ int attn_page_plan(const int* cached_lens, const int* new_lens, const int* free_
     if (grid > sms) grid = sms;
     if (grid < 1) grid = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (threads == 256)
-        page_plan_kernel<256, 1><<<(unsigned)grid, 256, 0, s>>>(a);
-    else
-        page_plan_kernel<1024, kPlanMost / 1024><<<(unsigned)grid, 1024, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    const dim3 g((unsigned)grid);
+    const cudaError_t e = threads == 256
+                              ? launch_programmatic(page_plan_kernel<256, 1>, g, threads, s, a)
+                              : launch_programmatic(page_plan_kernel<1024, kPlanMost / 1024>, g, threads, s, a);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"
