@@ -83,7 +83,7 @@ struct DecodeArgs {
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
     int causal, window, sinks;
-    int whole;         // one segment per place, none cut
+    int whole;         // one segment per place, none cut (the kernel's kWhole)
     float scale_log2;  // logit scale and K factor, times log2(e)
     float v_scale;
 };
@@ -346,10 +346,22 @@ struct Stage {
     }
 };
 
+// What a team's warps share.
+struct Shared {
+    float m[kWarps][ROWS], l[kWarps][ROWS];  // of a part, by warp
+    int2 vis[2][ROWS];                       // the visible range of every row, of this part and of the last or next
+    long long sums[kWarps];
+    long long end;  // of the team's range
+    Part parts[2];
+    Shares shares;
+};
+
+__device__ __forceinline__ void sync_team(int team) {
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kThreads) : "memory");
+}
+
 // Exclusive sum over a team's threads, and the total.
-template <class Sync>
-__device__ __forceinline__ long long team_sum(long long x, int thread, long long* part, const Sync& sync,
-                                              long long* total) {
+__device__ __forceinline__ long long team_sum(long long x, int thread, int team, long long* part, long long* total) {
     const int lane = thread & 31, warp = thread >> 5;
     long long s = x;
 #pragma unroll
@@ -358,7 +370,7 @@ __device__ __forceinline__ long long team_sum(long long x, int thread, long long
         if (lane >= d) s += y;
     }
     if (lane == 31) part[warp] = s;
-    sync();
+    sync_team(team);
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -369,51 +381,13 @@ __device__ __forceinline__ long long team_sum(long long x, int thread, long long
     return s - x + before;
 }
 
-template <int D>
-constexpr int kTeamBytes = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(DecodeArgs a) {
-    using St = Stage<D>;
-    constexpr int NG = D / kKv4Group;
-    extern __shared__ __align__(16) uint8_t smem_of_block[];
-    struct Shared {
-        float m[kWarps][ROWS], l[kWarps][ROWS];  // of a part, by warp
-        int2 vis[2][ROWS];                       // the visible range of every row, of this part and of the last or next
-        long long sums[kWarps];
-        long long end;  // of the team's range
-        Part parts[2];
-        Shares shares;
-    };
-    __shared__ Shared shared_of_block[kTeams];
-    const int team = threadIdx.x / kThreads, thread = threadIdx.x % kThreads;
-    Shared& sh = shared_of_block[team];
-    uint8_t* smem = smem_of_block + team * kTeamBytes<D>;  // the rings, then the warps' sums of a part
-    float* sm_acc = reinterpret_cast<float*>(smem + kWarps * kStages * St::kBytes);  // [kWarps][ROWS][D]
-    const auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kThreads) : "memory"); };
-    const int place = team * (int)gridDim.x + (int)blockIdx.x;
-
-    const int warp = thread >> 5, lane = thread & 31;
-    const int gq = lane >> 2, cq = lane & 3;  // the lane's place in a matrix fragment
-    const int key_slot = (gq >> 1) + 4 * (gq & 1);  // the key of slot gq; slot gq + 8: 8 more
-    const uint32_t ring = ptx::smem_u32(smem) + warp * (kStages * St::kBytes);
-    const St from(a.c, lane);
-    // where the lane reads in a stage; the values' chunks of every other pair of rows are exchanged
-    const int at_k = St::kK + gq * St::kRow + cq * (4 * NG), at_ks = St::kKs + key_slot * NG * (St::kSpread ? 2 : 1);
-    const int at_v = St::kV + cq * St::kRow + (D == 128 ? (gq * 8) ^ ((cq & 2) * 16) : gq * (2 * NG));
-    const int at_vs = St::kVs + cq * NG * (St::kSpread ? 4 : 1);
+// Finds the team's range of the tiles: its first part and its end. False: there is none. The costs are summed a chunk of
+// sequences at a time, one per thread; up to kThreads sequences take one pass.
+template <bool kWhole>
+__device__ __forceinline__ bool find_range(const DecodeArgs& a, Shared& sh, int thread, int team, int place) {
     const int H = a.Hkv * a.Z;
-    const int R = a.G * a.M;
-    const int ps = a.c.page_size;
-
-    // The join kernel may be launched now (it waits for this one's end); and this kernel may itself have been launched
-    // before the end of the one in front of it, so nothing in memory is touched before that has ended.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // ---- this team's range of the tiles ----
-    if (a.whole) {
-        if (place >= a.B * H) return;
+    if (kWhole) {
+        if (place >= a.B * H) return false;
         if (thread == 0) {
             Part& p = sh.parts[0];
             p.u = p.rem = 0;
@@ -427,12 +401,17 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(Decode
             sh.end = 1;
         }
     } else {
-        // each thread sums the costs of a run of sequences
-        const int run = (a.B + kThreads - 1) / kThreads, b0 = min(thread * run, a.B), b1 = min(b0 + run, a.B);
-        const auto cost_of = [&](int b) { return (long long)(tiles_of(a, length_of(a, b)).n + kPartCost) * H; };
-        long long total, cost = 0;
-        for (int b = b0; b < b1; ++b) cost += cost_of(b);
-        long long before = team_sum(cost, thread, sh.sums, team_sync, &total);
+        const auto cost_of = [&](int b) {
+            return b < a.B ? (long long)(tiles_of(a, length_of(a, b)).n + kPartCost) * H : 0ll;
+        };
+        long long total = 0, cost = 0, before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            long long all;
+            cost = cost_of(b0 + thread);
+            sync_team(team);
+            before = team_sum(cost, thread, team, sh.sums, &all);
+            total += all;
+        }
         // a grid that is larger than the tiles need uses its first places only
         const int all_places = (int)gridDim.x * kTeams;
         const int places =
@@ -440,23 +419,65 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(Decode
         Shares shares;
         shares.per = divide(total, places, &shares.more);
         if (thread == 0) a.cut[place] = make_int4(-1, 0, 0, 0);
-        if (place >= places) return;
+        if (place >= places) return false;
         if (thread == 0) sh.shares = shares;
         const long long u0 = shares.begin(place);
-        if (before <= u0 && u0 < before + cost) {
-            int b = b0;
-            for (;; ++b) {
-                const long long c = cost_of(b);
-                if (u0 < before + c) break;
-                before += c;
+        long long behind = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            long long all = total;
+            if (a.B > kThreads) {  // one chunk's sums are still at hand
+                cost = cost_of(b0 + thread);
+                sync_team(team);
+                before = behind + team_sum(cost, thread, team, sh.sums, &all);
             }
-            sh.parts[0].u = u0;
-            sh.parts[0].rem = u0 - before;
-            sh.parts[0].b = b;
-            sh.end = shares.begin(place + 1);
-            set_part(sh.parts[0], a, sh.end);
+            if (before <= u0 && u0 < before + cost) {
+                sh.parts[0].u = u0;
+                sh.parts[0].rem = u0 - before;
+                sh.parts[0].b = b0 + thread;
+                sh.end = shares.begin(place + 1);
+                set_part(sh.parts[0], a, sh.end);
+            }
+            behind += all;
+            if (u0 < behind) break;
         }
     }
+    return true;
+}
+
+template <int D>
+constexpr int kTeamBytes = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
+
+template <typename T, int D, bool kWhole>
+__global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const __grid_constant__ DecodeArgs a) {
+    using St = Stage<D>;
+    constexpr int NG = D / kKv4Group;
+    extern __shared__ __align__(16) uint8_t smem_of_block[];
+    __shared__ Shared shared_of_block[kTeams];
+    const int team = threadIdx.x / kThreads, thread = threadIdx.x % kThreads;
+    Shared& sh = shared_of_block[team];
+    uint8_t* smem = smem_of_block + team * kTeamBytes<D>;  // the rings, then the warps' sums of a part
+    float* sm_acc = reinterpret_cast<float*>(smem + kWarps * kStages * St::kBytes);  // [kWarps][ROWS][D]
+    const auto team_sync = [&] { sync_team(team); };
+    const int place = team * (int)gridDim.x + (int)blockIdx.x;
+
+    const int warp = thread >> 5, lane = thread & 31;
+    const int gq = lane >> 2, cq = lane & 3;  // the lane's place in a matrix fragment
+    const int key_slot = (gq >> 1) + 4 * (gq & 1);  // the key of slot gq; slot gq + 8: 8 more
+    const uint32_t ring = ptx::smem_u32(smem) + warp * (kStages * St::kBytes);
+    const St from(a.c, lane);
+    // where the lane reads in a stage; the values' chunks of every other pair of rows are exchanged
+    const int at_k = St::kK + gq * St::kRow + cq * (4 * NG), at_ks = St::kKs + key_slot * NG * (St::kSpread ? 2 : 1);
+    const int at_v = St::kV + cq * St::kRow + (D == 128 ? (gq * 8) ^ ((cq & 2) * 16) : gq * (2 * NG));
+    const int at_vs = St::kVs + cq * NG * (St::kSpread ? 4 : 1);
+    const int R = a.G * a.M;
+    const int ps = a.c.page_size;
+
+    // The join kernel may be launched now (it waits for this one's end); and this kernel may itself have been launched
+    // before the end of the one in front of it, so nothing in memory is touched before that has ended.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (!find_range<kWhole>(a, sh, thread, team, place)) return;
     team_sync();
 
     // ---- the copies of a part ----
@@ -910,16 +931,16 @@ Plan plan_blocks(const Kv4Call& c) {
     return Plan{(int)(want < sms ? want : sms), false};
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWhole>
 cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
     constexpr int kSmem = kTeams * kTeamBytes<D>;
     static PerDeviceOnce once;
     const cudaError_t e = once_per_device(once, [] {
-        return cudaFuncSetAttribute(kv4_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        return cudaFuncSetAttribute(kv4_decode_kernel<T, D, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (e != cudaSuccess) return e;
     const cudaError_t r =
-        launch_programmatic(kv4_decode_kernel<T, D>, dim3((unsigned)blocks), kTeams * kThreads, s, a, kSmem);
+        launch_programmatic(kv4_decode_kernel<T, D, kWhole>, dim3((unsigned)blocks), kTeams * kThreads, s, a, kSmem);
     if (r != cudaSuccess || a.whole) return r;
     return launch_programmatic(kv4_join_kernel<T, D>, dim3((unsigned)blocks * kTeams), 32 * kJoinWarps, s, a);
 }
@@ -927,9 +948,9 @@ cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_d(const DecodeArgs& a, int D, int blocks, cudaStream_t s) {
     switch (D) {
-        case 32: return launch_t<T, 32>(a, blocks, s);
-        case 64: return launch_t<T, 64>(a, blocks, s);
-        default: return launch_t<T, 128>(a, blocks, s);
+        case 32: return (a.whole ? launch_t<T, 32, true>(a, blocks, s) : launch_t<T, 32, false>(a, blocks, s));
+        case 64: return (a.whole ? launch_t<T, 64, true>(a, blocks, s) : launch_t<T, 64, false>(a, blocks, s));
+        default: return (a.whole ? launch_t<T, 128, true>(a, blocks, s) : launch_t<T, 128, false>(a, blocks, s));
     }
 }
 
