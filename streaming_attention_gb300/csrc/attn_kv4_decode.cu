@@ -79,7 +79,9 @@ struct DecodeArgs {
     const int* lens;
     void* o;
     float *ws_m, *ws_l, *ws_acc;  // [places][2][ROWS], the same, [places][2][ROWS][D]
-    int4* cut;                    // [places]: segment that a team leaves unfinished (b, head * Z + z), last place of it
+    int4* cut;  // segments that are in parts (b, head * Z + z, first and last place; b < 0: none): by segment, [segments],
+                // or where there are more segments than places by the place that begins one, [places]
+    int by_segment;
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
     int causal, window, sinks;
@@ -418,7 +420,7 @@ __device__ __forceinline__ bool find_range(const DecodeArgs& a, Shared& sh, int 
             total >= (long long)kMinTiles * all_places ? all_places : (int)((total + kMinTiles - 1) / kMinTiles);
         Shares shares;
         shares.per = divide(total, places, &shares.more);
-        if (thread == 0) a.cut[place] = make_int4(-1, 0, 0, 0);
+        if (thread == 0 && !a.by_segment) a.cut[place] = make_int4(-1, 0, 0, 0);
         if (place >= places) return false;
         if (thread == 0) sh.shares = shares;
         const long long u0 = shares.begin(place);
@@ -803,9 +805,16 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
                     }
                 }
             }
-            if (thread == 0 && begun && !done) {
-                const int n = tl.n + kPartCost;
-                a.cut[place] = make_int4(part.b, part.hz, sh.shares.place_of(part.u - part.rem % n + n - 1), 0);
+            if (!kWhole && thread == 0 && begun) {  // a whole segment has no list and no workspace
+                int4 cut = make_int4(-1, 0, 0, 0);
+                if (!done) {
+                    const int n = tl.n + kPartCost;
+                    cut = make_int4(part.b, part.hz, place, sh.shares.place_of(part.u - part.rem % n + n - 1));
+                }
+                if (a.by_segment)
+                    a.cut[part.b * (a.Hkv * a.Z) + part.hz] = cut;
+                else if (!done)
+                    a.cut[place] = cut;
             }
             team_sync();  // the part and the sums are read
             if (thread == 0) next_part(sh.parts[turn], sh.parts[turn ^ 1], a, sh.end);
@@ -814,29 +823,34 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
     }
 }
 
-// Joins the parts of the segment that the team at place blockIdx.x left unfinished: the part in that place's second
-// slot and those in the first slots of the places behind it. kJoinWarps / rows of the warps share the parts of a row,
-// eight at a time: what bounds this kernel is the chain of loads (cut, then parts).
-constexpr int kJoinWarps = 16, kJoinBatch = 8;
+// Joins the parts of the segment cut[blockIdx.x]: the part in its first place's second slot and those in the first slots
+// of the places behind it. The W warps take a row each, or share a row's parts where there are fewer rows, kJoinBatch at
+// a time; kRow: the block takes row blockIdx.y alone. What bounds this kernel is its launch and the chain of loads (cut,
+// then parts), so a block is as small as the number of parts lets it be. The whole decode of 64 segments in 7 parts each
+// took 18.2 us with 16 warps and all rows a block, 17.3 with 4 warps a row; of 8 segments in 57 parts 38.8 and, with 8
+// warps a row, 35.9; of 512 segments mostly in one part 122.4 and, with 4 warps a block, 118.3.
+constexpr int kJoinBatch = 8;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(DecodeArgs a) {
-    __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
-    __shared__ float4 sm_y[kJoinWarps][D / 4];
+template <typename T, int D, int W, bool kRow>
+__global__ void __launch_bounds__(32 * W) kv4_join_kernel(DecodeArgs a) {
+    __shared__ float sm_m[W], sm_l[W];
+    __shared__ float4 sm_y[W][D / 4];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 cut = a.cut[blockIdx.x];
     if (cut.x < 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = (cut.y % a.Z) * ROWS, rows = min(ROWS, a.G * a.M - r0);
-    const int team = rows <= 1 ? 16 : rows <= 2 ? 8 : rows <= 4 ? 4 : 2;  // warps of a row
-    const int r = warp / team, share = warp % team;
-    const int parts = cut.z - (int)blockIdx.x + 1;
+    if (kRow && (int)blockIdx.y >= rows) return;
+    const int most = kRow || rows <= 1 ? W : rows <= 2 ? W / 2 : rows <= 4 ? W / 4 : W / 8;
+    const int team = most > 1 ? most : 1;  // warps of a row
+    const int share = warp % team;
+    const int parts = cut.w - cut.z + 1;
     const bool has = lane < D / 4;
-    float mx = -FLT_MAX, l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < rows) {
-        for (int x0 = share; x0 < parts; x0 += kJoinBatch * team) {
+    for (int r = kRow ? (int)blockIdx.y : warp / team; r < ROWS; r += W / team) {  // one turn unless rows exceed warps
+        float mx = -FLT_MAX, l = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x0 = share; r < rows && x0 < parts; x0 += kJoinBatch * team) {
             float m[kJoinBatch], s[kJoinBatch];
             float4 v[kJoinBatch];
 #pragma unroll
@@ -846,7 +860,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(DecodeArgs a)
                 s[e] = 0.f;
                 v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (x < parts) {
-                    const size_t row = ((size_t)(blockIdx.x + x) * 2 + (x == 0)) * ROWS + r;
+                    const size_t row = ((size_t)(cut.z + x) * 2 + (x == 0)) * ROWS + r;
                     m[e] = a.ws_m[row];
                     s[e] = a.ws_l[row];
                     if (has) v[e] = reinterpret_cast<const float4*>(a.ws_acc + row * D)[lane];
@@ -866,30 +880,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(DecodeArgs a)
                 y = make_float4(fmaf(f, v[e].x, y.x), fmaf(f, v[e].y, y.y), fmaf(f, v[e].z, y.z), fmaf(f, v[e].w, y.w));
             }
         }
+        if (team > 1) {
+            if (lane == 0) {
+                sm_m[warp] = mx;
+                sm_l[warp] = l;
+            }
+            if (has) sm_y[warp][lane] = y;
+            __syncthreads();
+            if (share != 0 || r >= rows || !has) return;
+            float top = mx;
+            for (int w = warp + 1; w < warp + team; ++w) top = fmaxf(top, sm_m[w]);
+            l = 0.f;
+            y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = warp; w < warp + team; ++w) {
+                const float f = ptx::ex2(sm_m[w] - top);
+                const float4 v = sm_y[w][lane];
+                l = fmaf(f, sm_l[w], l);
+                y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
+            }
+        }
+        if (r < rows && has) {
+            const size_t at = (((size_t)cut.x * a.Hq + cut.y / a.Z * a.G) * a.M + r0 + r) * D + 4 * lane;
+            const float f = l > 0.f ? a.v_scale / l : 0.f;
+            put<T>(a.o, at, y.x * f);
+            put<T>(a.o, at + 1, y.y * f);
+            put<T>(a.o, at + 2, y.z * f);
+            put<T>(a.o, at + 3, y.w * f);
+        }
+        if (team > 1) return;
     }
-    if (lane == 0) {
-        sm_m[warp] = mx;
-        sm_l[warp] = l;
-    }
-    if (has) sm_y[warp][lane] = y;
-    __syncthreads();
-    if (share != 0 || r >= rows || !has) return;
-    float top = mx;
-    for (int w = warp + 1; w < warp + team; ++w) top = fmaxf(top, sm_m[w]);
-    l = 0.f;
-    y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = warp; w < warp + team; ++w) {
-        const float f = ptx::ex2(sm_m[w] - top);
-        const float4 v = sm_y[w][lane];
-        l = fmaf(f, sm_l[w], l);
-        y = make_float4(fmaf(f, v.x, y.x), fmaf(f, v.y, y.y), fmaf(f, v.z, y.z), fmaf(f, v.w, y.w));
-    }
-    const size_t at = (((size_t)cut.x * a.Hq + cut.y / a.Z * a.G) * a.M + r0 + r) * D + 4 * lane;
-    const float f = l > 0.f ? a.v_scale / l : 0.f;
-    put<T>(a.o, at, y.x * f);
-    put<T>(a.o, at + 1, y.y * f);
-    put<T>(a.o, at + 2, y.z * f);
-    put<T>(a.o, at + 3, y.w * f);
 }
 
 struct Kv4Call {
@@ -942,7 +961,12 @@ cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
     const cudaError_t r =
         launch_programmatic(kv4_decode_kernel<T, D, kWhole>, dim3((unsigned)blocks), kTeams * kThreads, s, a, kSmem);
     if (r != cudaSuccess || a.whole) return r;
-    return launch_programmatic(kv4_join_kernel<T, D>, dim3((unsigned)blocks * kTeams), 32 * kJoinWarps, s, a);
+    const unsigned entries = (unsigned)(a.by_segment ? a.B * a.Hkv * a.Z : blocks * kTeams);
+    const unsigned rows = (unsigned)(a.G * a.M < ROWS ? a.G * a.M : ROWS);
+    const unsigned parts = (unsigned)(blocks * kTeams) / entries;  // of a segment, about
+    if (parts >= 16) return launch_programmatic(kv4_join_kernel<T, D, 8, true>, dim3(entries, rows), 32 * 8, s, a);
+    if (parts >= 3) return launch_programmatic(kv4_join_kernel<T, D, 4, true>, dim3(entries, rows), 32 * 4, s, a);
+    return launch_programmatic(kv4_join_kernel<T, D, 4, false>, dim3(entries), 32 * 4, s, a);
 }
 
 template <typename T>
@@ -1015,14 +1039,15 @@ int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void
         const Plan& plan, cudaStream_t s) {
     const Problem& p = c.p;
     const int blocks = plan.blocks;
-    if (!plan.whole) {
+    if (!plan.whole) {  // (the cut segments' list has an entry per place, and is by segment only where it has room)
         if (!ws || ws_bytes < workspace_bytes(plan, p.D)) return ATTN_ERR_WORKSPACE;
         if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
     }
     const size_t n = (size_t)blocks * kTeams * 2 * ROWS;
     int4* cut = static_cast<int4*>(ws);
     float* wm = plan.whole ? nullptr : reinterpret_cast<float*>(cut + (size_t)blocks * kTeams);
-    const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
+    const int by_segment = (int64_t)p.B * p.Hkv * row_blocks(p) <= (int64_t)blocks * kTeams;
+    const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, by_segment, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
                        c.max_pages, c.max_len, p.causal, p.window, c.sinks, plan.whole, p.scale_log2, c.v_descale};
     const cudaError_t e =
         p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, blocks, s) : launch_d<__half>(a, p.D, blocks, s);

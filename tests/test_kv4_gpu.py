@@ -55,9 +55,11 @@ def run_decode(q, dev, table, lens, cap, causal=True, window=0, sinks=0, scale=0
     if ws:
         n = sa.attn_decode_paged_kv4_workspace_bytes(B, Hq, dev[0].shape[1], M, D, dev[0].shape[2], table.shape[1], cap,
                                                      causal, window, sinks)
-        work = torch.full((max(n, 1),), 255, dtype=torch.uint8, device=DEV)
+        room = torch.full((n + 4096,), 255, dtype=torch.uint8, device=DEV)  # exactly n bytes, watched behind
+        work = room[:n]
     sa.attn_decode_paged_kv4(q, *dev, i32(table), i32(lens), o, cap, causal, window, sinks, scale, kd, vd, work)
     torch.cuda.synchronize()
+    assert not ws or bool((room[n:] == 255).all()), "written behind the workspace"
     return o
 
 
