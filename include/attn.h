@@ -84,7 +84,7 @@ typedef enum {
     ATTN_ERR_CUDA = -9,      /* a CUDA runtime/driver call failed (launch, copy, ...) */
     ATTN_ERR_TIMEOUT = -10,  /* a kernel gave up on a bounded wait (see attn_last_device_status) */
     ATTN_ERR_PATH = -11,     /* the requested path cannot run this problem */
-    ATTN_ERR_SCALE = -12,    /* a factor of a 4-bit cache is not a positive power of two */
+    ATTN_ERR_SCALE = -12,    /* a factor of a 4-bit cache is no power of two of 2^-64 .. 2^64 */
     ATTN_ERR_ALIAS = -13     /* an output overlaps an input or another output */
 } attn_status_t;
 
@@ -401,7 +401,7 @@ ATTN_API int attn_decode_paged_fp8(const void* q, const void* k_pages, const voi
  * each with 32 codes n in 0..15 and a scale s; an element stands for
  *   descale * s * (n - 8),
  * exact in FP16 and BF16 times descale. k_descale and v_descale are one factor
- * for a whole cache, positive powers of two (else ATTN_ERR_SCALE), to be given
+ * for a whole cache, powers of two 2^-64 .. 2^64 (else ATTN_ERR_SCALE), to be given
  * with the same value to every call; they move the range of the scales
  * (2^-9 .. 448) to that of the data (1 suits magnitudes from 0.1 to a few
  * hundred). Codes lie in a row in units of consecutive elements, 8 in a key row
@@ -472,9 +472,11 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  *   window: row i sees the keys j <= p_i (causal) with j > p_i - window or
  *   j < sinks. <= 0: none; without a window it changes nothing.
  * The values of the cache enter the products exactly; the query is rounded to
- * FP16 relative to its row's largest element and the probabilities to FP16, all
- * sums are FP32. Pages need not be clean: rows behind a sequence's end may hold
- * anything. A table entry outside [0, num_pages) reads a page of zeros.
+ * FP16 relative to its row's largest element and the probabilities to FP16 before
+ * and after their product with a scale (for FP16 outputs after it), all sums are
+ * FP32. Pages need not be clean: rows that no query row sees (behind a
+ * sequence's end, or in front of its window and no sinks) may hold anything. A
+ * table entry outside [0, num_pages) reads a page of zeros.
  * D is 32, 64 or 128 (else ATTN_ERR_HEADDIM); B * Hkv <= 65535 and at most
  * 8 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
  * to 8 grouped rows read the cache once, more in blocks of 8 rows; for many

@@ -408,7 +408,7 @@ const char* attn_strerror(int status) {
         case ATTN_ERR_CUDA: return "CUDA call failed";
         case ATTN_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
         case ATTN_ERR_PATH: return "the requested path cannot run this problem";
-        case ATTN_ERR_SCALE: return "a 4-bit cache's factor is not a positive power of two";
+        case ATTN_ERR_SCALE: return "a 4-bit cache's factor is no power of two of 2^-64 .. 2^64";
         case ATTN_ERR_ALIAS: return "an output overlaps an input or another output";
         default: return "unknown status";
     }

@@ -220,6 +220,7 @@ struct Pair;
 template <>
 struct Pair<__nv_bfloat16> {
     static constexpr uint32_t kBase = 0x43004300u;  // 128 + n
+    static constexpr bool kAlways = true;           // every allowed factor is narrow
     static __device__ __forceinline__ uint32_t value(uint32_t h, uint32_t s2) {
         const __nv_bfloat162 x = __hsub2(as_pair<__nv_bfloat162>(h), __floats2bfloat162_rn(136.f, 136.f));
         const __nv_bfloat162 y = __hmul2(x, as_pair<__nv_bfloat162>(s2));
@@ -229,6 +230,7 @@ struct Pair<__nv_bfloat16> {
 template <>
 struct Pair<__half> {
     static constexpr uint32_t kBase = 0x64006400u;  // 1024 + n
+    static constexpr bool kAlways = false;
     static __device__ __forceinline__ uint32_t value(uint32_t h, uint32_t s2) {
         const __half2 x = __hsub2(as_pair<__half2>(h), __floats2half2_rn(1032.f, 1032.f));
         const __half2 y = __hmul2(x, as_pair<__half2>(s2));
@@ -316,27 +318,19 @@ cudaError_t launch_append(const AppendArgs& a, int D, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_gather_d(const GatherArgs& a, dim3 grid, bool narrow, cudaStream_t s) {
-    return narrow ? launch_programmatic(kv4_gather_kernel<T, D, true>, grid, kThreads, s, a)
-                  : launch_programmatic(kv4_gather_kernel<T, D, false>, grid, kThreads, s, a);
+    if constexpr (!Pair<T>::kAlways)
+        if (!narrow) return launch_programmatic(kv4_gather_kernel<T, D, false>, grid, kThreads, s, a);
+    return launch_programmatic(kv4_gather_kernel<T, D, true>, grid, kThreads, s, a);
 }
 
-// Whether every scale (2^-9 .. 448) times the factor is a normal number of T.
-template <typename T>
-bool narrow_factor(float f);
-template <>
-bool narrow_factor<__half>(float f) {
-    return f >= 0x1p-5f && f <= 0x1p7f;
-}
-template <>
-bool narrow_factor<__nv_bfloat16>(float f) {
-    return f >= 0x1p-117f && f <= 0x1p119f;
-}
+// Whether every scale (2^-9 .. 448) times the factor is a normal FP16 number. In BF16 all are.
+bool narrow_factor(float f) { return f >= 0x1p-5f && f <= 0x1p7f; }
 
 template <typename T>
 cudaError_t launch_gather(const GatherArgs& a, int B, int D, cudaStream_t s) {
     const int per = kGatherRows * (kThreads / (D / 8));
     const dim3 grid((unsigned)(((long long)a.N + per - 1) / per), (unsigned)a.Hkv, (unsigned)B);
-    const bool narrow = narrow_factor<T>(a.k_scale) && narrow_factor<T>(a.v_scale);
+    const bool narrow = narrow_factor(a.k_scale) && narrow_factor(a.v_scale);
     switch (D) {
         case 32: return launch_gather_d<T, 32>(a, grid, narrow, s);
         case 64: return launch_gather_d<T, 64>(a, grid, narrow, s);

@@ -35,7 +35,8 @@ struct Kv4Cache {
 inline bool kv4_head_dim(int D) { return D == 32 || D == 64 || D == 128; }
 inline bool kv4_page_size(int ps) { return ps == 16 || ps == 32 || ps == 64 || (ps > 0 && ps % 128 == 0); }
 
-// A positive power of two in the normal range: scaling by it is exact.
+// A power of two from 2^-64 to 2^64: scaling by it is exact, and what the kernels make of it (its product with a scale,
+// its reciprocal over a scale, its quotient by a row sum) stays in the normal range of FP32.
 inline bool kv4_descale(float x) {
     union {
         float f;
@@ -43,7 +44,7 @@ inline bool kv4_descale(float x) {
     } b;
     b.f = x;
     const uint32_t e = b.u >> 23;
-    return (b.u & 0x007FFFFFu) == 0 && e >= 1 && e <= 253;  // 2^-126 .. 2^126: its reciprocal is normal too
+    return (b.u & 0x007FFFFFu) == 0 && e >= 127 - 64 && e <= 127 + 64;
 }
 
 // Launches a kernel that may start while the one in front of it in the stream runs, and waits for its end itself

@@ -44,6 +44,7 @@ def decode(L, q=at(0), kc=at(1), ks=at(2), vc=at(3), vs=at(4), table=at(5), lens
     (dict(B_=1 << 20, maxp=1 << 12), -6),          # the table
     (dict(kd=0.0), -12), (dict(kd=-1.0), -12), (dict(vd=0.3), -12), (dict(vd=float("inf")), -12),
     (dict(vd=float("nan")), -12), (dict(kd=2.0 ** -130), -12), (dict(kd=2.0 ** 127), -12),
+    (dict(kd=2.0 ** -65), -12), (dict(vd=2.0 ** 65), -12),
     (dict(q=None), -1), (dict(o=None), -1), (dict(kc=None), -1), (dict(vs=None), -1), (dict(table=None), -1),
     (dict(lens=None), -1),
     (dict(q=OFF), -7), (dict(o=OFF), -7), (dict(ks=OFF), -7), (dict(table=ODD), -7), (dict(lens=ODD), -7),
@@ -72,6 +73,7 @@ def append(L, k=at(0), v=at(1), slots=at(2), kc=at(3), ks=at(4), vc=at(5), vs=at
     (dict(dtype=2), -3), (dict(T=-1), -2), (dict(Hkv=-1), -2), (dict(ps=8), -2), (dict(D=80), -4),
     (dict(kst=255), -2), (dict(vst=0), -2), (dict(kst=260), -7), (dict(vst=1028), -7),
     (dict(T=1 << 24), -6), (dict(pages=1 << 28), -6), (dict(kd=3.0), -12), (dict(vd=0.0), -12),
+    (dict(kd=2.0 ** 65), -12), (dict(vd=2.0 ** -65), -12),
     (dict(k=None), -1), (dict(slots=None), -1), (dict(vc=None), -1), (dict(v=OFF), -7), (dict(slots=ODD), -7),
     (dict(T=0, k=None, v=None, slots=None), 0), (dict(pages=0, kc=None, ks=None, vc=None, vs=None), 0),
 ])
@@ -86,7 +88,7 @@ def gather(L, kc=at(0), ks=at(1), vc=at(2), vs=at(3), table=at(4), lens=at(5), k
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), -3), (dict(N=-1), -2), (dict(B_=-1), -2), (dict(maxp=-1), -2), (dict(D=8), -4), (dict(ps=12), -2),
-    (dict(N=1 << 24), -6), (dict(B_=70000, N=1), -6), (dict(kd=0.7), -12), (dict(k=None), -1), (dict(lens=None), -1),
+    (dict(N=1 << 24), -6), (dict(B_=70000, N=1), -6), (dict(kd=0.7), -12), (dict(vd=2.0 ** -65), -12), (dict(k=None), -1), (dict(lens=None), -1),
     (dict(table=None), -1), (dict(v=OFF), -7), (dict(N=0, k=None, v=None), 0),
 ])
 def test_gather_refusals(L, kw, status):
