@@ -29,22 +29,26 @@
 // 8 of n - 8 is subtracted from sums: 8 times the groups' sums of Q, times the keys'
 // scales, is where the logits start (one product more), and the sums of P, which a
 // product with a matrix of ones gives in the accumulators' own layout, are taken off
-// at the end. (Exact
-// n - 8 in halves took one more addition per pair: 430 -> 350 instructions per 16
-// keys.) The scales are applied where there are fewer numbers than elements: a
-// key's to the sum of a group's 32 products, a value's to the probabilities, once
-// per group.
+// at the end. (Exact n - 8 in halves took one more addition per pair: 430 -> 350
+// instructions per 16 keys.) The scales are applied where there are fewer numbers than
+// elements: a key's to the sum of a group's 32 products, a value's to the
+// probabilities, once per group.
 // What bounds it: the expansion, 320 instructions of a warp per 16 keys of D = 128 on
-// pipes that the 21 matrix instructions among them share. 64 sequences of 8192 keys,
-// 8 KV heads (570 MB): 122 us, 4.7 TB/s, 69 % of the measured copy bandwidth; with
-// the copies left out 115 us. 12 warps of 168 registers beat 16 of 128 (139 us), 20 of
-// 96 and 24 of 80: fewer registers leave the compiler less to overlap in a warp.
-// FP8 products (half the expansion) run at a quarter of the rate and lose (144 us).
+// pipes that the 21 matrix instructions among them share. 64 sequences of up to 16384
+// keys, 8192 on average, 8 KV heads (580 MB): 117 us, 5.0 TB/s, 73 % of the measured
+// copy bandwidth; with the copies left out it took 115 us. 12 warps of 168 registers
+// beat 16 of 128 (139 us where 12 took 122), 20 of 96 and 24 of 80: fewer registers
+// leave the compiler less to overlap in a warp. 16 query rows to a team, for more than
+// 8, need 255 registers and leave 8 warps: 44.6 us for 16 sequences of 8192 keys with 16
+// rows each, and in two blocks of 8 rows 41.7. FP8 products (half the expansion) run at a
+// quarter of the rate and lose (144 us). The time moves by up to 8 % with the order in
+// which the compiler is given the same work: the values' scales are converted in front
+// of the softmax, where the matrix instructions leave room (117 us; behind it 121).
 // Rounded below 32 bits: Q to FP16 after scaling each row by a power of two to
 // maximum 2^14..2^15 (exact for elements above 2^-20 of the maximum), the
-// probabilities to FP16, kept 64 times too large to stay clear of its small numbers
-// (the row sum adds them unrounded), and their products with the values' scales
-// (2^-9 .. 448, so between 2^-3 and 28672 at probability 1) to FP16.
+// probabilities to FP16, kept 8 to 128 times too large to stay clear of its small
+// numbers (the row sum adds them unrounded), and their products with the values' scales
+// (2^-9 .. 448, so between 2^-6 and 57344 at the largest score) to FP16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
         // product with the keys' scales (column k of that product's left operand is the scale of group k % 4).
         uint32_t qf[NG][2][2], start[2];
         float sc[2];
-{
+        {
             const int r = r0 + gq;
             float x[NG][8], top = 0.f;
             const bool row = r < R;
@@ -603,11 +607,10 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
             key_range(p, L, a.causal, a.window, &v.x, &v.y);
             sh.vis[turn][lane] = v;
         }
-        __syncwarp();
         // keys [all_lo, all_hi) are visible to every row
-        int all_lo, all_hi, skip;
+        int all_lo, all_hi, any_lo, skip;
         key_range(L - 1, L, a.causal, a.window, &all_lo, &skip);
-        key_range(L - a.M, L, a.causal, a.window, &skip, &all_hi);
+        key_range(L - a.M, L, a.causal, a.window, &any_lo, &all_hi);
 
         // m: the score that stands for the largest one so far, in units of sc: it is set anew only when a score exceeds it
         // by kPSlack in base 2 (else every few steps some row's would be); limit: that border; mu: kPShift less m in base 2
@@ -639,8 +642,6 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
                 else
                     load_shared(v[e], st + at_v + 4 * e * St::kRow);
                 if constexpr (!St::kSpread) vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
-                // whatever stands behind the sequence counts as zero
-                if (edge && j0 + cq + 4 * e >= L) vs[e] = 0;
             }
             // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
             float s[4];
@@ -673,6 +674,12 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
                 }
             }
 
+            // the scales as halves, those of a pair of keys side by side
+            uint32_t f0[4], f1[4];
+            e4m3x4(__byte_perm(vs[0], vs[1], 0x5140u), f0[0], f0[1]);
+            e4m3x4(__byte_perm(vs[2], vs[3], 0x5140u), f1[0], f1[1]);
+            e4m3x4(__byte_perm(vs[0], vs[1], 0x7362u), f0[2], f0[3]);
+            e4m3x4(__byte_perm(vs[2], vs[3], 0x7362u), f1[2], f1[3]);
             // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
             bool rises = false;
 #pragma unroll
@@ -715,12 +722,6 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
             add2(l[0], l[1], s[2], s[3]);
 
             // ---- O^T += V^T (P s)^T ----
-            // the scales as halves, those of a pair of keys side by side
-            uint32_t f0[4], f1[4];
-            e4m3x4(__byte_perm(vs[0], vs[1], 0x5140u), f0[0], f0[1]);
-            e4m3x4(__byte_perm(vs[2], vs[3], 0x5140u), f1[0], f1[1]);
-            e4m3x4(__byte_perm(vs[0], vs[1], 0x7362u), f0[2], f0[3]);
-            e4m3x4(__byte_perm(vs[2], vs[3], 0x7362u), f1[2], f1[3]);
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 // the unit of group n of both keys of a pair: its low byte and its high byte
@@ -738,11 +739,27 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
             }
         };
 
+        // What stands behind the sequence, or in front of its window on pages that may have been given up, counts as
+        // zero: the scales of such values are cleared in the stage (a probability of zero would not hide a NaN).
+        const auto hide = [&](uint32_t st, int j0) {
+            const int x = lane & 15, j = j0 + x;
+            if (lane < 16 && !(j < L && (j >= any_lo || j < a.sinks))) {
+                if constexpr (NG == 4)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kVs + ((x & 3) * 4 + (x >> 2)) * NG), "r"(0) : "memory");
+                else if constexpr (NG == 2)
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(st + St::kVs + x * NG), "h"((short)0) : "memory");
+                else
+                    asm volatile("st.shared.b8 [%0], %1;" ::"r"(st + St::kVs + x), "r"(0) : "memory");
+            }
+            __syncwarp();
+        };
         const auto any_step = [&](uint32_t st, int j0) {
             if (j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks))
                 step(st, j0, Flag<false>());
-            else if (j0 < L)
+            else if (j0 < L) {
+                hide(st, j0);
                 step(st, j0, Flag<true>());
+            }
         };
         for (int t = part.t0; t < t1; t += 2) {
             const uint32_t st = ring + (fill ^ 2 * St::kBytes);  // the pair of tiles t, t + 1
@@ -756,26 +773,24 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
 
         // ---- the next part's copies begin; then the warps' sums are joined ----
         begin_copies(ahead, page0, page1);
-{
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
-                const int r = 2 * cq + t;
-                if (gq == 0) {
-                    sh.m[warp][r] = m[t] * sc[t];
-                    sh.l[warp][r] = l[t];
-                }
-                // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even: low nibbles) or gq + 8
+            for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
+            const int r = 2 * cq + t;
+            if (gq == 0) {
+                sh.m[warp][r] = m[t] * sc[t];
+                sh.l[warp][r] = l[t];
+            }
+            // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even: low nibbles) or gq + 8
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const float off = -8.f * psum[n][t];
-                    *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) =
-                        make_float4(fmaf(acc[2 * n][t], 1.f / kLowUnit, off),
-                                    fmaf(acc[2 * n][2 + t], 1.f / kHighUnit, off),
-                                    fmaf(acc[2 * n + 1][t], 1.f / kLowUnit, off),
-                                    fmaf(acc[2 * n + 1][2 + t], 1.f / kHighUnit, off));
-                }
+            for (int n = 0; n < NG; ++n) {
+                const float off = -8.f * psum[n][t];
+                *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) =
+                    make_float4(fmaf(acc[2 * n][t], 1.f / kLowUnit, off),
+                                fmaf(acc[2 * n][2 + t], 1.f / kHighUnit, off),
+                                fmaf(acc[2 * n + 1][t], 1.f / kLowUnit, off),
+                                fmaf(acc[2 * n + 1][2 + t], 1.f / kHighUnit, off));
             }
         }
         team_sync();

@@ -574,5 +574,189 @@ def test_calls_on_two_streams_and_two_threads():
     assert not errors and all(torch.equal(o, j[5]) for o, j in zip(outs, jobs))
 
 
+@pytest.mark.parametrize("ps,M,sinks", [(16, 1, 0), (16, 3, 5), (64, 1, 70), (32, 9, 16)])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_decode_rows_no_query_sees_may_hold_anything(ps, M, sinks, D):
+    """NaN scales in front of the window: on pages wholly behind it (given up) and in the one it begins in."""
+    lens, window = [500, 90, 333, 64], 75
+    q, dev, host, table = case(90 + M, lens, 4, 2, M, D, ps, BF16)
+    want = run_decode(q, dev, table, lens, 512, True, window, sinks)
+    seen = np.zeros(host[1].shape[:3:2], bool)
+    for b, L in enumerate(lens):
+        for j in range(L):
+            seen[table[b, j // ps], j % ps] = j >= max(L - M - window + 1, 0) or j < sinks
+    dead = torch.from_numpy(~seen).to(DEV)
+    assert int(dead.sum()) > 200
+    for n in (1, 3):
+        dev[n].view(torch.uint8).permute(0, 2, 1, 3)[dead] = 0x7F  # E4M3 NaN
+    for n in (0, 2):
+        dev[n].permute(0, 2, 1, 3)[dead] = 0xF0
+    assert torch.equal(run_decode(q, dev, table, lens, 512, True, window, sinks), want)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("dtype,kd,vd", [(BF16, 2.0 ** -64, 2.0 ** 64), (BF16, 2.0 ** 64, 2.0 ** -64),
+                                         (FP16, 2.0 ** -5, 2.0 ** 7), (FP16, 2.0 ** -6, 1.0), (FP16, 1.0, 2.0 ** 8),
+                                         (FP16, 2.0 ** -16, 2.0 ** 10), (FP16, 2.0 ** -64, 2.0 ** -20)])
+def test_factors_at_their_ends(D, dtype, kd, vd):
+    """The largest and the smallest factors, and on both sides of where FP16 holds every scale times the factor as a
+    normal number: write, read back (rounded once to dtype) and attention. FP16 rows are far from their factor's
+    range where that is needed: all codes 8, or scales at the top."""
+    rng = np.random.default_rng(91)
+    Hkv, ps, pages, T = 2, 16, 8, 100
+    x = {}
+    for which, d in (("k", kd), ("v", vd)):
+        size = d if dtype == BF16 else min(max(d, 2.0 ** -14), 2.0 ** 9)
+        x[which] = torch.from_numpy(model_rows(rng, (T, Hkv, D), which) * size).to(dtype)
+        x[which][5] = 0
+        x[which][6] *= 2.0 ** 5
+        assert torch.isfinite(x[which]).all()
+    dev = sa.kv4_cache(pages, Hkv, ps, D)
+    table = make_table(rng, [T], ps, pages)
+    slots = [int(table[0, j // ps]) * ps + j % ps for j in range(T)]
+    sa.attn_kv4_append(x["k"].to(DEV), x["v"].to(DEV), i32(slots), *dev, kd, vd)
+    out = {w: torch.full((1, Hkv, T, D), float("nan"), dtype=dtype, device=DEV) for w in "kv"}
+    sa.attn_kv4_gather(*dev, i32(table), i32([T]), out["k"], out["v"], kd, vd)
+    val, unit = {}, {}
+    for which, d, n in (("k", kd, 0), ("v", vd, 2)):
+        codes, byte, val[which] = ref.quantize(ref.f64(x[which]).transpose(1, 0, 2), d)
+        unit[which] = ref.units(byte, d)
+        got = bytes_np(dev[n])[table[0]].transpose(1, 0, 2, 3).reshape(Hkv, -1, D // 2)[:, :T]
+        assert np.array_equal(got, ref.pack(codes, which)), which
+        got = bytes_np(dev[n + 1])[table[0]].transpose(1, 0, 2, 3).reshape(Hkv, -1, D // 32)[:, :T]
+        assert np.array_equal(got, byte), which
+        assert torch.equal(out[which][0].cpu(), torch.from_numpy(val[which]).to(dtype)), which
+    # keys of order one for the query's scale; outputs of FP16 stay in its range
+    q = torch.from_numpy(rng.normal(size=(1, 4, 1, D))).to(dtype)
+    scale = float(1 / (np.abs(val["k"]).max() + 2.0 ** -66) / 8)
+    if dtype == FP16 and np.abs(val["v"]).max() > 60000:
+        return
+    o = run_decode(q.to(DEV), dev, table, [T], T, True, 0, 0, scale, kd, vd)
+    want, bound = ref.attention(ref.f64(q)[0], val["k"], val["v"], True, 0, 0, scale, dtype, unit["k"], unit["v"], vd)
+    assert (np.abs(ref.f64(o)[0] - want) <= bound).all()
+
+
+@pytest.mark.parametrize("B,Hkv,most,D", [(300, 2, 1500, 64), (130, 4, 900, 32), (229, 2, 2500, 64), (457, 1, 400, 128)])
+def test_decode_many_ragged_sequences(B, Hkv, most, D):
+    """More sequences than a team has threads, more segments than there are teams, some of them cut."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, most, B).tolist()
+    lens[7], lens[8], lens[B - 1] = most, 0, 1
+    q, dev, host, table = case(B, lens, 2 * Hkv, Hkv, 1, D, 16, BF16)
+    o = run_decode(q, dev, table, lens, most)
+    check_decode(o, q, host, table, lens, most)
+
+
+@pytest.mark.parametrize("cap", [1023, 1024, 1025])
+@pytest.mark.parametrize("B,Hq,Hkv", [(3, 4, 2), (228, 2, 2), (229, 2, 2)])
+def test_decode_on_both_sides_of_whole_segments(B, Hq, Hkv, cap):
+    """16 tiles of keys and 456 segments (three teams on each of 152 SMs) are left whole, more are cut."""
+    rng = np.random.default_rng(cap)
+    lens = rng.integers(1, cap + 1, B).tolist()
+    lens[0] = cap
+    q, dev, host, table = case(cap + B, lens, Hq, Hkv, 1, 64, 64, FP16)
+    o = run_decode(q, dev, table, lens, cap)
+    check_decode(o, q, host, table, lens, cap)
+
+
+def test_append_and_gather_on_pages_of_no_power_of_two():
+    rng = np.random.default_rng(92)
+    Hkv, ps, pages, D, T = 2, 384, 4, 128, 700
+    x = {w: torch.from_numpy(model_rows(rng, (T, Hkv, D), w)).to(BF16).to(DEV) for w in "kv"}
+    table = np.array([[2, 0], [3, 1]], np.int32)
+    dev = sa.kv4_cache(pages, Hkv, ps, D)
+    slots = [int(table[0, j // ps]) * ps + j % ps for j in range(T)]
+    sa.attn_kv4_append(x["k"], x["v"], i32(slots), *dev, 1.0, 0.125)
+    k = torch.full((2, Hkv, 800, D), float("nan"), dtype=BF16, device=DEV)
+    v = k.clone()
+    sa.attn_kv4_gather(*dev, i32(table), i32([T, 500]), k, v, 1.0, 0.125)
+    torch.cuda.synchronize()
+    for out, w, d in ((k, "k", 1.0), (v, "v", 0.125)):
+        want = ref.quantize(ref.f64(x[w]).transpose(1, 0, 2), d)[2]
+        assert np.array_equal(ref.f64(out[0, :, :T]), want) and not out[0, :, T:].any() and not out[1].any()
+
+
+def test_one_workspace_for_calls_and_graphs_one_after_the_other():
+    """Nothing in a workspace outlives a call: one of them serves calls of other shapes in turn (cut segments listed by
+    segment and by team, left whole), holds any bytes before a call, and is shared by two graphs."""
+    jobs, most = [], 0
+    for seed, lens, Hq, Hkv, M, D in ((1, [5000], 8, 2, 1, 128), (2, list(range(1, 901, 2)), 2, 2, 1, 64),
+                                      (3, [30, 900], 4, 2, 3, 32), (4, [9000, 1, 2000], 16, 8, 2, 128)):
+        q, dev, host, table = case(seed, lens, Hq, Hkv, M, D, 16, BF16)
+        n = sa.attn_decode_paged_kv4_workspace_bytes(len(lens), Hq, Hkv, M, D, 16, table.shape[1], max(lens))
+        most = max(most, n)
+        jobs.append((q, dev, i32(table), i32(lens), max(lens), run_decode(q, dev, table, lens, max(lens))))
+    work = torch.empty(most, dtype=torch.uint8, device=DEV)
+    outs = [torch.zeros_like(j[0]) for j in jobs]
+
+    def call(j, o):
+        sa.attn_decode_paged_kv4(j[0], *j[1], j[2], j[3], o, j[4], k_descale=1.0, v_descale=0.125, workspace=work)
+
+    for fill in (0, 0x7F, 0xFF):
+        work.fill_(fill)
+        for o in outs:
+            o.zero_()
+        for x in (0, 1, 2, 3, 0, 2, 1, 0):
+            call(jobs[x], outs[x])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, j[5]) for o, j in zip(outs, jobs))
+    graphs = []
+    for x in range(4):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(jobs[x], outs[x])
+        graphs.append(g)
+    for o in outs:
+        o.zero_()
+    for x in (3, 0, 1, 0, 2, 1, 3):
+        graphs[x].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, j[5]) for o, j in zip(outs, jobs))
+
+
+def test_captured_behind_copies_and_branches():
+    """The calls in a graph behind copies, fills and other kernels and with two branches joined in front of them: their
+    early launch must not get ahead of any of those."""
+    rng = np.random.default_rng(93)
+    lens = [3000, 700]
+    q, dev, host, table = case(93, lens, 8, 2, 1, 128, 16, BF16)
+    want = run_decode(q, dev, table, lens, 3000)
+    d_table, d_lens = i32(table), i32(lens)
+    x = torch.from_numpy(rng.normal(size=(64, 2, 128))).to(BF16).to(DEV)
+    slots = i32(rng.permutation(3 * 16)[:40].tolist() + [-1] * 24)
+    pool = sa.kv4_cache(3, 2, 16, 128)
+    sa.attn_kv4_append(x, x, slots, *pool)
+    k = torch.empty(1, 2, 48, 128, dtype=BF16, device=DEV)
+    v = torch.empty_like(k)
+    pages, n48 = i32([[0, 1, 2]]), i32([48])
+    sa.attn_kv4_gather(*pool, pages, n48, k, v)
+    torch.cuda.synchronize()
+    w_k, w_v = k.clone(), v.clone()
+    late = [torch.zeros_like(t) for t in (q, d_table, d_lens, x, slots)]
+    o = torch.zeros_like(q)
+    other = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for t in pool:
+            t.view(torch.uint8).zero_()
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            late[0].copy_(q)
+            late[3].copy_(x * 1.0)
+        for n, src in ((1, d_table), (2, d_lens), (4, slots)):
+            late[n].copy_(src)
+        torch.cuda.current_stream().wait_stream(other)
+        sa.attn_kv4_append(late[3], late[3], late[4], *pool)
+        sa.attn_kv4_gather(*pool, pages, n48, k, v)
+        sa.attn_decode_paged_kv4(late[0], *dev, late[1], late[2], o, 3000, k_descale=1.0, v_descale=0.125)
+        sa.attn_decode_paged_kv4(late[0], *dev, late[1], late[2], o, 3000, k_descale=1.0, v_descale=0.125)
+    for _ in range(5):
+        for t in (*late, o, k, v):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(k, w_k) and torch.equal(v, w_v)
+
+
 def test_status_word_stays_clear():
     assert sa.last_device_status() == 0
