@@ -48,7 +48,8 @@
 // maximum 2^14..2^15 (exact for elements above 2^-20 of the maximum), the
 // probabilities to FP16, kept 8 to 128 times too large to stay clear of its small
 // numbers (the row sum adds them unrounded), and their products with the values' scales
-// (2^-9 .. 448, so between 2^-6 and 57344 at the largest score) to FP16.
+// (2^-9 .. 448, so between 2^-6 and 57344 at the largest score) to FP16; with FP16
+// outputs the former rounding's remainder is not lost.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -135,6 +136,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 // four E4M3 bytes -> four halves
 __device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
@@ -185,6 +191,11 @@ __device__ __forceinline__ const void* row_block(const uint8_t* pool, uint32_t b
     asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(p) : "r"(block), "r"(bytes), "l"(reinterpret_cast<uint64_t>(pool)));
     return reinterpret_cast<const void*>(p);
 }
+
+template <typename T>
+constexpr bool is_half = false;
+template <>
+constexpr bool is_half<__half> = true;
 
 template <typename T>
 __device__ __forceinline__ float lo_of(uint32_t w);
@@ -457,6 +468,9 @@ template <typename T, int D, bool kWhole>
 __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const __grid_constant__ DecodeArgs a) {
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
+    // An output in FP16 shows the two roundings of a probability (1.7 times the error of the output's own rounding), one
+    // in BF16 does not: for FP16 the first one's remainder is carried into the second (1.4 times, and 1 % of the time).
+    constexpr bool kFine = is_half<T>;
     extern __shared__ __align__(16) uint8_t smem_of_block[];
     __shared__ Shared shared_of_block[kTeams];
     const int team = threadIdx.x / kThreads, thread = threadIdx.x % kThreads;
@@ -717,7 +731,14 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
             fma2(s[2], s[3], sc, mu);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = ptx::ex2(s[e]);
-            const uint32_t pb0 = transpose8(ptx::pack_f16(s[0], s[1])), pb1 = transpose8(ptx::pack_f16(s[2], s[3]));
+            const uint32_t h0 = ptx::pack_f16(s[0], s[1]), h1 = ptx::pack_f16(s[2], s[3]);
+            const uint32_t pb0 = transpose8(h0), pb1 = transpose8(h1);
+            [[maybe_unused]] uint32_t rest0 = 0, rest1 = 0;  // what the rounding of P left
+            if constexpr (kFine) {
+                const float2 y0 = halves(h0), y1 = halves(h1);
+                rest0 = transpose8(ptx::pack_f16(s[0] - y0.x, s[1] - y0.y));
+                rest1 = transpose8(ptx::pack_f16(s[2] - y1.x, s[3] - y1.y));
+            }
             add2(l[0], l[1], s[0], s[1]);
             add2(l[0], l[1], s[2], s[3]);
 
@@ -728,7 +749,14 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
                 const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
                 const uint32_t u0 = __byte_perm(v[0][n / 2], v[1][n / 2], lo), u1 = __byte_perm(v[2][n / 2], v[3][n / 2], lo);
                 const uint32_t h0 = __byte_perm(v[0][n / 2], v[1][n / 2], hi), h1 = __byte_perm(v[2][n / 2], v[3][n / 2], hi);
-                const uint32_t p0 = hmul2(pb0, f0[n]), p1 = hmul2(pb1, f1[n]);
+                uint32_t p0, p1;
+                if constexpr (kFine) {
+                    p0 = hfma2(pb0, f0[n], hmul2(rest0, f0[n]));
+                    p1 = hfma2(pb1, f1[n], hmul2(rest1, f1[n]));
+                } else {
+                    p0 = hmul2(pb0, f0[n]);
+                    p1 = hmul2(pb1, f1[n]);
+                }
                 float (&lo_acc)[4] = acc[2 * n], (&hi_acc)[4] = acc[2 * n + 1];
                 mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
                 mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);

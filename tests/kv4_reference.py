@@ -93,6 +93,8 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype, ku=None, vu=None
       such products below FP16's normal range: each is off by at most 2^-25, times a code of at most 8 and
       the factor vd, over a sum of p that is at least 2^3; the same again for p itself
                                                        L 2 * 2^-25 8 vd / 2^3 max(1, s)
+      With FP16 outputs the first rounding's remainder (itself rounded, 2^-11 of 2^-11) is multiplied by the scale and
+      added before the second: 2^-11 + 2 * 2^-22 in all, and one product more that may be small (3 in place of 2).
       FP32 sums over the keys, 16 a matrix instruction (L/16 + 64) 2^-23 23 sum w vu
       the logits: the query's small elements (2^-25 of the row's largest), FP32 sums over D (truncating
       adders counted: 2^-23 a term) of up to 23 ku |q| each, and the exponent's argument; a logit's error
@@ -121,7 +123,10 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype, ku=None, vu=None
             logit = (logit + 4 * 2.0 ** -24 * (np.abs(s) + abs(s.max()))).max()
             n = len(s)
             small = n * 2.0 ** -24 * max(vd, np.abs(vv).max())  # 8 vd s is at most the largest value and more
-            bound[h, i] = (half * np.abs(o[h, i]) + A * (2.0 ** -10 + 2 * logit) + U * (n / 16 + 64) * 2.0 ** -23
+            p = 2.0 ** -10
+            if out_dtype == torch.float16:
+                small, p = 1.5 * small, 2.0 ** -11 + 2.0 ** -21
+            bound[h, i] = (half * np.abs(o[h, i]) + A * (p + 2 * logit) + U * (n / 16 + 64) * 2.0 ** -23
                            + small + 1e-30)
             if out_dtype == torch.float16:
                 bound[h, i] += 2.0 ** -25  # its smallest numbers
