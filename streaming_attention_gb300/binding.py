@@ -486,8 +486,8 @@ def attn_page_plan(cached_lens, new_lens, free_pages, block_table, seq_lens, row
         raise ValueError("free_pages and slot_map are one-dimensional, stats is [3]")
     dev = _device_of(stats, cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map)
     st = (_lib or lib()).attn_page_plan(
-        _address(cached_lens), _address(new_lens), _address(free_pages), _address(block_table), _address(seq_lens),
-        row_starts.data_ptr(), _address(slot_map), stats.data_ptr(), B, int(page_size), max_pages, free_pages.numel(),
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        row_starts.data_ptr(), slot_map.data_ptr(), stats.data_ptr(), B, int(page_size), max_pages, free_pages.numel(),
         slot_map.numel(), _raw_stream(stream, dev))
     if st:
         _check(st, "attn_page_plan")
@@ -510,8 +510,8 @@ def attn_kv4_append(k, v, slot_map, k_codes, k_scales, v_codes, v_scales, k_desc
         raise ValueError("slot_map must be [T]")
     dev = _device_of(k, v, slot_map, k_codes, k_scales, v_codes, v_scales)
     st = (_lib or lib()).attn_kv4_append(
-        _address(k), _address(v), _address(slot_map), _address(k_codes), _address(k_scales), _address(v_codes),
-        _address(v_scales), T, Hkv, D, ks[0], vs[0], num_pages, page_size, k_descale, v_descale, dtype,
+        k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+        v_scales.data_ptr(), T, Hkv, D, ks[0], vs[0], num_pages, page_size, k_descale, v_descale, dtype,
         _raw_stream(stream, dev))
     if st:
         _check(st, "attn_kv4_append")
@@ -531,8 +531,8 @@ def attn_kv4_gather(k_codes, k_scales, v_codes, v_scales, block_table, seq_lens,
     max_pages = _tables(block_table, seq_lens, shape[0])
     dev = _device_of(k, v, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales)
     st = (_lib or lib()).attn_kv4_gather(
-        _address(k_codes), _address(k_scales), _address(v_codes), _address(v_scales), _address(block_table),
-        _address(seq_lens), _address(k), _address(v), shape[0], Hkv, shape[2], D, num_pages, page_size, max_pages,
+        k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(), shape[0], Hkv, shape[2], D, num_pages, page_size, max_pages,
         k_descale, v_descale, dtype, _raw_stream(stream, dev))
     if st:
         _check(st, "attn_kv4_gather")
@@ -567,8 +567,8 @@ def attn_decode_paged_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, 
         dev = _device_of(q, o, block_table, seq_lens, k_codes, k_scales, v_codes, v_scales, workspace)
         ws, ws_bytes = _address(workspace), workspace.nbytes
     st = (_lib or lib()).attn_decode_paged_kv4(
-        _address(q), _address(k_codes), _address(k_scales), _address(v_codes), _address(v_scales),
-        _address(block_table), _address(seq_lens), _address(o), shape[0], shape[1], Hkv, shape[2], D, num_pages,
+        q.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), shape[0], shape[1], Hkv, shape[2], D, num_pages,
         page_size, max_pages, int(max_seq_len), 1 if causal else 0, int(window), int(sinks), scale or 0.0, k_descale,
         v_descale, dtype, ws, ws_bytes, _raw_stream(stream, dev))
     if st:
