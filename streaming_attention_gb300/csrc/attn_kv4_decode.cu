@@ -1,22 +1,25 @@
 // Decode attention over the 4-bit paged KV cache (format: attn_kv4.h).
 //
 // Work. A segment is the visible keys of one (sequence, KV head, block of 8 grouped
-// query rows), in tiles of 64 keys; query head h = g * G + r / M, row i = r % M. The
-// tiles of all segments in a row are cut into equal ranges, one per team of four
-// warps; a block of three teams fills an SM, and the grid the GPU, once, whatever the
-// lengths are: each team counts the tiles from seq_lens itself. A segment that lies
+// query rows), in tiles; query head h = g * G + r / M, row i = r % M. The tiles of all
+// segments in a row are cut into equal ranges, one per team of W warps, whose tiles are
+// of 16 W keys; a block of 12 warps fills an SM, and the grid the GPU, once, whatever the
+// lengths are: each block counts the tiles from seq_lens itself. A segment that lies
 // inside a team's range is written to o there; of one that is cut, each team leaves
 // its part's (m, l, acc) in the workspace (at most two parts a team: one begun before
 // it, one that goes on behind it), and a second kernel joins them by the
 // common-maximum rule. Ranges depend on the lengths and the grid alone, so the order
-// of all sums does too. (Three teams in one block and not in three: the schedulers
-// then serve them alike; as blocks they ended one after the other, 135 us for 129.)
+// of all sums does too. (Teams in one block and not one to a block: the schedulers then
+// serve them alike; as blocks they ended one after the other, 135 us for 129.)
 //
-// The warps of a team take 16 keys each of a tile and keep their own running
-// (m, l, acc) per row, joined through shared memory at the end of a segment's part.
-// Each warp copies its keys' codes and scales into a ring of its own (cp.async, a
-// pair of tiles ahead, no barrier between warps); the next part's copies begin
-// before the sums of the last one are joined.
+// A team is one warp where there are many segments (the rule is at Plan): it has no
+// sums of other warps to wait for and reads a segment's query once instead of four
+// times. It is four warps for few segments, which would be cut into many parts, and for
+// segments that are left whole: the warps take 16 keys each of a tile and keep their own
+// running (m, l, acc) per row, joined through shared memory at the end of a segment's
+// part. Each warp copies its keys' codes and scales into a ring of its own (cp.async, a
+// pair of tiles ahead, no barrier between warps); the next part's copies begin before
+// the sums of the last one are joined.
 //
 // A warp's products run transposed, on m16n8k16 matrix instructions with the
 // cache as the left operand, so that a row of the cache is expanded once for all
@@ -35,7 +38,7 @@
 // probabilities, once per group.
 // What bounds it: the expansion, 320 instructions of a warp per 16 keys of D = 128 on
 // pipes that the 21 matrix instructions among them share. 64 sequences of up to 16384
-// keys, 8192 on average, 8 KV heads (580 MB): 117 us, 5.0 TB/s, 73 % of the measured
+// keys, 8192 on average, 8 KV heads (580 MB): 116 us, 5.0 TB/s, 74 % of the measured
 // copy bandwidth; with the copies left out it took 115 us. 12 warps of 168 registers
 // beat 16 of 128 (139 us where 12 took 122), 20 of 96 and 24 of 80: fewer registers
 // leave the compiler less to overlap in a warp. 16 query rows to a team, for more than
@@ -65,10 +68,11 @@
 namespace attn {
 namespace {
 
-constexpr int kTeams = 3;            // of a block; one block per SM: 12 warps of 168 registers
-constexpr int kWarps = 4;            // of a team
+constexpr int kWarps = 12;           // of a block, 168 registers a thread; one block per SM
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16 * kWarps;   // keys of a tile, 16 per warp
+// W warps make a team, 4 or 1, and share a tile of 16 keys per warp.
+constexpr int teams_of(int W) { return kWarps / W; }
+constexpr int tile_of(int W) { return 16 * W; }
 constexpr int kStages = 4;           // tiles in a warp's ring, two pairs
 constexpr int ROWS = 8;              // query rows of a team
 constexpr int kPartCost = 6;         // what a segment costs beside its tiles, in tiles (see Part)
@@ -90,7 +94,6 @@ struct DecodeArgs {
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
     int causal, window, sinks;
-    int whole;         // one segment per place, none cut (the kernel's kWhole)
     float scale_log2;  // logit scale and K factor, times log2(e)
     float v_scale;
 };
@@ -101,7 +104,9 @@ struct Tiles {
     int sink, win, n;  // tiles of the sinks, first tile of the window, all
     __device__ int at(int t) const { return t < sink ? t : t - sink + win; }
 };
+template <int W>
 __device__ __forceinline__ Tiles tiles_of(const DecodeArgs& a, int L) {
+    constexpr int kTile = tile_of(W);
     int lo0, hi0, lo1, hi1;
     key_range(L - a.M, L, a.causal, a.window, &lo0, &hi0);
     key_range(L - 1, L, a.causal, a.window, &lo1, &hi1);
@@ -218,6 +223,21 @@ __device__ __forceinline__ void put<__half>(void* o, size_t i, float x) {
     reinterpret_cast<__half*>(o)[i] = __float2half_rn(x);
 }
 
+// four elements y f from i on, i a multiple of 4
+template <typename T>
+__device__ __forceinline__ void put4(void* o, size_t i, const float4& y, float f);
+template <>
+__device__ __forceinline__ void put4<__nv_bfloat16>(void* o, size_t i, const float4& y, float f) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * f, y.y * f), hi = __floats2bfloat162_rn(y.z * f, y.w * f);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(o) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+template <>
+__device__ __forceinline__ void put4<__half>(void* o, size_t i, const float4& y, float f) {
+    *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(o) + i) =
+        make_uint2(ptx::pack_f16(y.x * f, y.y * f), ptx::pack_f16(y.z * f, y.w * f));
+}
+
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -256,8 +276,8 @@ struct Shares {
 // The part of a segment that a block is at: tiles [t0, t1) of it. Kept in shared memory, so that what the warps need
 // only before and after a part's tiles takes no registers while they run through them.
 // Every segment counts kPartCost more than its tiles when the tiles are shared out, in front of its first one: that is
-// what a team spends on starting its copies, its query and its sums. 64 ragged sequences of up to 16384 keys: 129 us
-// at a cost of 3, 122 at 5, 123 at 7; 256 of up to 1000 keys, D = 64: 32, 28.8 and 28.1.
+// what a team spends on starting its copies, its query and its sums. 256 ragged sequences of up to 1000 keys, 4 KV heads,
+// D = 64: 22.7 us at a cost of 4, 22.0 at 5, 21.4 at 6, 21.7 at 8; 64 of up to 16384, D = 128: 117.1, 117.2, 117.2, 117.8.
 struct Part {
     long long u, rem;      // before the part: of all, and of its sequence
     int b, L, hz, t0, t1;  // t0 == t1: no part
@@ -265,11 +285,12 @@ struct Part {
     Tiles tl;
 };
 // The part at p.u, p.rem of sequence p.b in a range that ends at `end`.
+template <int W>
 __device__ __forceinline__ void set_part(Part& p, const DecodeArgs& a, long long end) {
     p.t0 = p.t1 = 0;
     if (p.u >= end) return;
     p.L = length_of(a, p.b);
-    p.tl = tiles_of(a, p.L);
+    p.tl = tiles_of<W>(a, p.L);
     const int n = p.tl.n + kPartCost;
     int from;
     p.hz = (int)divide(p.rem, n, &from);
@@ -277,6 +298,7 @@ __device__ __forceinline__ void set_part(Part& p, const DecodeArgs& a, long long
     p.t0 = max(from - kPartCost, 0);
     p.t1 = max(from + p.len - kPartCost, 0);
 }
+template <int W>
 __device__ __forceinline__ void next_part(Part& p, const Part& q, const DecodeArgs& a, long long end) {
     p.t0 = p.t1 = 0;
     if (q.t0 == q.t1) return;
@@ -287,7 +309,7 @@ __device__ __forceinline__ void next_part(Part& p, const Part& q, const DecodeAr
         ++p.b;
         p.rem = 0;
     }
-    set_part(p, a, end);
+    set_part<W>(p, a, end);
 }
 
 template <bool B>
@@ -364,22 +386,26 @@ struct Stage {
 };
 
 // What a team's warps share.
+template <int W>
 struct Shared {
-    float m[kWarps][ROWS], l[kWarps][ROWS];  // of a part, by warp
-    int2 vis[2][ROWS];                       // the visible range of every row, of this part and of the last or next
-    long long sums[kWarps];
-    long long end;  // of the team's range
+    float m[W][ROWS], l[W][ROWS];  // of a part, by warp
+    int2 vis[2][ROWS];             // the visible range of every row, of this part and of the last or next
+    long long end;                 // of the team's range
     Part parts[2];
     Shares shares;
 };
 
+template <int W>
 __device__ __forceinline__ void sync_team(int team) {
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kThreads) : "memory");
+    if constexpr (W == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory");
 }
 
-// Exclusive sum over a team's threads, and the total.
-__device__ __forceinline__ long long team_sum(long long x, int thread, int team, long long* part, long long* total) {
-    const int lane = thread & 31, warp = thread >> 5;
+// Exclusive sum over a block's threads, and the total.
+__device__ __forceinline__ long long block_sum(long long x, long long* part, long long* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long s = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -387,7 +413,7 @@ __device__ __forceinline__ long long team_sum(long long x, int thread, int team,
         if (lane >= d) s += y;
     }
     if (lane == 31) part[warp] = s;
-    sync_team(team);
+    __syncthreads();
     long long before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -398,35 +424,37 @@ __device__ __forceinline__ long long team_sum(long long x, int thread, int team,
     return s - x + before;
 }
 
-// Finds the team's range of the tiles: its first part and its end. False: there is none. The costs are summed a chunk of
-// sequences at a time, one per thread; up to kThreads sequences take one pass.
-template <bool kWhole>
-__device__ __forceinline__ bool find_range(const DecodeArgs& a, Shared& sh, int thread, int team, int place) {
+// Finds the ranges of the block's teams: the first part and the end of each. False: there is none for this team. The
+// costs are summed a chunk of sequences at a time, one per thread; up to kThreads sequences take one pass.
+template <int W, bool kWhole>
+__device__ __forceinline__ bool find_range(const DecodeArgs& a, Shared<W>* teams, int team, int place, bool first) {
+    constexpr int kTeams = teams_of(W);
     const int H = a.Hkv * a.Z;
     if (kWhole) {
         if (place >= a.B * H) return false;
-        if (thread == 0) {
-            Part& p = sh.parts[0];
+        if (first) {
+            Part& p = teams[team].parts[0];
             p.u = p.rem = 0;
             p.b = place / H;
             p.hz = place % H;
             p.L = length_of(a, p.b);
-            p.tl = tiles_of(a, p.L);
+            p.tl = tiles_of<W>(a, p.L);
             p.t0 = 0;
             p.t1 = p.tl.n;
             p.len = 1;
-            sh.end = 1;
+            teams[team].end = 1;
         }
     } else {
+        __shared__ long long sums[kWarps];
         const auto cost_of = [&](int b) {
-            return b < a.B ? (long long)(tiles_of(a, length_of(a, b)).n + kPartCost) * H : 0ll;
+            return b < a.B ? (long long)(tiles_of<W>(a, length_of(a, b)).n + kPartCost) * H : 0ll;
         };
         long long total = 0, cost = 0, before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             long long all;
-            cost = cost_of(b0 + thread);
-            sync_team(team);
-            before = team_sum(cost, thread, team, sh.sums, &all);
+            cost = cost_of(b0 + (int)threadIdx.x);
+            if (b0 > 0) __syncthreads();
+            before = block_sum(cost, sums, &all);
             total += all;
         }
         // a grid that is larger than the tiles need uses its first places only
@@ -435,49 +463,55 @@ __device__ __forceinline__ bool find_range(const DecodeArgs& a, Shared& sh, int 
             total >= (long long)kMinTiles * all_places ? all_places : (int)((total + kMinTiles - 1) / kMinTiles);
         Shares shares;
         shares.per = divide(total, places, &shares.more);
-        if (thread == 0 && !a.by_segment) a.cut[place] = make_int4(-1, 0, 0, 0);
-        if (place >= places) return false;
-        if (thread == 0) sh.shares = shares;
-        const long long u0 = shares.begin(place);
+        if (first && !a.by_segment) a.cut[place] = make_int4(-1, 0, 0, 0);
+        if (first) teams[team].shares = shares;
         long long behind = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             long long all = total;
             if (a.B > kThreads) {  // one chunk's sums are still at hand
-                cost = cost_of(b0 + thread);
-                sync_team(team);
-                before = behind + team_sum(cost, thread, team, sh.sums, &all);
+                cost = cost_of(b0 + (int)threadIdx.x);
+                __syncthreads();
+                before = behind + block_sum(cost, sums, &all);
             }
-            if (before <= u0 && u0 < before + cost) {
-                sh.parts[0].u = u0;
-                sh.parts[0].rem = u0 - before;
-                sh.parts[0].b = b0 + thread;
-                sh.end = shares.begin(place + 1);
-                set_part(sh.parts[0], a, sh.end);
+            for (int t = 0; t < kTeams; ++t) {
+                const int at = t * (int)gridDim.x + (int)blockIdx.x;
+                const long long u0 = shares.begin(at);
+                if (at < places && before <= u0 && u0 < before + cost) {
+                    Part& p = teams[t].parts[0];
+                    p.u = u0;
+                    p.rem = u0 - before;
+                    p.b = b0 + (int)threadIdx.x;
+                    teams[t].end = shares.begin(at + 1);
+                }
             }
             behind += all;
-            if (u0 < behind) break;
         }
+        __syncthreads();
+        if (place >= places) return false;
+        if (first) set_part<W>(teams[team].parts[0], a, teams[team].end);
     }
     return true;
 }
 
-template <int D>
-constexpr int kTeamBytes = kWarps * (kStages * Stage<D>::kBytes + ROWS * D * (int)sizeof(float));
+// the rings of a team's warps, and where there are more than one their sums of a part
+template <int D, int W>
+constexpr int kTeamBytes = W * (kStages * Stage<D>::kBytes + (W > 1 ? ROWS * D * (int)sizeof(float) : 0));
 
-template <typename T, int D, bool kWhole>
-__global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const __grid_constant__ DecodeArgs a) {
+template <typename T, int D, int W, bool kWhole>
+__global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_constant__ DecodeArgs a) {
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
     // An output in FP16 shows the two roundings of a probability (1.7 times the error of the output's own rounding), one
     // in BF16 does not: for FP16 the first one's remainder is carried into the second (1.4 times, and 1 % of the time).
     constexpr bool kFine = is_half<T>;
     extern __shared__ __align__(16) uint8_t smem_of_block[];
-    __shared__ Shared shared_of_block[kTeams];
-    const int team = threadIdx.x / kThreads, thread = threadIdx.x % kThreads;
-    Shared& sh = shared_of_block[team];
-    uint8_t* smem = smem_of_block + team * kTeamBytes<D>;  // the rings, then the warps' sums of a part
-    float* sm_acc = reinterpret_cast<float*>(smem + kWarps * kStages * St::kBytes);  // [kWarps][ROWS][D]
-    const auto team_sync = [&] { sync_team(team); };
+    constexpr int kTile = tile_of(W);
+    __shared__ Shared<W> shared_of_block[teams_of(W)];
+    const int team = threadIdx.x / (32 * W), thread = threadIdx.x % (32 * W);
+    Shared<W>& sh = shared_of_block[team];
+    uint8_t* smem = smem_of_block + team * kTeamBytes<D, W>;  // the rings, then the warps' sums of a part
+    [[maybe_unused]] float* sm_acc = reinterpret_cast<float*>(smem + W * kStages * St::kBytes);  // [W][ROWS][D]
+    const auto team_sync = [&] { sync_team<W>(team); };
     const int place = team * (int)gridDim.x + (int)blockIdx.x;
 
     const int warp = thread >> 5, lane = thread & 31;
@@ -497,7 +531,7 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    if (!find_range<kWhole>(a, sh, thread, team, place)) return;
+    if (!find_range<W, kWhole>(a, shared_of_block, team, place, thread == 0)) return;
     team_sync();
 
     // ---- the copies of a part ----
@@ -534,7 +568,7 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
         issue(p, p.t0);
     };
     begin_copies(sh.parts[0], page_of(sh.parts[0], sh.parts[0].t0 + lane), page_of(sh.parts[0], sh.parts[0].t0 + 32 + lane));
-    if (thread == 0) next_part(sh.parts[1], sh.parts[0], a, sh.end);
+    if (thread == 0) next_part<W>(sh.parts[1], sh.parts[0], a, sh.end);
     team_sync();
 
     for (int turn = 0;; turn ^= 1) {
@@ -801,39 +835,58 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
 
         // ---- the next part's copies begin; then the warps' sums are joined ----
         begin_copies(ahead, page0, page1);
+        const bool begun = part.t0 == 0, done = begun && t1 == tl.n;
+        const size_t part_row = ((size_t)place * 2 + begun) * ROWS;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
             const int r = 2 * cq + t;
-            if (gq == 0) {
-                sh.m[warp][r] = m[t] * sc[t];
-                sh.l[warp][r] = l[t];
-            }
             // element 32 n + 4 gq + x: accumulator 2 n + x / 2, its row gq (x even: low nibbles) or gq + 8
+            float4 y[NG];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const float off = -8.f * psum[n][t];
-                *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) =
-                    make_float4(fmaf(acc[2 * n][t], 1.f / kLowUnit, off),
-                                fmaf(acc[2 * n][2 + t], 1.f / kHighUnit, off),
-                                fmaf(acc[2 * n + 1][t], 1.f / kLowUnit, off),
-                                fmaf(acc[2 * n + 1][2 + t], 1.f / kHighUnit, off));
+                y[n] = make_float4(fmaf(acc[2 * n][t], 1.f / kLowUnit, off), fmaf(acc[2 * n][2 + t], 1.f / kHighUnit, off),
+                                   fmaf(acc[2 * n + 1][t], 1.f / kLowUnit, off),
+                                   fmaf(acc[2 * n + 1][2 + t], 1.f / kHighUnit, off));
+            }
+            if constexpr (W > 1) {
+                if (gq == 0) {
+                    sh.m[warp][r] = m[t] * sc[t];
+                    sh.l[warp][r] = l[t];
+                }
+#pragma unroll
+                for (int n = 0; n < NG; ++n)
+                    *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) = y[n];
+            } else if (r0 + r < R) {
+                if (done) {
+                    const float f = l[t] > 0.f ? a.v_scale / l[t] : 0.f;
+                    const size_t at = (first_row + r0 + r) * D + 4 * gq;
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) put4<T>(a.o, at + 32 * n, y[n], f);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+                        *reinterpret_cast<float4*>(a.ws_acc + (part_row + r) * D + 32 * n + 4 * gq) = y[n];
+                    if (gq == 0) {
+                        a.ws_m[part_row + r] = m[t] * sc[t];
+                        a.ws_l[part_row + r] = l[t];
+                    }
+                }
             }
         }
         team_sync();
-        {
-            const bool begun = part.t0 == 0, done = begun && t1 == tl.n;
-            const size_t part_row = ((size_t)place * 2 + begun) * ROWS;
-            for (int x = thread; x < ROWS * D; x += kThreads) {
+        if constexpr (W > 1) {
+            for (int x = thread; x < ROWS * D; x += 32 * W) {
                 const int r = x / D, d = x % D;
                 if (r0 + r >= R) break;
                 float mx = -FLT_MAX;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sh.m[w][r]);
+                for (int w = 0; w < W; ++w) mx = fmaxf(mx, sh.m[w][r]);
                 float lt = 0.f, y = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = 0; w < W; ++w) {
                     const float f = ptx::ex2(sh.m[w][r] - mx);  // a warp that saw no key has sums of zero
                     lt = fmaf(f, sh.l[w][r], lt);
                     y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
@@ -848,21 +901,21 @@ __global__ void __launch_bounds__(kTeams * kThreads, 1) kv4_decode_kernel(const 
                     }
                 }
             }
-            if (!kWhole && thread == 0 && begun) {  // a whole segment has no list and no workspace
-                int4 cut = make_int4(-1, 0, 0, 0);
-                if (!done) {
-                    const int n = tl.n + kPartCost;
-                    cut = make_int4(part.b, part.hz, place, sh.shares.place_of(part.u - part.rem % n + n - 1));
-                }
-                if (a.by_segment)
-                    a.cut[part.b * (a.Hkv * a.Z) + part.hz] = cut;
-                else if (!done)
-                    a.cut[place] = cut;
-            }
-            team_sync();  // the part and the sums are read
-            if (thread == 0) next_part(sh.parts[turn], sh.parts[turn ^ 1], a, sh.end);
-            team_sync();
         }
+        if (!kWhole && thread == 0 && begun) {  // a whole segment has no list and no workspace
+            int4 cut = make_int4(-1, 0, 0, 0);
+            if (!done) {
+                const int n = tl.n + kPartCost;
+                cut = make_int4(part.b, part.hz, place, sh.shares.place_of(part.u - part.rem % n + n - 1));
+            }
+            if (a.by_segment)
+                a.cut[part.b * (a.Hkv * a.Z) + part.hz] = cut;
+            else if (!done)
+                a.cut[place] = cut;
+        }
+        team_sync();  // the part and the sums are read
+        if (thread == 0) next_part<W>(sh.parts[turn], sh.parts[turn ^ 1], a, sh.end);
+        team_sync();
     }
 }
 
@@ -968,42 +1021,53 @@ int sm_count() {
 
 int row_blocks(const Problem& p) { return (int)(((long long)p.G * p.M + ROWS - 1) / ROWS); }
 
-// Few short segments are left whole, one to a team: no sums of costs, no second kernel. 2 KV heads of one sequence,
-// D = 64: 300 keys (5 tiles) 5.5 us whole and 8.2 cut, 1000 keys (16 tiles) 9.0 and 8.4, 2000 keys 14.2 and 8.6; 64 KV
-// heads (8 sequences), D = 128: 6.9 and 10.5, 11.3 and 12.4, 17.6 and 14.5.
+// Few short segments are left whole, one to a team of four warps: no sums of costs, no second kernel. 2 KV heads of one
+// sequence, D = 64: 300 keys (5 tiles) 5.4 us whole and 8.2 cut, 1000 keys (16 tiles) 9.0 and 8.4, 2000 keys 14.2 and
+// 8.6; 64 KV heads (8 sequences), D = 128: 6.9 and 10.5, 11.3 and 12.4, 17.6 and 14.5.
+// Otherwise a team is one warp where a segment is cut into kManyParts parts or less on average, and four warps (a quarter
+// of the parts) where there are fewer segments. Microseconds with one and with four, D = 128: 8 segments of 131072 keys
+// 39.5 and 36.2; 16 of 4096 11.4 and 11.2; 32 of 32768 36.3 and 37.1; 64 of 2048 11.5 and 12.9; 128 of up to 8192 24.6 and
+// 25.1; 512 of up to 1500 23.2 and 24.5; at D = 64 29.0 and 27.4 (16 of 65536), 28.1 and 27.1 (32), 10.2 and 10.5 (64 of
+// 2048), 18.3 and 18.3 (512), 21.4 and 25.0 (1024 of up to 1000).
 struct Plan {
-    int blocks;
+    int blocks, warps;  // warps of a team
     bool whole;
 };
-constexpr int kWholeTiles = 16;
+constexpr int kWholeTiles = 16;  // of 64 keys
+constexpr int kManyParts = 32;
 
 // One block for every SM, fewer while the longest lengths could not give one team of each kMinTiles tiles.
 Plan plan_blocks(const Kv4Call& c) {
     const Problem& p = c.p;
-    long long tiles = ((long long)c.max_len + kTile - 1) / kTile;
-    if (p.window > 0) {
-        const long long span = (long long)p.window + p.M - 1 + (kTile - 1);
-        const long long wt = (span + kTile - 1) / kTile + ((long long)c.sinks + kTile - 1) / kTile;
-        if (wt < tiles) tiles = wt;
-    }
-    if (tiles < 1) tiles = 1;
     const long long segments = (long long)p.B * p.Hkv * row_blocks(p), sms = sm_count();
-    if (tiles <= kWholeTiles && segments <= sms * kTeams) return Plan{(int)(segments < sms ? segments : sms), true};
-    const long long want = ((tiles + kPartCost) * segments + kMinTiles - 1) / kMinTiles;
-    return Plan{(int)(want < sms ? want : sms), false};
+    const auto tiles_at = [&](int kTile) {
+        long long tiles = ((long long)c.max_len + kTile - 1) / kTile;
+        if (p.window > 0) {
+            const long long span = (long long)p.window + p.M - 1 + (kTile - 1);
+            const long long wt = (span + kTile - 1) / kTile + ((long long)c.sinks + kTile - 1) / kTile;
+            if (wt < tiles) tiles = wt;
+        }
+        return tiles < 1 ? 1 : tiles;
+    };
+    if (tiles_at(tile_of(4)) <= kWholeTiles && segments <= sms * teams_of(4))
+        return Plan{(int)(segments < sms ? segments : sms), 4, true};
+    const int W = segments * kManyParts >= sms * teams_of(1) ? 1 : 4;
+    const long long want = ((tiles_at(tile_of(W)) + kPartCost) * segments + kMinTiles - 1) / kMinTiles;
+    return Plan{(int)(want < sms ? want : sms), W, false};
 }
 
-template <typename T, int D, bool kWhole>
+template <typename T, int D, int W, bool kWhole>
 cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
-    constexpr int kSmem = kTeams * kTeamBytes<D>;
+    constexpr int kTeams = teams_of(W), kSmem = kTeams * kTeamBytes<D, W>;
     static PerDeviceOnce once;
     const cudaError_t e = once_per_device(once, [] {
-        return cudaFuncSetAttribute(kv4_decode_kernel<T, D, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        return cudaFuncSetAttribute(kv4_decode_kernel<T, D, W, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmem);
     });
     if (e != cudaSuccess) return e;
     const cudaError_t r =
-        launch_programmatic(kv4_decode_kernel<T, D, kWhole>, dim3((unsigned)blocks), kTeams * kThreads, s, a, kSmem);
-    if (r != cudaSuccess || a.whole) return r;
+        launch_programmatic(kv4_decode_kernel<T, D, W, kWhole>, dim3((unsigned)blocks), kThreads, s, a, kSmem);
+    if (r != cudaSuccess || kWhole) return r;
     const unsigned entries = (unsigned)(a.by_segment ? a.B * a.Hkv * a.Z : blocks * kTeams);
     const unsigned rows = (unsigned)(a.G * a.M < ROWS ? a.G * a.M : ROWS);
     const unsigned parts = (unsigned)(blocks * kTeams) / entries;  // of a segment, about
@@ -1012,12 +1076,18 @@ cudaError_t launch_t(const DecodeArgs& a, int blocks, cudaStream_t s) {
     return launch_programmatic(kv4_join_kernel<T, D, 4, false>, dim3(entries), 32 * 4, s, a);
 }
 
+template <typename T, int D>
+cudaError_t launch_w(const DecodeArgs& a, const Plan& plan, cudaStream_t s) {
+    if (plan.whole) return launch_t<T, D, 4, true>(a, plan.blocks, s);
+    return plan.warps == 4 ? launch_t<T, D, 4, false>(a, plan.blocks, s) : launch_t<T, D, 1, false>(a, plan.blocks, s);
+}
+
 template <typename T>
-cudaError_t launch_d(const DecodeArgs& a, int D, int blocks, cudaStream_t s) {
+cudaError_t launch_d(const DecodeArgs& a, int D, const Plan& plan, cudaStream_t s) {
     switch (D) {
-        case 32: return (a.whole ? launch_t<T, 32, true>(a, blocks, s) : launch_t<T, 32, false>(a, blocks, s));
-        case 64: return (a.whole ? launch_t<T, 64, true>(a, blocks, s) : launch_t<T, 64, false>(a, blocks, s));
-        default: return (a.whole ? launch_t<T, 128, true>(a, blocks, s) : launch_t<T, 128, false>(a, blocks, s));
+        case 32: return launch_w<T, 32>(a, plan, s);
+        case 64: return launch_w<T, 64>(a, plan, s);
+        default: return launch_w<T, 128>(a, plan, s);
     }
 }
 
@@ -1039,7 +1109,7 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
     const int64_t cover = (int64_t)max_pages * cache.page_size;
     const int64_t longest = cover < max_seq_len ? cover : max_seq_len;
     if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + ROWS - 1) / ROWS > 65535 ||
-        longest > kI32Max - kTile || (int64_t)cache.num_pages * (cache.page_size / 16) * Hkv > kI32Max)
+        longest > kI32Max - tile_of(4) || (int64_t)cache.num_pages * (cache.page_size / 16) * Hkv > kI32Max)
         return ATTN_ERR_OVERFLOW;
     if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
     if ((nq > 0 && (!q || !o)) || (ntab > 0 && !table) || (B > 0 && !lens)) return ATTN_ERR_NULL;
@@ -1074,26 +1144,27 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
 bool nothing_to_attend(const Kv4Call& c) { return c.max_len == 0 || c.c.num_pages == 0; }
 
 // Cut segments and their parts, two per team: [places] int4, then m, l and acc.
+int places_of(const Plan& plan) { return plan.blocks * teams_of(plan.warps); }
 size_t workspace_bytes(const Plan& plan, int D) {
-    return plan.whole ? 0 : (size_t)plan.blocks * kTeams * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
+    return plan.whole ? 0 : (size_t)places_of(plan) * (sizeof(int4) + (size_t)2 * ROWS * (2 + D) * sizeof(float));
 }
 
 int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void* o, void* ws, size_t ws_bytes,
         const Plan& plan, cudaStream_t s) {
     const Problem& p = c.p;
-    const int blocks = plan.blocks;
+    const int places = places_of(plan);
     if (!plan.whole) {  // (the cut segments' list has an entry per place, and is by segment only where it has room)
         if (!ws || ws_bytes < workspace_bytes(plan, p.D)) return ATTN_ERR_WORKSPACE;
         if (!aligned(ws, 16)) return ATTN_ERR_ALIGN;
     }
-    const size_t n = (size_t)blocks * kTeams * 2 * ROWS;
+    const size_t n = (size_t)places * 2 * ROWS;
     int4* cut = static_cast<int4*>(ws);
-    float* wm = plan.whole ? nullptr : reinterpret_cast<float*>(cut + (size_t)blocks * kTeams);
-    const int by_segment = (int64_t)p.B * p.Hkv * row_blocks(p) <= (int64_t)blocks * kTeams;
+    float* wm = plan.whole ? nullptr : reinterpret_cast<float*>(cut + places);
+    const int by_segment = (int64_t)p.B * p.Hkv * row_blocks(p) <= places;
     const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, by_segment, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
-                       c.max_pages, c.max_len, p.causal, p.window, c.sinks, plan.whole, p.scale_log2, c.v_descale};
+                       c.max_pages, c.max_len, p.causal, p.window, c.sinks, p.scale_log2, c.v_descale};
     const cudaError_t e =
-        p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, blocks, s) : launch_d<__half>(a, p.D, blocks, s);
+        p.dtype == ATTN_BF16 ? launch_d<__nv_bfloat16>(a, p.D, plan, s) : launch_d<__half>(a, p.D, plan, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -647,6 +647,24 @@ def test_decode_many_ragged_sequences(B, Hkv, most, D):
     check_decode(o, q, host, table, lens, most)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,M,D,ps,dtype,causal,window,sinks", [
+    (20, 12, 2, 2, 128, 16, BF16, True, 0, 0), (20, 12, 2, 2, 128, 64, FP16, True, 100, 20),
+    (400, 1, 1, 1, 64, 32, FP16, True, 0, 0), (70, 8, 1, 3, 32, 16, BF16, False, 333, 65),
+    (58, 3, 1, 1, 128, 128, BF16, True, 17, 0), (30, 4, 2, 5, 64, 16, FP16, True, 1, 3),
+    (800, 2, 1, 1, 32, 16, FP16, True, 600, 5)])
+def test_decode_more_segments_than_a_third_of_the_sms(B, Hq, Hkv, M, D, ps, dtype, causal, window, sinks):
+    """Segments to single warps: several row blocks, windows that begin anywhere, more sequences than a block's threads,
+    lengths of zero and one and below the rows."""
+    rng = np.random.default_rng(B + D)
+    most = 1700
+    lens = rng.integers(0, most, B).tolist()
+    lens[0], lens[3], lens[4], lens[5], lens[B - 1] = most, 0, 1, 2, 16
+    q, dev, host, table = case(B, lens, Hq, Hkv, M, D, ps, dtype)
+    o = run_decode(q, dev, table, lens, most, causal, window, sinks)
+    check_decode(o, q, host, table, lens, most, causal, window, sinks)
+    assert torch.equal(run_decode(q, dev, table, lens, most, causal, window, sinks), o)
+
+
 @pytest.mark.parametrize("cap", [1023, 1024, 1025])
 @pytest.mark.parametrize("B,Hq,Hkv", [(3, 4, 2), (228, 2, 2), (229, 2, 2)])
 def test_decode_on_both_sides_of_whole_segments(B, Hq, Hkv, cap):
