@@ -543,6 +543,7 @@ def extra_measurements(args, dev, stream, flush):
         # the grouped CUDA-core paged kernel (D = 32, a covering path)
         d32 = DECODE_GQA.with_(D=32, name="decode_gqa_b8_hq32_hkv8_m1_n8192_w4096_d32_bf16")
         out["decode_gqa_d32_paged16"] = paged_decode_measure(d32, 16, steps, dev, stream, flush)
+        out["decode_gqa_kv4_paged16"] = kv4_decode_measure(DECODE_GQA, 16, steps, dev, stream, flush)
     return out
 
 
@@ -727,6 +728,47 @@ def paged_decode_measure(w, page_size, steps, dev, stream, flush):
     return {"GB/s": round(gbs, 1), "us": round(ms * 1e3, 2), "cold_call_us": round(cold * 1e3, 2),
             "frac_of_hbm": round(gbs / pk["hbm_gbs"], 4), "peak_source": pk_src,
             "path": f"paged decode ({kernel} kernel), {page_size}-key pages, shuffled pool",
+            "shape": {"B": w.B, "Hq": w.Hq, "Hkv": w.Hkv, "M": w.M, "N": w.N, "window": w.window, "D": w.D}}
+
+
+def kv4_decode_measure(w, page_size, steps, dev, stream, flush):
+    """The decode workload over a 4-bit paged cache (attn_decode_paged_kv4), written by attn_kv4_append in
+    pages of `page_size` keys stored in a shuffled order. Bytes count the codes and scales of the visible keys."""
+    import numpy as np
+
+    import streaming_attention_gb300 as sa
+
+    q, k, v = workload_inputs(w)
+    npg = w.N // page_size
+    perm = torch.from_numpy(np.random.default_rng(w.seed).permutation(w.B * npg))
+    td = perm.reshape(w.B, npg).to(torch.int32).to(dev)
+    rows = [x.transpose(1, 2).reshape(w.B * w.N, w.Hkv, w.D).contiguous().to(dev) for x in (k, v)]
+    slots = (td.repeat_interleave(page_size, 1) * page_size
+             + torch.arange(w.N, device=dev, dtype=torch.int32) % page_size).reshape(-1).contiguous()
+    nbytes = 2 * w.B * w.Hkv * min(w.N, w.window or w.N) * (w.D // 2 + w.D // 32) + 2 * q.numel() * 2
+    l2 = torch.cuda.get_device_properties(dev).L2_cache_size
+    r = max(2, min(16, math.ceil(3 * l2 / nbytes) + 1))
+    sets = []
+    for _ in range(r):
+        cache = sa.kv4_cache(w.B * npg, w.Hkv, page_size, w.D, dev)
+        sa.attn_kv4_append(*rows, slots, *cache, 1.0, 1.0)
+        sets.append((q.to(dev), cache, torch.empty_like(q, device=dev)))
+    lens = torch.full((w.B,), w.N, dtype=torch.int32, device=dev)
+    nb = sa.attn_decode_paged_kv4_workspace_bytes(w.B, w.Hq, w.Hkv, w.M, w.D, page_size, npg, w.N, w.causal, w.window)
+    ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+    torch.cuda.synchronize()
+
+    def fn_on(t, st):
+        sa.attn_decode_paged_kv4(t[0], *t[1], td, lens, t[2], w.N, w.causal, w.window, workspace=ws, stream=st)
+
+    ms = time_steady(fn_on, sets, steps, 3, stream)
+    cold = statistics.median(time_graph(lambda st: fn_on(sets[0], st), steps, 3, flush))
+    gbs = nbytes / (ms * 1e-3) / 1e9
+    pk, pk_src = peaks()
+    return {"GB/s": round(gbs, 1), "us": round(ms * 1e3, 2), "cold_call_us": round(cold * 1e3, 2),
+            "frac_of_hbm": round(gbs / pk["hbm_gbs"], 4), "peak_source": pk_src,
+            "bytes": "4-bit codes and E4M3 scales of the visible keys + Q + O",
+            "path": f"paged decode, {page_size}-key pages, shuffled pool, 4-bit cache",
             "shape": {"B": w.B, "Hq": w.Hq, "Hkv": w.Hkv, "M": w.M, "N": w.N, "window": w.window, "D": w.D}}
 
 
