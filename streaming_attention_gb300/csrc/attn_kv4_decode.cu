@@ -36,17 +36,17 @@
 // instructions per 16 keys.) The scales are applied where there are fewer numbers than
 // elements: a key's to the sum of a group's 32 products, a value's to the
 // probabilities, once per group.
-// What bounds it: the expansion, 320 instructions of a warp per 16 keys of D = 128 on
-// pipes that the 21 matrix instructions among them share. 64 sequences of up to 16384
-// keys, 8192 on average, 8 KV heads (580 MB): 116 us, 5.0 TB/s, 74 % of the measured
-// copy bandwidth; with the copies left out it took 115 us. 12 warps of 168 registers
-// beat 16 of 128 (139 us where 12 took 122), 20 of 96 and 24 of 80: fewer registers
-// leave the compiler less to overlap in a warp. 16 query rows to a team, for more than
+// What bounds it: the expansion, about 310 instructions of a warp per 16 keys of D = 128
+// on pipes that the 21 matrix instructions among them share, issued in 55 of 100 cycles:
+// each waits for the one before. 64 sequences of up to 16384 keys, 8192 on average, 8 KV
+// heads (580 MB): 111 us, 5.2 TB/s, 77 % of the measured copy bandwidth. (Without its
+// copies a kernel of 122 us took 115.) 12 warps of 168 registers beat 16 of 128 (139 us
+// where 12 took 122), 20 of 96 and 24 of 80: fewer registers leave the compiler less to
+// overlap in a warp. 16 query rows to a team, for more than
 // 8, need 255 registers and leave 8 warps: 44.6 us for 16 sequences of 8192 keys with 16
 // rows each, and in two blocks of 8 rows 41.7. FP8 products (half the expansion) run at a
 // quarter of the rate and lose (144 us). The time moves by up to 8 % with the order in
-// which the compiler is given the same work: the values' scales are converted in front
-// of the softmax, where the matrix instructions leave room (117 us; behind it 121).
+// which the compiler is given the same work.
 // Rounded below 32 bits: Q to FP16 after scaling each row by a power of two to
 // maximum 2^14..2^15 (exact for elements above 2^-20 of the maximum), the
 // probabilities to FP16, kept 8 to 128 times too large to stay clear of its small
@@ -315,6 +315,10 @@ __device__ __forceinline__ void next_part(Part& p, const Part& q, const DecodeAr
 template <bool B>
 struct Flag {
     static constexpr bool value = B;
+};
+template <int N>
+struct Number {
+    static constexpr int value = N;
 };
 
 // One stage of a warp's ring: the codes and scales of 16 keys and values. Row `slot` of the S^T product's left
@@ -677,39 +681,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
 #pragma unroll
         for (int n = 0; n < NG; ++n) psum[n][0] = psum[n][1] = 0.f;
 
-        // One step: the 16 keys at j0, from the stage at st. `edge`: some row does not see some of them.
-        const auto step = [&](uint32_t st, int j0, auto edge_tag) {
+        // One step: N blocks of 16 keys, the first at j0, from the stages at st. `edge`: some row does not see some of
+        // them. Two blocks at a time wherever both are seen by every row: their products do not depend on each other, and
+        // one test of the maximum serves both (64 ragged sequences of up to 16384 keys: 111 us, 116 one at a time).
+        const auto step = [&](uint32_t st, auto n_tag, int j0, auto edge_tag) {
             constexpr bool edge = decltype(edge_tag)::value;
-            // the values' codes and scales are loaded with the keys', ahead of the branch below: the lane's are cq + 4 e
-            uint32_t v[4][(NG + 1) / 2], vs[4];
-            if constexpr (St::kSpread) load_shared(vs, st + at_vs);
+            constexpr int N = decltype(n_tag)::value;
+            uint32_t v[N][4][(NG + 1) / 2], vs[N][4];
+            const auto load_values = [&](int b) {  // the lane's are keys cq + 4 e
+                const uint32_t at = st + b * St::kBytes;
+                if constexpr (St::kSpread) load_shared(vs[b], at + at_vs);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (NG == 1)
-                    v[e][0] = load_shared_small<2>(st + at_v + 4 * e * St::kRow);
-                else
-                    load_shared(v[e], st + at_v + 4 * e * St::kRow);
-                if constexpr (!St::kSpread) vs[e] = load_shared_small<NG>(st + at_vs + 4 * e * NG);
-            }
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (NG == 1)
+                        v[b][e][0] = load_shared_small<2>(at + at_v + 4 * e * St::kRow);
+                    else
+                        load_shared(v[b][e], at + at_v + 4 * e * St::kRow);
+                    if constexpr (!St::kSpread) vs[b][e] = load_shared_small<NG>(at + at_vs + 4 * e * NG);
+                }
+            };
+            // of one block with the keys', ahead of the branch below; of two where registers allow, behind the keys' products
+            if constexpr (N == 1) load_values(0);
             // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
-            float s[4];
-            {
+            float s[N][4];
+#pragma unroll
+            for (int b = 0; b < N; ++b) {
+                const uint32_t at = st + b * St::kBytes;
                 uint32_t k0[NG], k1[NG], e0[2], e1[2];
-                load_shared(k0, st + at_k);
-                load_shared(k1, st + at_k + 8 * St::kRow);
+                load_shared(k0, at + at_k);
+                load_shared(k1, at + at_k + 8 * St::kRow);
                 uint32_t ks[2];
                 if constexpr (St::kSpread) {
-                    load_shared(ks, st + at_ks);
+                    load_shared(ks, at + at_ks);
                 } else {
-                    ks[0] = load_shared_small<NG>(st + at_ks);
-                    ks[1] = load_shared_small<NG>(st + at_ks + 8 * NG);
+                    ks[0] = load_shared_small<NG>(at + at_ks);
+                    ks[1] = load_shared_small<NG>(at + at_ks + 8 * NG);
                 }
                 e4m3x4(ks[0], e0[0], e0[1]);
                 e4m3x4(ks[1], e1[0], e1[1]);
                 const float2 f0[2] = {halves(e0[0]), halves(e0[1])}, f1[2] = {halves(e1[0]), halves(e1[1])};
                 const uint32_t g0 = cq & 1 ? e0[1] : e0[0], g1 = cq & 1 ? e1[1] : e1[0];
                 const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(s, g0, g1, g0, g1, start[0], start[1], zero);
+                mma_16816(s[b], g0, g1, g0, g1, start[0], start[1], zero);
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
                     const uint32_t h0 = k0[n] >> 8, h1 = k1[n] >> 8;
@@ -718,31 +731,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     mma_16816(x, k0[n] & kLow, k1[n] & kLow, k0[n] & kHigh, k1[n] & kHigh, qf[n][0][0], qf[n][0][1], zero);
                     mma_16816(x, h0 & kLow, h1 & kLow, h0 & kHigh, h1 & kHigh, qf[n][1][0], qf[n][1][1], x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[e] = fmaf(x[e], e < 2 ? y0 : y1, s[e]);
+                    for (int e = 0; e < 4; ++e) s[b][e] = fmaf(x[e], e < 2 ? y0 : y1, s[b][e]);
                 }
+            }
+            uint32_t f0[N][4], f1[N][4];
+            const auto convert = [&](int b) {  // the values' scales as halves, those of a pair of keys side by side
+                e4m3x4(__byte_perm(vs[b][0], vs[b][1], 0x5140u), f0[b][0], f0[b][1]);
+                e4m3x4(__byte_perm(vs[b][2], vs[b][3], 0x5140u), f1[b][0], f1[b][1]);
+                e4m3x4(__byte_perm(vs[b][0], vs[b][1], 0x7362u), f0[b][2], f0[b][3]);
+                e4m3x4(__byte_perm(vs[b][2], vs[b][3], 0x7362u), f1[b][2], f1[b][3]);
+            };
+            if constexpr (N == 1) {
+                convert(0);
+            } else {
+#pragma unroll
+                for (int b = 0; b < N; ++b) load_values(b);
             }
 
-            // the scales as halves, those of a pair of keys side by side
-            uint32_t f0[4], f1[4];
-            e4m3x4(__byte_perm(vs[0], vs[1], 0x5140u), f0[0], f0[1]);
-            e4m3x4(__byte_perm(vs[2], vs[3], 0x5140u), f1[0], f1[1]);
-            e4m3x4(__byte_perm(vs[0], vs[1], 0x7362u), f0[2], f0[3]);
-            e4m3x4(__byte_perm(vs[2], vs[3], 0x7362u), f1[2], f1[3]);
-            // ---- softmax: s[0..1] is slot gq of rows 2 cq, 2 cq + 1; s[2..3] slot gq + 8 ----
+            // ---- softmax: s[b][0..1] is slot gq of rows 2 cq, 2 cq + 1; s[b][2..3] slot gq + 8 ----
             bool rises = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (edge) {
-                    const int j = j0 + key_slot + 8 * (e >> 1);
-                    const int2 vis = sh.vis[turn][2 * cq + (e & 1)];
-                    if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[e] = -INFINITY;  // a masked key scores -inf
+            for (int b = 0; b < N; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (edge) {
+                        const int j = j0 + key_slot + 8 * (e >> 1);
+                        const int2 vis = sh.vis[turn][2 * cq + (e & 1)];
+                        if (!(j < vis.y && (j >= vis.x || j < a.sinks))) s[b][e] = -INFINITY;  // a masked key scores -inf
+                    }
+                    rises |= s[b][e] > limit[e & 1];
                 }
-                rises |= s[e] > limit[e & 1];
-            }
             if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(m[e], fmaxf(s[e], s[2 + e]));
+                    float mx = m[e];
+#pragma unroll
+                    for (int b = 0; b < N; ++b) mx = fmaxf(mx, fmaxf(s[b][e], s[b][2 + e]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                     const float alpha = ptx::ex2((m[e] - mx) * sc[e]);
@@ -761,43 +785,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     for (int n = 0; n < NG; ++n) psum[n][e] *= alpha;
                 }
             }
-            fma2(s[0], s[1], sc, mu);
-            fma2(s[2], s[3], sc, mu);
+            uint32_t pb0[N], pb1[N];
+            [[maybe_unused]] uint32_t rest0[N], rest1[N];  // what the rounding of P left
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = ptx::ex2(s[e]);
-            const uint32_t h0 = ptx::pack_f16(s[0], s[1]), h1 = ptx::pack_f16(s[2], s[3]);
-            const uint32_t pb0 = transpose8(h0), pb1 = transpose8(h1);
-            [[maybe_unused]] uint32_t rest0 = 0, rest1 = 0;  // what the rounding of P left
-            if constexpr (kFine) {
-                const float2 y0 = halves(h0), y1 = halves(h1);
-                rest0 = transpose8(ptx::pack_f16(s[0] - y0.x, s[1] - y0.y));
-                rest1 = transpose8(ptx::pack_f16(s[2] - y1.x, s[3] - y1.y));
+            for (int b = 0; b < N; ++b) {
+                fma2(s[b][0], s[b][1], sc, mu);
+                fma2(s[b][2], s[b][3], sc, mu);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[b][e] = ptx::ex2(s[b][e]);
+                const uint32_t h0 = ptx::pack_f16(s[b][0], s[b][1]), h1 = ptx::pack_f16(s[b][2], s[b][3]);
+                pb0[b] = transpose8(h0);
+                pb1[b] = transpose8(h1);
+                if constexpr (kFine) {
+                    const float2 y0 = halves(h0), y1 = halves(h1);
+                    rest0[b] = transpose8(ptx::pack_f16(s[b][0] - y0.x, s[b][1] - y0.y));
+                    rest1[b] = transpose8(ptx::pack_f16(s[b][2] - y1.x, s[b][3] - y1.y));
+                }
+                add2(l[0], l[1], s[b][0], s[b][1]);
+                add2(l[0], l[1], s[b][2], s[b][3]);
             }
-            add2(l[0], l[1], s[0], s[1]);
-            add2(l[0], l[1], s[2], s[3]);
 
             // ---- O^T += V^T (P s)^T ----
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                // the unit of group n of both keys of a pair: its low byte and its high byte
-                const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
-                const uint32_t u0 = __byte_perm(v[0][n / 2], v[1][n / 2], lo), u1 = __byte_perm(v[2][n / 2], v[3][n / 2], lo);
-                const uint32_t h0 = __byte_perm(v[0][n / 2], v[1][n / 2], hi), h1 = __byte_perm(v[2][n / 2], v[3][n / 2], hi);
-                uint32_t p0, p1;
-                if constexpr (kFine) {
-                    p0 = hfma2(pb0, f0[n], hmul2(rest0, f0[n]));
-                    p1 = hfma2(pb1, f1[n], hmul2(rest1, f1[n]));
-                } else {
-                    p0 = hmul2(pb0, f0[n]);
-                    p1 = hmul2(pb1, f1[n]);
+            for (int b = 0; b < N; ++b) {
+                if constexpr (N > 1) {
+                    convert(b);
                 }
-                float (&lo_acc)[4] = acc[2 * n], (&hi_acc)[4] = acc[2 * n + 1];
-                mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
-                mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
-                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-                float x[4];
-                mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, zero);
-                add2(psum[n][0], psum[n][1], x[0], x[1]);
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    // the unit of group n of both keys of a pair: its low byte and its high byte
+                    const uint32_t lo = n & 1 ? 0x7632u : 0x5410u, hi = n & 1 ? 0x0703u : 0x0501u;
+                    const auto& w = v[b];
+                    const uint32_t u0 = __byte_perm(w[0][n / 2], w[1][n / 2], lo), u1 = __byte_perm(w[2][n / 2], w[3][n / 2], lo);
+                    const uint32_t h0 = __byte_perm(w[0][n / 2], w[1][n / 2], hi), h1 = __byte_perm(w[2][n / 2], w[3][n / 2], hi);
+                    uint32_t p0, p1;
+                    if constexpr (kFine) {
+                        p0 = hfma2(pb0[b], f0[b][n], hmul2(rest0[b], f0[b][n]));
+                        p1 = hfma2(pb1[b], f1[b][n], hmul2(rest1[b], f1[b][n]));
+                    } else {
+                        p0 = hmul2(pb0[b], f0[b][n]);
+                        p1 = hmul2(pb1[b], f1[b][n]);
+                    }
+                    float (&lo_acc)[4] = acc[2 * n], (&hi_acc)[4] = acc[2 * n + 1];
+                    mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, p0, p1, lo_acc);
+                    mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, p0, p1, hi_acc);
+                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                    float x[4];
+                    mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, zero);
+                    add2(psum[n][0], psum[n][1], x[0], x[1]);
+                }
             }
         };
 
@@ -815,12 +851,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
             }
             __syncwarp();
         };
+        const auto full = [&](int j0) { return j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks); };
         const auto any_step = [&](uint32_t st, int j0) {
-            if (j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks))
-                step(st, j0, Flag<false>());
-            else if (j0 < L) {
+            if (full(j0)) {
+                step(st, Number<1>(), j0, Flag<false>());
+            } else if (j0 < L) {
                 hide(st, j0);
-                step(st, j0, Flag<true>());
+                step(st, Number<1>(), j0, Flag<true>());
             }
         };
         for (int t = part.t0; t < t1; t += 2) {
@@ -829,8 +866,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
             issue(part, t + 2);  // into the half that was read in the last turn
             copy_wait<1>();
             __syncwarp();
-            any_step(st, tl.at(t) * kTile + warp * 16);
-            if (t + 1 < t1) any_step(st + St::kBytes, tl.at(t + 1) * kTile + warp * 16);
+            const int j0 = tl.at(t) * kTile + warp * 16, j1 = tl.at(t + 1) * kTile + warp * 16;
+            if (t + 1 < t1 && full(j0) && full(j1)) {
+                step(st, Number<2>(), j0, Flag<false>());
+            } else {
+                any_step(st, j0);
+                if (t + 1 < t1) any_step(st + St::kBytes, j1);
+            }
         }
 
         // ---- the next part's copies begin; then the warps' sums are joined ----
