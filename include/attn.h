@@ -473,7 +473,7 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  *   j < sinks. <= 0: none; without a window it changes nothing.
  * The values of the cache enter the products exactly; the query is rounded to
  * FP16 relative to its row's largest element and the probabilities to FP16 before
- * and after their product with a scale (for FP16 outputs after it), all sums are
+ * and after their product with a scale (for FP16 outputs at most after it), all sums are
  * FP32. Pages need not be clean: rows that no query row sees (behind a
  * sequence's end, or in front of its window and no sinks) may hold anything. A
  * table entry outside [0, num_pages) reads a page of zeros.

@@ -52,7 +52,7 @@
 // probabilities to FP16, kept 8 to 128 times too large to stay clear of its small
 // numbers (the row sum adds them unrounded), and their products with the values' scales
 // (2^-9 .. 448, so between 2^-6 and 57344 at the largest score) to FP16; with FP16
-// outputs the former rounding's remainder is not lost.
+// outputs less is lost (kFine).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -164,7 +164,7 @@ __device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*re
 // Bits 0..3 and 4..7 of both halves: n 2^-24 and n 2^-20 as FP16.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 constexpr float kLowUnit = 0x1p-24f, kHighUnit = 0x1p-20f;
-constexpr uint32_t kOnes = 0x3C003C00u;
+constexpr uint32_t kOnes = 0x3C003C00u, kMinus = 0x80008000u;
 
 // shared memory by its 32-bit address
 __device__ __forceinline__ void load_shared(uint32_t (&w)[4], uint32_t at) {
@@ -506,8 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
     using St = Stage<D>;
     constexpr int NG = D / kKv4Group;
     // An output in FP16 shows the two roundings of a probability (1.7 times the error of the output's own rounding), one
-    // in BF16 does not: for FP16 the first one's remainder is carried into the second (1.4 times, and 1 % of the time).
-    constexpr bool kFine = is_half<T>;
+    // in BF16 does not. For FP16 the first one's remainder is carried into the second (1.4 times, and 1 % of the time).
+    // Whole segments, whose time is mostly latency, multiply the second one's remainder too (1.0 times: 300 keys 5.6 us
+    // for 5.3, 8 sequences of up to 1000 keys, D = 128, 11.9 for 10.6); for 16 sequences of 8192 keys with 16 rows each
+    // that would be 46.6 us for 39.5.
+    constexpr bool kFine = is_half<T>, kFinest = kFine && kWhole;
     extern __shared__ __align__(16) uint8_t smem_of_block[];
     constexpr int kTile = tile_of(W);
     __shared__ Shared<W> shared_of_block[teams_of(W)];
@@ -819,9 +822,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     const uint32_t u0 = __byte_perm(w[0][n / 2], w[1][n / 2], lo), u1 = __byte_perm(w[2][n / 2], w[3][n / 2], lo);
                     const uint32_t h0 = __byte_perm(w[0][n / 2], w[1][n / 2], hi), h1 = __byte_perm(w[2][n / 2], w[3][n / 2], hi);
                     uint32_t p0, p1;
+                    [[maybe_unused]] uint32_t left0, left1;  // what the rounding of P s left
                     if constexpr (kFine) {
                         p0 = hfma2(pb0[b], f0[b][n], hmul2(rest0[b], f0[b][n]));
                         p1 = hfma2(pb1[b], f1[b][n], hmul2(rest1[b], f1[b][n]));
+                        if constexpr (kFinest) {
+                            left0 = hfma2(rest0[b], f0[b][n], hfma2(pb0[b], f0[b][n], p0 ^ kMinus));
+                            left1 = hfma2(rest1[b], f1[b][n], hfma2(pb1[b], f1[b][n], p1 ^ kMinus));
+                        }
                     } else {
                         p0 = hmul2(pb0[b], f0[b][n]);
                         p1 = hmul2(pb1[b], f1[b][n]);
@@ -832,6 +840,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
                     float x[4];
                     mma_16816(x, kOnes, kOnes, kOnes, kOnes, p0, p1, zero);
+                    if constexpr (kFinest) {
+                        mma_16816(lo_acc, u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh, left0, left1, lo_acc);
+                        mma_16816(hi_acc, h0 & kLow, h0 & kHigh, h1 & kLow, h1 & kHigh, left0, left1, hi_acc);
+                        mma_16816(x, kOnes, kOnes, kOnes, kOnes, left0, left1, x);
+                    }
                     add2(psum[n][0], psum[n][1], x[0], x[1]);
                 }
             }

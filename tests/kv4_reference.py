@@ -95,6 +95,7 @@ def attention(q, k, v, causal, window, sinks, scale, out_dtype, ku=None, vu=None
                                                        L 2 * 2^-25 8 vd / 2^3 max(1, s)
       With FP16 outputs the first rounding's remainder (itself rounded, 2^-11 of 2^-11) is multiplied by the scale and
       added before the second: 2^-11 + 2 * 2^-22 in all, and one product more that may be small (3 in place of 2).
+      (Short sequences carry the second rounding's remainder too; they are held to the same bound.)
       FP32 sums over the keys, 16 a matrix instruction (L/16 + 64) 2^-23 23 sum w vu
       the logits: the query's small elements (2^-25 of the row's largest), FP32 sums over D (truncating
       adders counted: 2^-23 a term) of up to 23 ku |q| each, and the exponent's argument; a logit's error
