@@ -151,13 +151,13 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(AppendArgs a) {
     for (int x = 0; x < kAppendRows; ++x) {
         const int t = first + x * (kThreads / U);
         const bool in = t < a.T;
-        slot[x] = in ? __ldg(a.slots + t) : -1;
+        slot[x] = in ? load_global(a.slots + t) : -1;
         if (slot[x] >= (long long)a.c.num_pages * ps) slot[x] = -1;
         // read whether the row has a slot or not: the loads need not wait for it
         wk[x] = wv[x] = make_uint4(0, 0, 0, 0);
         if (in) {
-            wk[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + h * D + u * 8));
-            wv[x] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + h * D + u * 8));
+            wk[x] = load_global(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.k) + t * a.k_stride + h * D + u * 8));
+            wv[x] = load_global(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.v) + t * a.v_stride + h * D + u * 8));
         }
     }
 #pragma unroll
@@ -268,13 +268,13 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(GatherArgs a) {
     const int first = (int)blockIdx.x * (kGatherRows * (kThreads / U)) + (int)threadIdx.x / U;
     const int ps = a.c.page_size;
     const int vword = NG > 1 ? ((2 * c + (odd ? 1 : 0)) * NG + (i & ~1)) / 2 : c;
-    const int L = min(__ldg(a.lens + b), a.N);
+    const int L = min(load_global(a.lens + b), a.N);
     int page[kGatherRows];
 #pragma unroll
     for (int x = 0; x < kGatherRows; ++x) {
         const int j = first + x * (kThreads / U);
         const int n = page_index(j, ps, a.ps_shift);
-        page[x] = j < L && n < a.max_pages ? __ldg(a.table + (size_t)b * a.max_pages + n) : -1;
+        page[x] = j < L && n < a.max_pages ? load_global(a.table + (size_t)b * a.max_pages + n) : -1;
         if (page[x] >= a.c.num_pages) page[x] = -1;
     }
     // a row behind the sequence, or on a page outside the pool, is zeros
@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(GatherArgs a) {
         if (page[x] >= 0) {
             const int j = first + x * (kThreads / U);
             const size_t at = ((size_t)page[x] * a.Hkv + h) * ps + (j - page_index(j, ps, a.ps_shift) * ps);
-            ck[x] = __ldg(reinterpret_cast<const uint32_t*>(a.c.k_codes + at * (D / 2)) + c * NG + i);
-            cv[x] = __ldg(reinterpret_cast<const uint32_t*>(a.c.v_codes + at * (D / 2)) + vword);
-            sk[x] = __ldg(a.c.k_scales + at * NG + i);
-            sv[x] = __ldg(a.c.v_scales + at * NG + i);
+            ck[x] = load_global(reinterpret_cast<const uint32_t*>(a.c.k_codes + at * (D / 2)) + c * NG + i);
+            cv[x] = load_global(reinterpret_cast<const uint32_t*>(a.c.v_codes + at * (D / 2)) + vword);
+            sk[x] = load_global(a.c.k_scales + at * NG + i);
+            sv[x] = load_global(a.c.v_scales + at * NG + i);
         }
     }
 #pragma unroll

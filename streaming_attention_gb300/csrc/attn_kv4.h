@@ -47,6 +47,13 @@ inline bool kv4_descale(float x) {
     return (b.u & 0x007FFFFFu) == 0 && e >= 127 - 64 && e <= 127 + 64;
 }
 
+// A load of what kernels in front of this one may have written. Not a non-coherent one: those want data that nothing
+// writes from the kernel's start on, and this one may have started before the kernel in front had ended.
+template <class T>
+__device__ __forceinline__ T load_global(const T* p) {
+    return *p;
+}
+
 // Launches a kernel that may start while the one in front of it in the stream runs, and waits for its end itself
 // (griddepcontrol.wait) before it touches memory.
 template <class Args>

@@ -118,7 +118,7 @@ __device__ __forceinline__ Tiles tiles_of(const DecodeArgs& a, int L) {
     return t;
 }
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
-    return min(max(__ldg(a.lens + b), 0), a.max_len);
+    return min(max(load_global(a.lens + b), 0), a.max_len);
 }
 
 // D = A B + C, FP16 in, FP32 out; the left operand's four registers one by one
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
     uint32_t fill = 0;  // the half of the ring that is filled next, in bytes
     const auto page_of = [&](const Part& p, int t) {
         const int j = p.tl.at(t) * kTile + warp * 16;
-        return t < p.t1 && j < p.L ? __ldg(a.table + (size_t)p.b * a.max_pages + j / ps) : -1;
+        return t < p.t1 && j < p.L ? load_global(a.table + (size_t)p.b * a.max_pages + j / ps) : -1;
     };
     const auto block_of = [&](const Part& p, int page, int t) {  // -1: a page outside the pool, or nothing to read
         const int j = p.tl.at(t) * kTile + warp * 16, g = p.hz / a.Z;
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
             const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q) + (first_row + (row ? r : 0)) * (D / 2) + cq * 4;
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                const uint4 w = row ? __ldg(reinterpret_cast<const uint4*>(qrow + n * 16)) : make_uint4(0, 0, 0, 0);
+                const uint4 w = row ? load_global(reinterpret_cast<const uint4*>(qrow + n * 16)) : make_uint4(0, 0, 0, 0);
                 const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
         long long s = 0, f = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            c[k] = b + k < a.B ? (uint32_t)max(__ldg(a.cached + b + k), 0) : 0;
-            n[k] = b + k < a.B ? (uint32_t)max(__ldg(a.fresh + b + k), 0) : 0;
+            c[k] = b + k < a.B ? (uint32_t)max(load_global(a.cached + b + k), 0) : 0;
+            n[k] = b + k < a.B ? (uint32_t)max(load_global(a.fresh + b + k), 0) : 0;
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
         for (long long x = pages + mine; x < page_end; x += step) {
             const int e = last_not_above(first, live, (int)x);
             const int k = old[e] + ((int)x - first[e]);
-            a.table[(size_t)(b0 + e) * a.max_pages + k] = x < a.num_free ? __ldg(a.free_pages + x) : -1;
+            a.table[(size_t)(b0 + e) * a.max_pages + k] = x < a.num_free ? load_global(a.free_pages + x) : -1;
         }
         const long long row_end = min(rows + chunk_rows, (long long)a.num_rows);
         for (long long r = rows + mine; r < row_end; r += step) {
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
                 page = a.table[(size_t)(b0 + e) * a.max_pages + k];
             } else if (k < (uint32_t)a.max_pages) {
                 const long long x = (long long)first[e] + (k - (uint32_t)old[e]);
-                if (x < a.num_free) page = __ldg(a.free_pages + x);
+                if (x < a.num_free) page = load_global(a.free_pages + x);
             }
             const long long slot = (long long)page * a.page_size + (pos - k * (uint32_t)a.page_size);
             a.slots[r] = page >= 0 && slot <= kI32Max ? (int)slot : -1;
