@@ -88,8 +88,8 @@ struct DecodeArgs {
     const int* lens;
     void* o;
     float *ws_m, *ws_l, *ws_acc;  // [places][2][ROWS], the same, [places][2][ROWS][D]
-    int4* cut;  // segments that are in parts (b, head * Z + z, first and last place; b < 0: none): by segment, [segments],
-                // or where there are more segments than places by the place that begins one, [places]
+    int4* cut;  // segments that are in parts (b, head * Z + z, first and last place; b < 0: none): by segment,
+                // [segments], or where there are more segments than places by the place that begins one, [places]
     int by_segment;
     int B, Hq, Hkv, M, G, Z;
     int max_pages, max_len;
@@ -276,8 +276,9 @@ struct Shares {
 // The part of a segment that a block is at: tiles [t0, t1) of it. Kept in shared memory, so that what the warps need
 // only before and after a part's tiles takes no registers while they run through them.
 // Every segment counts kPartCost more than its tiles when the tiles are shared out, in front of its first one: that is
-// what a team spends on starting its copies, its query and its sums. 256 ragged sequences of up to 1000 keys, 4 KV heads,
-// D = 64: 22.7 us at a cost of 4, 22.0 at 5, 21.4 at 6, 21.7 at 8; 64 of up to 16384, D = 128: 117.1, 117.2, 117.2, 117.8.
+// what a team spends on starting its copies, its query and its sums. 256 ragged sequences of up to 1000 keys, 4 KV
+// heads, D = 64: 22.8 us at a cost of 4, 22.0 at 5, 21.2 at 6, 21.0 at 8; 64 of up to 16384, 8 KV heads, D = 128:
+// 112.3, 111.6, 110.9, 111.3.
 struct Part {
     long long u, rem;      // before the part: of all, and of its sequence
     int b, L, hz, t0, t1;  // t0 == t1: no part
@@ -597,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                                                            cq * 128));
         }
 
-        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that), negated
-        // if the logit scale is negative.
+        // Q^T fragments, each row scaled to maximum 2^14..2^15 (the elements that meet high nibbles 2^-4 of that),
+        // negated if the logit scale is negative.
         // start: minus 8 times the rows' sums by group, each as the sum of four halves, as the right operand of a
         // product with the keys' scales (column k of that product's left operand is the scale of group k % 4).
         uint32_t qf[NG][2][2], start[2];
@@ -643,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                 sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], 1);
                 sums[n] += __shfl_xor_sync(0xffffffffu, sums[n], 2);
             }
-            // rows k of the right operand in this lane: 2 cq, 2 cq + 1 (term cq / 2 of two groups), and 8 further (term 2 more)
+            // rows k of the right operand in this lane: 2 cq, 2 cq + 1 (term cq / 2 of two groups), and 8 further (term
+            // 2 more)
             float two[2] = {-8.f * (cq & 1 ? sums[2] : sums[0]), -8.f * (cq & 1 ? sums[3] : sums[1])};
 #pragma unroll
             for (int term = 0; term < 4; ++term) {
@@ -667,8 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
         key_range(L - 1, L, a.causal, a.window, &all_lo, &skip);
         key_range(L - a.M, L, a.causal, a.window, &any_lo, &all_hi);
 
-        // m: the score that stands for the largest one so far, in units of sc: it is set anew only when a score exceeds it
-        // by kPSlack in base 2 (else every few steps some row's would be); limit: that border; mu: kPShift less m in base 2
+        // m: the score that stands for the largest one so far, in units of sc: it is set anew only when a score exceeds
+        // it by kPSlack in base 2 (else every few steps some row's would be); limit: that border; mu: kPShift less m in
+        // base 2
         float m[2], limit[2], mu[2], l[2], acc[2 * NG][4];
         float psum[NG][2];  // of the probabilities times a group's scales, as rounded for the products
 #pragma unroll
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     if constexpr (!St::kSpread) vs[b][e] = load_shared_small<NG>(at + at_vs + 4 * e * NG);
                 }
             };
-            // of one block with the keys', ahead of the branch below; of two where registers allow, behind the keys' products
+            // of one block with the keys', ahead of the branch below; of two behind the keys' products, for the registers
             if constexpr (N == 1) load_values(0);
             // ---- S^T = K Q^T, a group at a time: its 32 products' sum times the key's scale ----
             float s[N][4];
@@ -974,12 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
     }
 }
 
-// Joins the parts of the segment cut[blockIdx.x]: the part in its first place's second slot and those in the first slots
-// of the places behind it. The W warps take a row each, or share a row's parts where there are fewer rows, kJoinBatch at
-// a time; kRow: the block takes row blockIdx.y alone. What bounds this kernel is its launch and the chain of loads (cut,
-// then parts), so a block is as small as the number of parts lets it be. The whole decode of 64 segments in 7 parts each
-// took 18.2 us with 16 warps and all rows a block, 17.3 with 4 warps a row; of 8 segments in 57 parts 38.8 and, with 8
-// warps a row, 35.9; of 512 segments mostly in one part 122.4 and, with 4 warps a block, 118.3.
+// Joins the parts of the segment cut[blockIdx.x]: the part in its first place's second slot and those in the first
+// slots of the places behind it. The W warps take a row each, or share a row's parts where there are fewer rows,
+// kJoinBatch at a time; kRow: the block takes row blockIdx.y alone. What bounds this kernel is its launch and the chain
+// of loads (cut, then parts), so a block is as small as the number of parts lets it be. When this was chosen, a decode of
+// 64 segments in 7 parts each took 18.2 us with 16 warps and all rows a block and 17.3 with 4 warps a row; of 8 segments
+// in 57 parts 38.8 and, with 8 warps a row, 35.9; of 512 mostly in one part 122.4 and, with 4 warps a block, 118.3.
 constexpr int kJoinBatch = 8;
 
 template <typename T, int D, int W, bool kRow>
@@ -1076,14 +1079,14 @@ int sm_count() {
 
 int row_blocks(const Problem& p) { return (int)(((long long)p.G * p.M + ROWS - 1) / ROWS); }
 
-// Few short segments are left whole, one to a team of four warps: no sums of costs, no second kernel. 2 KV heads of one
-// sequence, D = 64: 300 keys (5 tiles) 5.4 us whole and 8.2 cut, 1000 keys (16 tiles) 9.0 and 8.4, 2000 keys 14.2 and
-// 8.6; 64 KV heads (8 sequences), D = 128: 6.9 and 10.5, 11.3 and 12.4, 17.6 and 14.5.
-// Otherwise a team is one warp where a segment is cut into kManyParts parts or less on average, and four warps (a quarter
-// of the parts) where there are fewer segments. Microseconds with one and with four, D = 128: 8 segments of 131072 keys
-// 39.5 and 36.2; 16 of 4096 11.4 and 11.2; 32 of 32768 36.3 and 37.1; 64 of 2048 11.5 and 12.9; 128 of up to 8192 24.6 and
-// 25.1; 512 of up to 1500 23.2 and 24.5; at D = 64 29.0 and 27.4 (16 of 65536), 28.1 and 27.1 (32), 10.2 and 10.5 (64 of
-// 2048), 18.3 and 18.3 (512), 21.4 and 25.0 (1024 of up to 1000).
+// Few short segments are left whole, one to a team of four warps: no sums of costs, no second kernel. Microseconds whole
+// and cut, 2 KV heads of one sequence, D = 64: 300 keys (5 tiles) 5.1 and 7.7, 1000 (16 tiles) 8.4 and 8.0, 2000 12.7 and
+// 8.1; 64 KV heads (8 sequences), D = 128: 6.9 and 10.5, 11.0 and 11.2, 16.6 and 13.2; 456 of 900 keys 17.2 and 23.0.
+// Otherwise a team is one warp where a segment is cut into kManyParts parts or less on average, and four warps (a
+// quarter of the parts) where there are fewer segments. With one and with four, D = 128: 8 segments of 131072 keys 38.6
+// and 35.6; 16 of 4096 11.3 and 11.1; 32 of 32768 35.4 and 36.7; 64 of 2048 11.4 and 12.9; 128 of up to 8192 24.2 and
+// 24.6; 512 of up to 16384 110.9 and 115.4; at D = 64 30.1 and 26.5 (8), 26.9 and 26.5 (32), 10.1 and 10.3 (64 of 2048),
+// 18.8 and 18.6 (128), 21.2 and 25.1 (1024 of up to 1000).
 struct Plan {
     int blocks, warps;  // warps of a team
     bool whole;
