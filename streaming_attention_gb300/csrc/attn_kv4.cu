@@ -59,7 +59,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // row; the 4 threads of a group share its maximum. A thread takes kAppendRows such
 // pieces, a block's width apart, with all their loads in flight at once: the chain
 // slot -> row -> store is what a thread waits for, and with one piece a thread the
-// kernel was bound by it.
+// kernel was bound by it. 16640 rows of 8 heads, D = 128, BF16 (68 MB read, 18 MB
+// written): 17.9 us, 4.8 TB/s, bound by memory and by the ALU (64 % of its pipe); with
+// one row a thread 19.9, with four 17.8 but 16 rows 2.2 us instead of 1.7.
 // ---------------------------------------------------------------------------
 constexpr int kAppendRows = 2;
 
@@ -197,7 +199,9 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(AppendArgs a) {
 
 // ---------------------------------------------------------------------------
 // gather: one thread writes 8 elements of a key row and the same 8 of the value row,
-// for kGatherRows rows a block's width apart, all their loads in flight at once.
+// for kGatherRows rows a block's width apart, all their loads in flight at once. Bound
+// by memory: 2 sequences of 32768 keys of 8 heads, D = 128 (340 MB): 54.1 us, 6.3 TB/s,
+// 93 % of the measured copy bandwidth; with two or eight rows a thread 53.7 and 54.3.
 // ---------------------------------------------------------------------------
 constexpr int kGatherRows = 4;
 
@@ -214,7 +218,7 @@ struct GatherArgs {
 // s (n - 8) of eight codes. Pairs: a byte b of the word times 0x1001 has its two nibbles at bits 0 and 16, where they
 // are small whole numbers under the exponent of 128 (BF16) or 1024 (FP16); n - 8 and its product with the scale are
 // exact in 16 bits (4 + 4 significant ones) where the scale times the factor is a normal number of T, which the caller
-// has seen to. 5 operations a pair; in 32 bits, for other factors, 10.
+// has seen to. 5 operations a pair; in 32 bits, for other factors, 10 (54.7 us where this takes 54.1).
 template <typename T>
 struct Pair;
 template <>

@@ -13,7 +13,8 @@
 // pages, whose request it finds by bisection in shared memory. No block reads a
 // table entry that another one writes: entries below old_b are only read, the
 // others only written (their page is computed from the free list instead).
-// Latency bounds it: loads, sums, bisection, loads, stores.
+// Latency bounds it: loads, sums, bisection, loads, stores. 64 requests of one new key
+// take 3.0 us, 2000 of 97 new keys 7.4.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -223,11 +224,12 @@ int attn_page_plan(const int* cached_lens, const int* new_lens, const int* free_
     }
     const PlanArgs a{cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats,
                      B, page_size, max_pages, num_free, num_rows};
-    // one row per thread, on at most one block per SM. Few requests take smaller blocks, whose sums are quicker; many take
-    // larger ones, and so fewer chunks one after the other.
+    // one row per thread, on at most one block per SM. Few requests take smaller blocks, whose sums are quicker; many
+    // take larger ones, and so fewer chunks one after the other: 64 requests 3.0 us in blocks of 256 threads and 4.8 in
+    // blocks of 1024, 256 3.1 and 5.0, 512 5.1 and 5.5, 2000 18.0 and 7.4.
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
-    const int threads = B <= 256 ? 256 : 1024;
+    const int threads = B <= 512 ? 256 : 1024;
     int64_t grid = ((int64_t)(num_rows > B ? num_rows : B) + threads - 1) / threads;
     if (grid > sms) grid = sms;
     if (grid < 1) grid = 1;
