@@ -402,7 +402,8 @@ def kv4_cache(num_pages, Hkv, page_size, D, device="cuda"):
 
 
 # These calls are small on the GPU (a few microseconds), so what surrounds them in Python is kept short: the stream is
-# taken as a number and pointers are passed as numbers.
+# taken as a number, pointers are passed as numbers and types are looked up once.
+_U8, _I32, _E4M3, _BF16, _FP16 = torch.uint8, torch.int32, torch.float8_e4m3fn, torch.bfloat16, torch.float16
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -430,21 +431,21 @@ def _device_of(first: torch.Tensor, *others) -> int:
 
 
 def _int32(name: str, t: torch.Tensor) -> None:
-    if t.dtype is not torch.int32 or not t.is_contiguous():
+    if t.dtype is not _I32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor")
 
 
 def _kv4_dims(k_codes, k_scales, v_codes, v_scales):
     shape = k_codes.shape
-    if len(shape) != 4 or k_codes.dtype is not torch.uint8 or v_codes.dtype is not torch.uint8:
+    if len(shape) != 4 or k_codes.dtype is not _U8 or v_codes.dtype is not _U8:
         raise ValueError("codes are uint8 [num_pages, Hkv, page_size, D/2]")
-    num_pages, Hkv, page_size, half = shape
     if v_codes.shape != shape:
         raise ValueError("k_codes and v_codes must have one shape")
+    num_pages, Hkv, page_size, half = shape
     want = (num_pages, Hkv, page_size, half // 16)
-    for t in (k_scales, v_scales):
-        if t.dtype is not torch.float8_e4m3fn or t.shape != want:
-            raise ValueError(f"scales are float8_e4m3fn [num_pages, Hkv, page_size, D/32] = {want}")
+    if (k_scales.dtype is not _E4M3 or v_scales.dtype is not _E4M3 or k_scales.shape != want
+            or v_scales.shape != want):
+        raise ValueError(f"scales are float8_e4m3fn [num_pages, Hkv, page_size, D/32] = {want}")
     if not (k_codes.is_contiguous() and k_scales.is_contiguous() and v_codes.is_contiguous()
             and v_scales.is_contiguous()):
         raise ValueError("the cache's tensors must be contiguous")
@@ -452,19 +453,22 @@ def _kv4_dims(k_codes, k_scales, v_codes, v_scales):
 
 
 def _one_dtype(what: str, x: torch.Tensor, y: torch.Tensor) -> int:
-    if x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16:
-        return ATTN_BF16
-    if x.dtype is torch.float16 and y.dtype is torch.float16:
-        return ATTN_FP16
+    dtype = x.dtype
+    if y.dtype is dtype:
+        if dtype is _BF16:
+            return ATTN_BF16
+        if dtype is _FP16:
+            return ATTN_FP16
     raise ValueError(f"{what} must share one dtype, bfloat16 or float16")
 
 
 def _tables(block_table, seq_lens, B: int) -> int:
     _int32("block_table", block_table)
     _int32("seq_lens", seq_lens)
-    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    return block_table.shape[1]
+    return shape[1]
 
 
 def attn_page_plan(cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats, page_size,
