@@ -484,7 +484,9 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  * faster way.
  *   workspace: device memory of attn_decode_paged_kv4_workspace_bytes(...)
  *   bytes, 16-byte aligned; NULL makes the call allocate it stream-ordered. The
- *   size is 0 for few short sequences (the workspace is then not read). */
+ *   size is 0 for few short sequences (the workspace is then not read), and it
+ *   does not fall as B, Hkv, Hq, M or max_seq_len rise: a workspace for the
+ *   largest call serves the smaller ones, one after the other. */
 ATTN_API size_t attn_decode_paged_kv4_workspace_bytes(int B, int Hq, int Hkv, int M, int D, int page_size,
                                                       int max_pages, int max_seq_len, int causal, int window,
                                                       int sinks);

@@ -64,6 +64,21 @@ def test_decode_workspace(L):
     assert sa.attn_decode_paged_kv4_workspace_bytes(1, 32, 8, 1, 128, 16, 8192, 0) == 0
 
 
+def test_decode_workspace_does_not_fall_with_larger_calls():
+    size = sa.attn_decode_paged_kv4_workspace_bytes
+    Bs, Hs, Ms = [1, 2, 14, 15, 57, 58, 152, 444, 445, 456, 457, 2000], [1, 2, 8], [1, 2, 9]
+    lens = [1, 64, 1000, 1024, 1025, 3000, 100000]
+    for window in (0, 1, 500):
+        n = {(B, H, M, N): size(B, 4 * H, H, M, 64, 16, 6250, N, True, window)
+             for B in Bs for H in Hs for M in Ms for N in lens}
+        for k, (axis, values) in enumerate((("B", Bs), ("Hkv", Hs), ("M", Ms), ("max_seq_len", lens))):
+            for key, got in n.items():
+                i = values.index(key[k])
+                if i + 1 < len(values):
+                    assert got <= n[key[:k] + (values[i + 1],) + key[k + 1:]], (axis, key, window)
+        assert max(n.values()) == n[Bs[-1], Hs[-1], Ms[-1], lens[-1]] > 0
+
+
 def append(L, k=at(0), v=at(1), slots=at(2), kc=at(3), ks=at(4), vc=at(5), vs=at(6), T=3, Hkv=2, D=128, kst=256, vst=256,
            pages=8, ps=16, kd=1.0, vd=1.0, dtype=0):
     return L.attn_kv4_append(k, v, slots, kc, ks, vc, vs, T, Hkv, D, kst, vst, pages, ps, kd, vd, dtype, None)

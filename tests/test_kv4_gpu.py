@@ -594,6 +594,28 @@ def test_decode_rows_no_query_sees_may_hold_anything(ps, M, sinks, D):
     assert torch.equal(run_decode(q, dev, table, lens, 512, True, window, sinks), want)
 
 
+@pytest.mark.parametrize("B,Hkv,window,sinks", [(3, 2, 0, 0), (3, 2, 1100, 21), (40, 2, 0, 0), (40, 2, 1100, 21)])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_decode_dirty_rows_of_cut_segments(B, Hkv, window, sinks, D):
+    """The same, and rows behind the sequences' ends, where segments are cut: teams of four warps and of one."""
+    rng = np.random.default_rng(B + D)
+    lens = rng.integers(1, 3001, B).tolist()
+    lens[0], lens[2] = 3000, 1101
+    q, dev, host, table = case(94, lens, 2 * Hkv, Hkv, 2, D, 32, BF16)
+    want = run_decode(q, dev, table, lens, 3000, True, window, sinks)
+    check_decode(want, q, host, table, lens, 3000, True, window, sinks)
+    seen = np.zeros(host[1].shape[:3:2], bool)
+    for b, L in enumerate(lens):
+        for j in range(L):
+            seen[table[b, j // 32], j % 32] = not window or j >= L - 2 - window + 1 or j < sinks
+    dead = torch.from_numpy(~seen).to(DEV)
+    for n in (1, 3):
+        dev[n].view(torch.uint8).permute(0, 2, 1, 3)[dead] = 0x7F  # E4M3 NaN
+    for n in (0, 2):
+        dev[n].permute(0, 2, 1, 3)[dead] = 0xF0
+    assert torch.equal(run_decode(q, dev, table, lens, 3000, True, window, sinks), want)
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 @pytest.mark.parametrize("dtype,kd,vd", [(BF16, 2.0 ** -64, 2.0 ** 64), (BF16, 2.0 ** 64, 2.0 ** -64),
                                          (FP16, 2.0 ** -5, 2.0 ** 7), (FP16, 2.0 ** -6, 1.0), (FP16, 1.0, 2.0 ** 8),
