@@ -445,6 +445,7 @@ ATTN_API int attn_page_plan(const int* cached_lens, const int* new_lens, const i
  *   s = E4M3(max|x| / 7.5), to nearest even, at most 448
  *   n = 8 + clamp(round(x / s), -8, 7), halves away from zero; 8 where s = 0
  * both exactly as written, for finite inputs, whatever their order of magnitude.
+ * A group with a NaN or an infinity gets a scale of NaN: it stands for 32 NaN.
  *   k, v: device [T, Hkv, D] of dtype (ATTN_BF16 / ATTN_FP16), 16-byte aligned,
  *   the D elements of a head and the heads of a row contiguous; k_stride and
  *   v_stride elements from one row to the next (at least Hkv * D, a multiple of
@@ -476,7 +477,8 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  * and after their product with a scale (for FP16 outputs at most after it), all sums are
  * FP32. Pages need not be clean: rows that no query row sees (behind a
  * sequence's end, or in front of its window and no sinks) may hold anything. A
- * table entry outside [0, num_pages) reads a page of zeros.
+ * table entry outside [0, num_pages) reads a page of zeros. NaN in a key that a
+ * row sees makes the row NaN, in a value the elements of its group.
  * D is 32, 64 or 128 (else ATTN_ERR_HEADDIM); B * Hkv <= 65535 and at most
  * 8 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
  * to 8 grouped rows read the cache once, more in blocks of 8 rows; for many

@@ -75,6 +75,12 @@ struct AppendArgs {
     float k_inv, v_inv;  // 1 / descale (a power of two)
 };
 
+// the larger one, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
 // max |x| of the 8 elements of four words, two halves at a time
 template <typename T2>
 __device__ __forceinline__ T2 as_pair(uint32_t w) {
@@ -85,16 +91,16 @@ __device__ __forceinline__ float largest(const uint32_t (&w)[4]);
 template <>
 __device__ __forceinline__ float largest<__nv_bfloat16>(const uint32_t (&w)[4]) {
     using P = __nv_bfloat162;
-    const P m = __hmax2(__hmax2(__habs2(as_pair<P>(w[0])), __habs2(as_pair<P>(w[1]))),
-                        __hmax2(__habs2(as_pair<P>(w[2])), __habs2(as_pair<P>(w[3]))));
-    return fmaxf(__low2float(m), __high2float(m));
+    const P m = __hmax2_nan(__hmax2_nan(__habs2(as_pair<P>(w[0])), __habs2(as_pair<P>(w[1]))),
+                        __hmax2_nan(__habs2(as_pair<P>(w[2])), __habs2(as_pair<P>(w[3]))));
+    return max_nan(__low2float(m), __high2float(m));
 }
 template <>
 __device__ __forceinline__ float largest<__half>(const uint32_t (&w)[4]) {
     using P = __half2;
-    const P m = __hmax2(__hmax2(__habs2(as_pair<P>(w[0])), __habs2(as_pair<P>(w[1]))),
-                        __hmax2(__habs2(as_pair<P>(w[2])), __habs2(as_pair<P>(w[3]))));
-    return fmaxf(__low2float(m), __high2float(m));
+    const P m = __hmax2_nan(__hmax2_nan(__habs2(as_pair<P>(w[0])), __habs2(as_pair<P>(w[1]))),
+                        __hmax2_nan(__habs2(as_pair<P>(w[2])), __habs2(as_pair<P>(w[3]))));
+    return max_nan(__low2float(m), __high2float(m));
 }
 
 // 8 elements -> 8 codes in one word (lowest element in the lowest bits) and the
@@ -109,13 +115,14 @@ __device__ __forceinline__ float largest<__half>(const uint32_t (&w)[4]) {
 //   of it away.
 //   The clamp to codes 0..15 is the saturation of (x / s + 8) / 15 to 0..1, which
 //   comes with the multiply-add.
-// inv, 1 / descale, is a power of two: x is scaled by way of r.
+// inv, 1 / descale, is a power of two: x is scaled by way of r. A NaN or an infinity among
+// the group's elements makes the scale NaN (the remainder of an infinite quotient is NaN).
 template <typename T>
 __device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_t* scale) {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
     float top = largest<T>(words);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * inv;
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2)) * inv;
     const float q = top * (1.0f / 7.5f);
     const uint32_t s =
         __nv_cvt_float_to_fp8(fmaf(fmaf(-7.5f, q, top), 1.0f / 7.5f, q), __NV_SATFINITE, __NV_E4M3);

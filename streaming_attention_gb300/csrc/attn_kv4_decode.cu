@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     *reinterpret_cast<float4*>(sm_acc + (warp * ROWS + r) * D + 32 * n + 4 * gq) = y[n];
             } else if (r0 + r < R) {
                 if (done) {
-                    const float f = l[t] > 0.f ? a.v_scale / l[t] : 0.f;
+                    const float f = l[t] != 0.f ? a.v_scale / l[t] : 0.f;
                     const size_t at = (first_row + r0 + r) * D + 4 * gq;
 #pragma unroll
                     for (int n = 0; n < NG; ++n) put4<T>(a.o, at + 32 * n, y[n], f);
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     y = fmaf(f, sm_acc[(w * ROWS + r) * D + d], y);
                 }
                 if (done) {
-                    put<T>(a.o, (first_row + r0 + r) * D + d, lt > 0.f ? y * (a.v_scale / lt) : 0.f);
+                    put<T>(a.o, (first_row + r0 + r) * D + d, lt != 0.f ? y * (a.v_scale / lt) : 0.f);
                 } else {
                     a.ws_acc[(part_row + r) * D + d] = y;
                     if (d == 0) {
@@ -1055,7 +1055,7 @@ __global__ void __launch_bounds__(32 * W) kv4_join_kernel(DecodeArgs a) {
         }
         if (r < rows && has) {
             const size_t at = (((size_t)cut.x * a.Hq + cut.y / a.Z * a.G) * a.M + r0 + r) * D + 4 * lane;
-            const float f = l > 0.f ? a.v_scale / l : 0.f;
+            const float f = l != 0.f ? a.v_scale / l : 0.f;
             put<T>(a.o, at, y.x * f);
             put<T>(a.o, at + 1, y.y * f);
             put<T>(a.o, at + 2, y.z * f);

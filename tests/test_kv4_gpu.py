@@ -192,6 +192,43 @@ def test_append_one_row_of_one_head_any_stride():
     assert np.array_equal(bytes_np(dev[3])[1, 0, 1], byte[0, 0])
 
 
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_groups_that_are_not_finite(D, dtype, bad):
+    """One such element makes its group NaN, in the cache, read back, and in the rows that see it; other groups, rows and
+    sequences, and rows whose window is past it, are as before. Rows without a slot may hold anything."""
+    rng = np.random.default_rng(95)
+    Hkv, ps, T, L = 2, 16, 200, 90  # two sequences of L keys, and rows without a slot
+    x = {w: torch.from_numpy(model_rows(rng, (T, Hkv, D), w)).to(dtype) for w in "kv"}
+    table = np.array([[3, 1, 4, 0, 9, 2], [6, 5, 11, 7, 10, 8]], np.int32)
+    slots = [int(table[j // L, j % L // ps]) * ps + j % L % ps for j in range(2 * L)] + [-1] * (T - 2 * L)
+    q = torch.from_numpy(rng.normal(size=(2, 2 * Hkv, 1, D))).to(dtype).to(DEV)
+
+    def step(window):
+        dev = sa.kv4_cache(12, Hkv, ps, D)
+        sa.attn_kv4_append(x["k"].to(DEV), x["v"].to(DEV), i32(slots), *dev, 1.0, 0.125)
+        out = [torch.empty(2, Hkv, L, D, dtype=dtype, device=DEV) for _ in range(2)]
+        sa.attn_kv4_gather(*dev, i32(table), i32([L, L]), *out, 1.0, 0.125)
+        return [t.cpu() for t in out], run_decode(q, dev, table, [L, L], L, True, window).cpu()
+
+    clean, o_all = step(0)
+    _, o_late = step(20)
+    for w, at in (("k", (40, 1, D - 1)), ("v", (L + 3, 0, 0))):  # a key of the first sequence, a value of the second
+        x[w][at] = bad
+        x[w][2 * L:] = bad
+    got, o = step(0)
+    for n, (b, h, j, g) in enumerate(((0, 1, 40, D // 32 - 1), (1, 0, 3, 0))):
+        hit = torch.zeros(2, Hkv, L, D, dtype=torch.bool)
+        hit[b, h, j, 32 * g:32 * g + 32] = True
+        assert got[n][hit].isnan().all() and torch.equal(got[n][~hit], clean[n][~hit])
+    hit = torch.zeros(2, 2 * Hkv, 1, D, dtype=torch.bool)
+    hit[0, 2:] = True
+    hit[1, :2, :, :32] = True
+    assert o[hit].isnan().all() and torch.equal(o[~hit], o_all[~hit])
+    assert torch.equal(step(20)[1], o_late)
+
+
 # ---------------------------------------------------------------------------
 # tables of a step
 # ---------------------------------------------------------------------------
