@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "attn.h"
@@ -122,7 +123,9 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& w, float inv, uint32_
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
     float top = largest<T>(words);
     top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2)) * inv;
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // scales end at 448: nothing is lost here, and a large number over a small factor stays finite
+    top = top < INFINITY ? fminf(top * inv, 2.0f * 7.5f * 448.0f) : top;
     const float q = top * (1.0f / 7.5f);
     const uint32_t s =
         __nv_cvt_float_to_fp8(fmaf(fmaf(-7.5f, q, top), 1.0f / 7.5f, q), __NV_SATFINITE, __NV_E4M3);

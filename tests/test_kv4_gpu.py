@@ -192,6 +192,27 @@ def test_append_one_row_of_one_head_any_stride():
     assert np.array_equal(bytes_np(dev[3])[1, 0, 1], byte[0, 0])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("descale", [2.0 ** -64, 1.0, 2.0 ** 64])
+def test_append_of_every_magnitude(dtype, descale):
+    """Groups whose largest element is anything from the type's smallest number to its largest: exact."""
+    rng = np.random.default_rng(96)
+    lo, hi = (-149, 128) if dtype == BF16 else (-24, 16)
+    T, D = hi - lo + 3, 64
+    x = torch.from_numpy(np.ldexp(rng.uniform(-1, 1, (T, 1, D)), (lo + np.arange(T) - 1)[:, None, None]))
+    x[-1] = torch.finfo(dtype).max
+    x[-1, 0, ::3] *= -1
+    x = x.to(dtype)
+    x = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    dev = sa.kv4_cache(-(-T // 16), 1, 16, D)
+    sa.attn_kv4_append(x.to(DEV), x.to(DEV), i32(list(range(T))), *dev, descale, descale)
+    torch.cuda.synchronize()
+    codes, byte, _ = ref.quantize(ref.f64(x), descale)
+    for n, which in ((0, "k"), (2, "v")):
+        assert np.array_equal(bytes_np(dev[n]).reshape(-1, 1, D // 2)[:T], ref.pack(codes, which))
+        assert np.array_equal(bytes_np(dev[n + 1]).reshape(-1, 1, D // 32)[:T], byte)
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
