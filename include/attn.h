@@ -475,10 +475,10 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  * The values of the cache enter the products exactly; the query is rounded to
  * FP16 relative to its row's largest element and the probabilities to FP16 before
  * and after their product with a scale (for FP16 outputs at most after it), all sums are
- * FP32. Pages need not be clean: rows that no query row sees (behind a
- * sequence's end, or in front of its window and no sinks) may hold anything. A
- * table entry outside [0, num_pages) reads a page of zeros. NaN in a key that a
- * row sees makes the row NaN, in a value the elements of its group.
+ * FP32. Pages need not be clean: what a query row does not see (behind a
+ * sequence's end, in front of its window and no sinks, or a later row's key) may
+ * hold anything. A table entry outside [0, num_pages) reads a page of zeros. NaN in
+ * a key that a row sees makes that row NaN, in a value the elements of its group.
  * D is 32, 64 or 128 (else ATTN_ERR_HEADDIM); B * Hkv <= 65535 and at most
  * 8 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
  * to 8 grouped rows read the cache once, more in blocks of 8 rows; for many

@@ -665,9 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
             sh.vis[turn][lane] = v;
         }
         // keys [all_lo, all_hi) are visible to every row
-        int all_lo, all_hi, any_lo, skip;
+        int all_lo, all_hi, skip;
         key_range(L - 1, L, a.causal, a.window, &all_lo, &skip);
-        key_range(L - a.M, L, a.causal, a.window, &any_lo, &all_hi);
+        key_range(L - a.M, L, a.causal, a.window, &skip, &all_hi);
 
         // m: the score that stands for the largest one so far, in units of sc: it is set anew only when a score exceeds
         // it by kPSlack in base 2 (else every few steps some row's would be); limit: that border; mu: kPShift less m in
@@ -704,6 +704,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
                     else
                         load_shared(v[b][e], at + at_v + 4 * e * St::kRow);
                     if constexpr (!St::kSpread) vs[b][e] = load_shared_small<NG>(at + at_vs + 4 * e * NG);
+                }
+                // A value that the lane's row of P^T does not see counts as zero, whatever it holds (a probability of
+                // zero would not hide a NaN): its scales are cleared.
+                if constexpr (edge) {
+                    const int2 vis = sh.vis[turn][gq];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + cq + 4 * e;
+                        if (!(j < vis.y && (j >= vis.x || j < a.sinks))) vs[b][e] = 0;
+                    }
                 }
             };
             // of one block with the keys', ahead of the branch below; of two behind the keys' products, for the registers
@@ -853,26 +863,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
             }
         };
 
-        // What stands behind the sequence, or in front of its window on pages that may have been given up, counts as
-        // zero: the scales of such values are cleared in the stage (a probability of zero would not hide a NaN).
-        const auto hide = [&](uint32_t st, int j0) {
-            const int x = lane & 15, j = j0 + x;
-            if (lane < 16 && !(j < L && (j >= any_lo || j < a.sinks))) {
-                if constexpr (NG == 4)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + St::kVs + ((x & 3) * 4 + (x >> 2)) * NG), "r"(0) : "memory");
-                else if constexpr (NG == 2)
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(st + St::kVs + x * NG), "h"((short)0) : "memory");
-                else
-                    asm volatile("st.shared.b8 [%0], %1;" ::"r"(st + St::kVs + x), "r"(0) : "memory");
-            }
-            __syncwarp();
-        };
         const auto full = [&](int j0) { return j0 + 16 <= all_hi && (j0 >= all_lo || j0 + 16 <= a.sinks); };
         const auto any_step = [&](uint32_t st, int j0) {
             if (full(j0)) {
                 step(st, Number<1>(), j0, Flag<false>());
             } else if (j0 < L) {
-                hide(st, j0);
                 step(st, Number<1>(), j0, Flag<true>());
             }
         };

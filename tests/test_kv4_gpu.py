@@ -674,6 +674,36 @@ def test_decode_dirty_rows_of_cut_segments(B, Hkv, window, sinks, D):
     assert torch.equal(run_decode(q, dev, table, lens, 3000, True, window, sinks), want)
 
 
+@pytest.mark.parametrize("causal,window,sinks", [(True, 0, 0), (True, 75, 0), (True, 75, 9), (False, 75, 0)])
+@pytest.mark.parametrize("B,most,Hq,Hkv,M,D,dtype", [
+    (4, 500, 4, 2, 4, 128, BF16), (4, 500, 2, 2, 12, 64, FP16), (4, 500, 2, 1, 5, 32, FP16),  # segments left whole
+    (4, 3000, 4, 2, 4, 128, FP16), (4, 3000, 2, 1, 5, 64, BF16),                              # cut, four warps a team
+    (45, 1700, 4, 2, 4, 128, BF16), (90, 1700, 1, 1, 9, 64, FP16)])                           # cut, single warps
+def test_what_a_row_does_not_see_does_not_reach_it(causal, window, sinks, B, most, Hq, Hkv, M, D, dtype):
+    """NaN in a key or a value that some rows of a sequence see and others do not (the last keys, which later rows see,
+    and those at the rows' window edges, which earlier ones see): rows that see the key are NaN, or the elements of
+    the value's group; all else is as without it."""
+    rng = np.random.default_rng(97)
+    lens = rng.integers(M, most + 1, B).tolist()
+    lens[0], lens[1], lens[2], lens[3] = most, M, 16 * (most // 16), 16 * (most // 16) - 15
+    ps, G = 16, Hq // Hkv
+    q, dev, host, table = case(98, lens, Hq, Hkv, M, D, ps, dtype)
+    clean = run_decode(q, dev, table, lens, most, causal, window, sinks)
+    hit = torch.zeros(B, Hq, M, D, dtype=torch.bool)
+    for b, L in enumerate(lens):
+        # the key that the last row alone sees; the one that the first row alone sees, and its neighbour; a middle one
+        spots = [L - 1, L - M - window + 1, L - M - window + 2, max(L - 1 - M // 2, 0)]
+        j, key, h, g = max(spots[b % 4], 0), b // 4 % 3 == 1, b % Hkv, b % (D // 32)
+        page = int(table[b, j // ps])
+        dev[1 if key else 3].view(torch.uint8)[page, h, j % ps, g] = 0x7F  # E4M3 NaN
+        for i in range(M):
+            if ref.visible(L, M, i, causal, window, sinks)[j]:
+                hit[b, h * G:(h + 1) * G, i, slice(None) if key else slice(32 * g, 32 * g + 32)] = True
+    assert hit.any() and not hit.all()
+    got = run_decode(q, dev, table, lens, most, causal, window, sinks).cpu()
+    assert got[hit].isnan().all() and torch.equal(got[~hit], clean.cpu()[~hit])
+
+
 @pytest.mark.parametrize("D", [32, 64, 128])
 @pytest.mark.parametrize("dtype,kd,vd", [(BF16, 2.0 ** -64, 2.0 ** 64), (BF16, 2.0 ** 64, 2.0 ** -64),
                                          (FP16, 2.0 ** -5, 2.0 ** 7), (FP16, 2.0 ** -6, 1.0), (FP16, 1.0, 2.0 ** 8),
