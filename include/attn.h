@@ -422,11 +422,14 @@ ATTN_API int attn_decode_paged_fp8(const void* q, const void* k_pages, const voi
  *     from free_pages in order, requests in order, pages of a request in order;
  *     only those entries are written.
  *   slot_map[r], r < num_rows: page * page_size + offset of row r's key; -1 for
- *     r >= row_starts[B] (a padded batch) and for a row without a page.
- *   stats[3]: rows of the step; pages taken from free_pages; rows without a
- *     slot: their page is behind max_pages or behind the end of free_pages (its
- *     table entry is then -1), or the row is behind num_rows. Callers that can
- *     run out check stats[2]; seq_lens counts such rows all the same.
+ *     r >= row_starts[B] (a padded batch) and for a row without a slot.
+ *   stats[3]: rows of the step; pages taken from free_pages (the next step's
+ *     begins that many entries further); rows without a slot: their page is
+ *     behind max_pages or behind the end of free_pages (its table entry is then
+ *     -1), or the entry is no page (negative, as a step that ran out of pages
+ *     left it, or with a slot past 2^31 - 1), or the row is behind num_rows.
+ *     Callers that can run out check stats[2]; seq_lens counts such rows all the
+ *     same, and the entries of cached keys stay as they are.
  * Sums that pass 2^31 - 1 are written as 2^31 - 1.
  *   cached_lens, new_lens, seq_lens [B], free_pages [num_free], block_table
  *   [B, max_pages], row_starts [B + 1], slot_map [num_rows], stats [3]: device

@@ -12,9 +12,12 @@
 // one or two requests per thread at a time, and takes its share of the chunk's rows and
 // pages, whose request it finds by bisection in shared memory. No block reads a
 // table entry that another one writes: entries below old_b are only read, the
-// others only written (their page is computed from the free list instead).
+// others only written (their page is computed from the free list instead). One more block
+// writes what there is per request and counts the rows without a slot: per request those
+// behind the pages it gets and behind slot_map, and those on the page its cached keys end in,
+// if that is none; per page taken, those on a page that is none.
 // Latency bounds it: loads, sums, bisection, loads, stores. 64 requests of one new key
-// take 3.0 us, 2000 of 97 new keys 7.4.
+// take 2.7 us, 2000 of 97 new keys each 6.5.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,6 +29,7 @@ namespace attn {
 namespace {
 
 constexpr int kPlanMost = 2048;  // requests of a chunk, at most
+constexpr int kPlanLoads = 16;   // entries of the free list that a counting thread has in flight
 constexpr long long kI32Max = 2147483647LL;
 
 struct PlanArgs {
@@ -38,6 +42,7 @@ struct PlanArgs {
     int* slots;
     int* stats;
     int B, page_size, max_pages, num_free, num_rows;
+    uint32_t last_page;  // all slots of the pages 0 .. last_page fit 32 bits
 };
 
 __device__ __forceinline__ int saturate(long long x) { return (int)(x < kI32Max ? x : kI32Max); }
@@ -95,6 +100,13 @@ __device__ __forceinline__ int pages_of(uint32_t x, uint32_t page_size, int most
     return (int)min(n, (uint32_t)most);
 }
 
+// How many of `rows` keys from offset `off` on of a page have no slot: all if it is no page (below 0), else those whose
+// slot passes 2^31 - 1.
+__device__ __forceinline__ long long without_slot(int page, int page_size, long long off, long long rows) {
+    const long long past = (long long)page * page_size + off + rows - 1 - kI32Max;
+    return max(page < 0 ? rows : min(past, rows), 0LL);
+}
+
 // N threads, K requests of a chunk to a thread.
 template <int N, int K>
 __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
@@ -105,14 +117,17 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
     // launched while the kernel in front of it may still run: nothing in memory is touched before that has ended
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // the last block writes what there is per request and the counts, the others share the pages and rows
+    const bool counts = blockIdx.x == gridDim.x - 1;
     const long long mine = (long long)blockIdx.x * N + threadIdx.x;
-    const long long step = (long long)gridDim.x * N;
+    const long long step = (long long)(gridDim.x - 1) * N;
     long long rows = 0, pages = 0;  // of the requests before this chunk
     long long lost = 0;             // rows without a place of this thread's requests
     for (int b0 = 0; b0 < a.B; b0 += N * K) {
         const int b = b0 + (int)threadIdx.x * K;
         uint32_t c[K], n[K];
         int had[K], need[K];
+        int begun[K];  // the table's entry for the page that the request's first new key goes to, if it has one already
         long long s = 0, f = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -123,6 +138,10 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
         for (int k = 0; k < K; ++k) {
             had[k] = pages_of(c[k], a.page_size, a.max_pages);
             need[k] = pages_of(c[k] + n[k], a.page_size, a.max_pages) - had[k];
+            const uint32_t at = c[k] / (uint32_t)a.page_size;
+            begun[k] = counts && n[k] > 0 && at < (uint32_t)had[k]
+                           ? load_global(a.table + (size_t)(b + k) * a.max_pages + at)
+                           : 0;
             s += n[k];
             f += need[k];
         }
@@ -137,13 +156,16 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
             first[e] = saturate(f);
             have[e] = (int)c[k];
             old[e] = had[k];
-            if (blockIdx.x == 0 && b + k < a.B) {
+            if (counts && b + k < a.B) {
                 const long long len = (long long)c[k] + n[k];
                 a.seq_lens[b + k] = saturate(len);
                 a.row_starts[b + k] = saturate(s);
                 // kept: the rows on pages that this request could get, and not behind slot_map
                 const long long got = had[k] + min(max(a.num_free - f, 0LL), (long long)need[k]);
-                lost += n[k] - min(max(min(len, got * a.page_size) - c[k], 0LL), max(a.num_rows - s, 0LL));
+                const long long kept =
+                    min(max(min(len, got * a.page_size) - c[k], 0LL), max(a.num_rows - s, 0LL));
+                const long long off = c[k] % (uint32_t)a.page_size;
+                lost += n[k] - kept + without_slot(begun[k], a.page_size, off, min(kept, a.page_size - off));
             }
             s += n[k];
             f += need[k];
@@ -151,32 +173,60 @@ __global__ void __launch_bounds__(N) page_plan_kernel(PlanArgs a) {
         __syncthreads();
         const int live = min(a.B - b0, N * K);
         const long long page_end = min(pages + chunk_pages, kI32Max);
-        for (long long x = pages + mine; x < page_end; x += step) {
-            const int e = last_not_above(first, live, (int)x);
-            const int k = old[e] + ((int)x - first[e]);
-            a.table[(size_t)(b0 + e) * a.max_pages + k] = x < a.num_free ? load_global(a.free_pages + x) : -1;
-        }
         const long long row_end = min(rows + chunk_rows, (long long)a.num_rows);
-        for (long long r = rows + mine; r < row_end; r += step) {
-            const int e = last_not_above(start, live, (int)r);
-            const uint32_t pos = (uint32_t)have[e] + (uint32_t)((int)r - start[e]);
-            const uint32_t k = pos / (uint32_t)a.page_size;
-            int page = -1;
-            if (k < (uint32_t)old[e]) {
-                page = a.table[(size_t)(b0 + e) * a.max_pages + k];
-            } else if (k < (uint32_t)a.max_pages) {
-                const long long x = (long long)first[e] + (k - (uint32_t)old[e]);
-                if (x < a.num_free) page = load_global(a.free_pages + x);
+        if (counts) {
+            // rows on entries of the free list that are no pages
+            const long long listed = min(page_end, (long long)a.num_free);
+            for (long long x0 = pages + threadIdx.x; x0 < listed; x0 += kPlanLoads * N) {
+                int page[kPlanLoads];
+                bool none = false;
+#pragma unroll
+                for (int i = 0; i < kPlanLoads; ++i) {
+                    page[i] = x0 + i * N < listed ? load_global(a.free_pages + x0 + i * N) : 0;
+                    none |= (uint32_t)page[i] > a.last_page;
+                }
+                if (!none) continue;
+#pragma unroll
+                for (int i = 0; i < kPlanLoads; ++i) {
+                    if ((uint32_t)page[i] <= a.last_page) continue;
+                    const int x = (int)(x0 + i * N);
+                    const int e = last_not_above(first, live, x);
+                    const long long next = e + 1 < live ? start[e + 1] : min(rows + chunk_rows, kI32Max);
+                    const long long r =
+                        start[e] + ((long long)(old[e] + (x - first[e])) * a.page_size - (uint32_t)have[e]);
+                    const long long on = min(min(next, (long long)a.num_rows) - r, (long long)a.page_size);
+                    lost += without_slot(page[i], a.page_size, 0, max(on, 0LL));
+                }
             }
-            const long long slot = (long long)page * a.page_size + (pos - k * (uint32_t)a.page_size);
-            a.slots[r] = page >= 0 && slot <= kI32Max ? (int)slot : -1;
+        } else {
+            for (long long x = pages + mine; x < page_end; x += step) {
+                const int e = last_not_above(first, live, (int)x);
+                const int k = old[e] + ((int)x - first[e]);
+                a.table[(size_t)(b0 + e) * a.max_pages + k] = x < a.num_free ? load_global(a.free_pages + x) : -1;
+            }
+            for (long long r = rows + mine; r < row_end; r += step) {
+                const int e = last_not_above(start, live, (int)r);
+                const uint32_t pos = (uint32_t)have[e] + (uint32_t)((int)r - start[e]);
+                const uint32_t k = pos / (uint32_t)a.page_size;
+                int page = -1;
+                if (k < (uint32_t)old[e]) {
+                    page = a.table[(size_t)(b0 + e) * a.max_pages + k];
+                } else if (k < (uint32_t)a.max_pages) {
+                    const long long x = (long long)first[e] + (k - (uint32_t)old[e]);
+                    if (x < a.num_free) page = load_global(a.free_pages + x);
+                }
+                const long long slot = (long long)page * a.page_size + (pos - k * (uint32_t)a.page_size);
+                a.slots[r] = page >= 0 && slot <= kI32Max ? (int)slot : -1;
+            }
         }
         rows += chunk_rows;
         pages += chunk_pages;
         __syncthreads();  // the chunk's arrays are read
     }
-    for (long long r = rows + mine; r < a.num_rows; r += step) a.slots[r] = -1;
-    if (blockIdx.x != 0) return;
+    if (!counts) {
+        for (long long r = rows + mine; r < a.num_rows; r += step) a.slots[r] = -1;
+        return;
+    }
     long long none = 0, all, all_none;
     block_sums<N>(lost, none, part, &all, &all_none);
     if (threadIdx.x == 0) {
@@ -223,16 +273,17 @@ int attn_page_plan(const int* cached_lens, const int* new_lens, const int* free_
             if (overlap(out[i], nout[i], out[j], nout[j])) return ATTN_ERR_ALIAS;
     }
     const PlanArgs a{cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats,
-                     B, page_size, max_pages, num_free, num_rows};
-    // one row per thread, on at most one block per SM. Few requests take smaller blocks, whose sums are quicker; many
+                     B, page_size, max_pages, num_free, num_rows, (uint32_t)((kI32Max - (page_size - 1)) / page_size)};
+    // one row per thread, on at most one block per SM, one of them the block that counts. Few requests take smaller blocks, whose sums are quicker; many
     // take larger ones, and so fewer chunks one after the other: 64 requests 3.0 us in blocks of 256 threads and 4.8 in
     // blocks of 1024, 256 3.1 and 5.0, 512 5.1 and 5.5, 2000 18.0 and 7.4.
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
     const int threads = B <= 512 ? 256 : 1024;
     int64_t grid = ((int64_t)(num_rows > B ? num_rows : B) + threads - 1) / threads;
-    if (grid > sms) grid = sms;
+    if (grid > sms - 1) grid = sms - 1;
     if (grid < 1) grid = 1;
+    ++grid;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 g((unsigned)grid);
     const cudaError_t e = threads == 256

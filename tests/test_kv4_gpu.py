@@ -287,6 +287,53 @@ def test_page_plan(B, ps, most, pad, short):
         assert got.tolist() == w
 
 
+@pytest.mark.parametrize("B,ps,most,pad,short", [
+    (2, 16, 3, 0, 0), (5, 1, 4, 3, 2), (31, 7, 40, -20, 0), (256, 16, 2, 0, 0), (257, 16, 40, 9, 0), (512, 32, 70, 0, 9),
+    (513, 16, 3, 1, 0), (2047, 16, 50, 0, 100), (2049, 128, 200, -3000, 5)])
+def test_page_plan_counts_every_row_without_a_slot(B, ps, most, pad, short):
+    """Entries that name no page, in the table of the cached keys (as a step that ran out of pages leaves them) and in the
+    free list, and pages whose slots pass 32 bits, in part or wholly: their rows have no slot and are counted."""
+    rng = np.random.default_rng(B + 1)
+    cached, new = rng.integers(0, 4 * ps + 1, B), rng.integers(0, most + 1, B)
+    cached[0], new[0] = ps - 1 if ps > 1 else 1, 3
+    width = int(max(-(-(cached + new) // ps)))
+    have = -(-cached // ps)
+    need = int((-(-(cached + new) // ps) - have).sum())
+    last = (2 ** 31 - 1) // ps  # its slots pass 32 bits behind the first few
+    odd = [-1, -2 ** 31, -5, last, min(last + 1, 2 ** 31 - 1), 2 ** 31 - 1]
+    table, free = rng.integers(0, 1000, (B, width)), rng.integers(0, 1000, max(need - short, 0))
+    for x in (table, free):
+        x[rng.random(x.shape) < 0.3] = 0  # (the same page twice is no matter here)
+        at = rng.random(x.shape) < 0.3
+        x[at] = rng.choice(odd, int(at.sum()))
+    table[0] = -1
+    T = max(int(new.sum()) + pad, 0)
+    want = ref.plan(cached.tolist(), new.tolist(), free.tolist(), table, ps, T)
+    want[3][:] = [x if x < 2 ** 31 else -1 for x in want[3]]
+    want[4][2] = int(new.sum()) - sum(x >= 0 for x in want[3])
+    assert want[4][2] > 0
+    out = [torch.full((n,), -9, dtype=torch.int32, device=DEV) for n in (B, B + 1, T, 3)]
+    d_table = i32(table)
+    sa.attn_page_plan(i32(cached), i32(new), i32(free), d_table, *out, ps)
+    torch.cuda.synchronize()
+    assert d_table.tolist() == want[0]
+    for got, w in zip(out, want[1:]):
+        assert got.tolist() == w
+
+
+def test_page_plan_after_a_step_that_ran_out():
+    """15 keys, 3 more, no page left: the table's new entry is -1. The next step's rows on it have no slot either, and
+    are counted; rows on a page of their own have one."""
+    table, lens, starts, slots, stats = i32([[4, -7, -7]]), i32([0]), i32([0, 0]), i32([9] * 3), i32([9] * 3)
+    sa.attn_page_plan(i32([15]), i32([3]), i32([]), table, lens, starts, slots, stats, 16)
+    assert (table.tolist(), slots.tolist(), stats.tolist()) == ([[4, -1, -7]], [79, -1, -1], [3, 0, 2])
+    sa.attn_page_plan(lens.clone(), i32([3]), i32([7, 8]), table, lens, starts, slots, stats, 16)
+    assert (table.tolist(), slots.tolist(), stats.tolist()) == ([[4, -1, -7]], [-1, -1, -1], [3, 0, 3])
+    slots = i32([9] * 12)
+    sa.attn_page_plan(lens.clone(), i32([12]), i32([7, 8]), table, lens, starts, slots, stats, 16)
+    assert (table.tolist(), slots.tolist(), stats.tolist()) == ([[4, -1, 7]], [-1] * 11 + [112], [12, 1, 11])
+
+
 def test_page_plan_of_nothing_and_of_huge_lengths():
     e = torch.empty(0, dtype=torch.int32, device=DEV)
     starts, slots, stats = i32([-9]), i32([5, 5]), i32([9, 9, 9])
