@@ -291,11 +291,12 @@ __global__ void __launch_bounds__(kThreads) kv4_gather_kernel(GatherArgs a) {
         page[x] = j < L && n < a.max_pages ? load_global(a.table + (size_t)b * a.max_pages + n) : -1;
         if (page[x] >= a.c.num_pages) page[x] = -1;
     }
-    // a row behind the sequence, or on a page outside the pool, is zeros
+    // a row behind the sequence, or on a page outside the pool, is zeros: code 8 (code 0 would make negative ones)
     uint32_t ck[kGatherRows], cv[kGatherRows], sk[kGatherRows], sv[kGatherRows];
 #pragma unroll
     for (int x = 0; x < kGatherRows; ++x) {
-        ck[x] = cv[x] = sk[x] = sv[x] = 0;
+        ck[x] = cv[x] = 0x88888888u;
+        sk[x] = sv[x] = 0;
         if (page[x] >= 0) {
             const int j = first + x * (kThreads / U);
             const size_t at = ((size_t)page[x] * a.Hkv + h) * ps + (j - page_index(j, ps, a.ps_shift) * ps);

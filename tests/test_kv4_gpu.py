@@ -179,6 +179,21 @@ def test_gather_lengths_past_the_table_and_short_outputs():
             assert np.array_equal(ref.f64(k[b]), want)
 
 
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("dtype,vd", [(BF16, 0.125), (FP16, 0.125), (FP16, 2.0 ** -20)])
+def test_gather_of_nothing_is_zeros_in_every_bit(D, dtype, vd):
+    """Rows behind the end and rows on pages outside the pool: no negative zeros."""
+    dev, _ = make_cache(np.random.default_rng(3), 4, 2, 16, D)
+    k = torch.full((3, 2, 70, D), float("nan"), dtype=dtype, device=DEV)
+    v = k.clone()
+    table = i32([[1, -1, 0, 2, 3], [4, 2 ** 31 - 1, -2 ** 31, 1, 1], [0, 0, 0, 0, 0]])
+    sa.attn_kv4_gather(*dev, table, i32([40, 48, -1]), k, v, 1.0, vd)
+    torch.cuda.synchronize()
+    for x in (k.view(torch.int16), v.view(torch.int16)):
+        assert not x[0, :, 16:32].any() and not x[0, :, 40:].any() and not x[1:].any()
+        assert x[0, :, :16].any() and x[0, :, 32:40].any()
+
+
 def test_append_one_row_of_one_head_any_stride():
     """A single row's stride is not read; a single head's neither."""
     rng = np.random.default_rng(9)
