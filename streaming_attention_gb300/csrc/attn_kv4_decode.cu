@@ -1089,10 +1089,24 @@ struct Plan {
 constexpr int kWholeTiles = 16;  // of 64 keys
 constexpr int kManyParts = 32;
 
-// One block for every SM, fewer while the longest lengths could not give one team of each kMinTiles tiles.
-Plan plan_blocks(const Kv4Call& c) {
+long long segments_of(const Problem& p) { return (long long)p.B * p.Hkv * row_blocks(p); }
+
+// The most segments of this and of any smaller call (at most B, Hq, Hkv and M of p): fewer KV heads may make more of
+// them, 18 query heads on 2 KV heads 4 (9 rows each), on 3 KV heads 3.
+long long most_segments(const Problem& p) {
+    long long most = 0;
+    for (int h = 1; h <= p.Hkv && h <= p.Hq; ++h) {
+        const long long n = h * (((long long)(p.Hq / h) * p.M + ROWS - 1) / ROWS);
+        if (n > most) most = n;
+    }
+    return p.B * most;
+}
+
+// One block for every SM, fewer while the longest lengths could not give one team of each kMinTiles tiles. What a plan
+// needs of workspace does not fall as the segments or the longest length rise.
+Plan plan_blocks(const Kv4Call& c, long long segments) {
     const Problem& p = c.p;
-    const long long segments = (long long)p.B * p.Hkv * row_blocks(p), sms = sm_count();
+    const long long sms = sm_count();
     const auto tiles_at = [&](int kTile) {
         long long tiles = ((long long)c.max_len + kTile - 1) / kTile;
         if (p.window > 0) {
@@ -1213,7 +1227,7 @@ int run(const Kv4Call& c, const void* q, const int* table, const int* lens, void
     const size_t n = (size_t)places * 2 * ROWS;
     int4* cut = static_cast<int4*>(ws);
     float* wm = plan.whole ? nullptr : reinterpret_cast<float*>(cut + places);
-    const int by_segment = (int64_t)p.B * p.Hkv * row_blocks(p) <= places;
+    const int by_segment = segments_of(p) <= places;
     const DecodeArgs a{q, c.c, table, lens, o, wm, wm + n, wm + 2 * n, cut, by_segment, p.B, p.Hq, p.Hkv, p.M, p.G, row_blocks(p),
                        c.max_pages, c.max_len, p.causal, p.window, c.sinks, p.scale_log2, c.v_descale};
     const cudaError_t e =
@@ -1238,7 +1252,7 @@ size_t attn_decode_paged_kv4_workspace_bytes(int B, int Hq, int Hkv, int M, int 
                  0.f, 1.f, 1.f, ATTN_BF16, &c) != ATTN_OK)
         return 0;
     if ((int64_t)B * Hq * M == 0 || nothing_to_attend(c)) return 0;
-    return workspace_bytes(plan_blocks(c), D);
+    return workspace_bytes(plan_blocks(c, most_segments(c.p)), D);
 }
 
 int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
@@ -1256,7 +1270,7 @@ int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scal
     if ((int64_t)B * Hq * M == 0) return ATTN_OK;
     if (nothing_to_attend(c))  // no sequence can hold a key: every row outputs 0
         return cudaMemsetAsync(o, 0, (size_t)B * Hq * M * D * 2, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-    const Plan plan = plan_blocks(c);
+    const Plan plan = plan_blocks(c, segments_of(c.p));
     const size_t bytes = workspace_bytes(plan, D);
     if (workspace || bytes == 0) return run(c, q, block_table, seq_lens, o, workspace, ws_bytes, plan, s);
     void* ws = nullptr;

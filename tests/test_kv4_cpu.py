@@ -79,6 +79,31 @@ def test_decode_workspace_does_not_fall_with_larger_calls():
         assert max(n.values()) == n[Bs[-1], Hs[-1], Ms[-1], lens[-1]] > 0
 
 
+def test_decode_workspace_serves_every_smaller_call(L):
+    """Query and KV heads one by one (a call needs Hq % Hkv == 0): the size does not fall along any argument, also where
+    more KV heads make fewer segments (18 query heads on 2 and on 3, 36 on 4 and on 6), and a workspace of the largest
+    call's size is not refused by a smaller one."""
+    size = sa.attn_decode_paged_kv4_workspace_bytes
+    assert size(1, 18, 2, 1, 128, 16, 125, 2000) <= size(1, 18, 3, 1, 128, 16, 125, 2000)
+    assert size(1, 36, 4, 1, 128, 16, 125, 2000) <= size(1, 36, 6, 1, 128, 16, 125, 2000)
+    for B, M, N, window in ((1, 1, 2000, 0), (4, 3, 1000, 0), (16, 1, 5000, 700), (60, 5, 900, 0), (200, 1, 1024, 100)):
+        heads = [(q, h) for q in (1, 2, 3, 6, 8, 9, 12, 18, 24, 36, 40, 64, 72, 100) for h in range(1, q + 1) if q % h == 0]
+        n = {x: size(B, *x, M, 64, 16, 400, N, True, window) for x in heads}
+        for (q, h), got in n.items():
+            for (q2, h2), more in n.items():
+                if q <= q2 and h <= h2:
+                    assert got <= more, (B, M, N, window, (q, h), (q2, h2))
+            for smaller in (size(B - 1, q, h, M, 64, 16, 400, N, True, window) if B > 1 else 0,
+                            size(B, q, h, M - 1, 64, 16, 400, N, True, window) if M > 1 else 0,
+                            size(B, q, h, M, 64, 16, 400, N - 1, True, window)):
+                assert smaller <= got
+    # the smaller call itself: a workspace that is too small is told before anything else happens
+    big = size(1, 18, 3, 1, 128, 16, 125, 2000)
+    short = dict(B_=1, Hq=18, Hkv=2, maxp=125, max_len=2000)
+    assert decode(L, ws=OFF, nb=big, **short) == -7  # large enough, not aligned
+    assert decode(L, ws=at(8), nb=16, **short) == -8
+
+
 def append(L, k=at(0), v=at(1), slots=at(2), kc=at(3), ks=at(4), vc=at(5), vs=at(6), T=3, Hkv=2, D=128, kst=256, vst=256,
            pages=8, ps=16, kd=1.0, vd=1.0, dtype=0):
     return L.attn_kv4_append(k, v, slots, kc, ks, vc, vs, T, Hkv, D, kst, vst, pages, ps, kd, vd, dtype, None)
