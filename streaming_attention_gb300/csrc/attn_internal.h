@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "attn.h"
@@ -39,6 +40,15 @@ cudaError_t once_per_device(PerDeviceOnce& o, F&& fn) {
 
 // Number of SMs of the current device (cached per device); 0 when it cannot be read.
 int device_sm_count();
+
+// Elements of a tensor of these sizes (none negative): their product, or INT64_MAX where it does not fit 64 bits.
+inline int64_t elements(std::initializer_list<int> sizes) {
+    int64_t n = 1;
+    for (const int x : sizes)
+        if (x == 0) return 0;
+    for (const int x : sizes) n = n > INT64_MAX / x ? INT64_MAX : n * x;
+    return n;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

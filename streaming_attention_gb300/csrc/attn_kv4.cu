@@ -383,7 +383,7 @@ int attn_kv4_append(const void* k, const void* v, const int* slot_map, void* k_c
     const int rc = kv4_validate_cache(c, Hkv, D);
     if (rc != ATTN_OK) return rc;
     const int64_t row = (int64_t)Hkv * D;
-    if ((int64_t)T * row > kI32Max) return ATTN_ERR_OVERFLOW;
+    if (elements({T, Hkv, D}) > kI32Max) return ATTN_ERR_OVERFLOW;
     if (T > 1 && (k_stride < row || v_stride < row)) return ATTN_ERR_SHAPE;
     if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
     if (T == 0 || Hkv == 0 || num_pages == 0) return ATTN_OK;
@@ -406,10 +406,10 @@ int attn_kv4_gather(const void* k_codes, const void* k_scales, const void* v_cod
     const int rc = kv4_validate_cache(c, Hkv, D);
     if (rc != ATTN_OK) return rc;
     // the grid holds a KV head per y and a sequence per z index
-    if ((int64_t)B * Hkv * N * D > kI32Max || (int64_t)B * max_pages > kI32Max || B > 65535 || Hkv > 65535)
+    if (elements({B, Hkv, N, D}) > kI32Max || elements({B, max_pages}) > kI32Max || B > 65535 || Hkv > 65535)
         return ATTN_ERR_OVERFLOW;
     if (!kv4_descale(k_descale) || !kv4_descale(v_descale)) return ATTN_ERR_SCALE;
-    if ((int64_t)B * Hkv * N == 0) return ATTN_OK;
+    if (elements({B, Hkv, N}) == 0) return ATTN_OK;
     if (!k || !v || !seq_lens || (max_pages > 0 && !block_table)) return ATTN_ERR_NULL;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq_lens, 4) || !aligned(block_table, 4)) return ATTN_ERR_ALIGN;
     const GatherArgs a{c, block_table, seq_lens, k, v, Hkv, N, max_pages, shift_of(page_size), k_descale, v_descale};

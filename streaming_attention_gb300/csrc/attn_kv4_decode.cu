@@ -1172,7 +1172,7 @@ int validate(const void* q, const Kv4Cache& cache, const int* table, const int* 
     const int rc = kv4_validate_cache(cache, Hkv, D);
     if (rc != ATTN_OK) return rc;
     const int G = Hkv > 0 ? Hq / Hkv : 1;
-    const int64_t nq = (int64_t)B * Hq * M * D, ntab = (int64_t)B * max_pages;
+    const int64_t nq = elements({B, Hq, M, D}), ntab = elements({B, max_pages});
     const int64_t cover = (int64_t)max_pages * cache.page_size;
     const int64_t longest = cover < max_seq_len ? cover : max_seq_len;
     if (nq > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535 || ((int64_t)G * M + ROWS - 1) / ROWS > 65535 ||
@@ -1251,7 +1251,7 @@ size_t attn_decode_paged_kv4_workspace_bytes(int B, int Hq, int Hkv, int M, int 
     if (validate(dummy, cache, idummy, idummy, dummy, B, Hq, Hkv, M, D, max_pages, max_seq_len, causal, window, sinks,
                  0.f, 1.f, 1.f, ATTN_BF16, &c) != ATTN_OK)
         return 0;
-    if ((int64_t)B * Hq * M == 0 || nothing_to_attend(c)) return 0;
+    if (elements({B, Hq, M}) == 0 || nothing_to_attend(c)) return 0;
     return workspace_bytes(plan_blocks(c, most_segments(c.p)), D);
 }
 
@@ -1267,7 +1267,7 @@ int attn_decode_paged_kv4(const void* q, const void* k_codes, const void* k_scal
                       sinks, scale, k_descale, v_descale, dtype, &c);
     if (rc != ATTN_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((int64_t)B * Hq * M == 0) return ATTN_OK;
+    if (elements({B, Hq, M}) == 0) return ATTN_OK;
     if (nothing_to_attend(c))  // no sequence can hold a key: every row outputs 0
         return cudaMemsetAsync(o, 0, (size_t)B * Hq * M * D * 2, s) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     const Plan plan = plan_blocks(c, segments_of(c.p));

@@ -135,6 +135,19 @@ def test_gather_refusals(L, kw, status):
     assert gather(L, **kw) == status
 
 
+@pytest.mark.parametrize("call,kw", [
+    (gather, dict(B_=1 << 15, Hkv=1 << 15, N=1 << 27, D=128)),   # 2^64 elements
+    (gather, dict(B_=65535, Hkv=65535, N=(1 << 31) - 1, D=128)),
+    (gather, dict(B_=1 << 15, Hkv=1 << 15, N=1 << 27, D=128, k=None, v=None)),
+    (append, dict(T=1 << 30, Hkv=1 << 27, D=128)),
+    (append, dict(T=(1 << 31) - 1, Hkv=(1 << 31) - 1, D=128)),
+    (decode, dict(B_=1 << 15, Hq=1 << 15, Hkv=1, M=1 << 27, D=128)),
+    (decode, dict(B_=1, Hq=(1 << 31) - 1, Hkv=1, M=(1 << 31) - 1, D=128)),
+])
+def test_sizes_whose_product_passes_64_bits(L, call, kw):
+    assert call(L, **kw) == -6
+
+
 def plan(L, cached=at(0), new=at(1), free=at(2), table=at(3), lens=at(4), starts=at(5), slots=at(6), stats=at(7), B_=4,
          ps=16, maxp=8, nfree=5, rows=9):
     return L.attn_page_plan(cached, new, free, table, lens, starts, slots, stats, B_, ps, maxp, nfree, rows, None)
