@@ -49,8 +49,8 @@ int validate(const void* q, const void* k, const void* v, const void* o, int B, 
     if (Hq > 0 && Hkv == 0) return ATTN_ERR_SHAPE;
     if (Hq > 0 && Hq % Hkv != 0) return ATTN_ERR_GQA;
     if (!simt_head_dim(D)) return ATTN_ERR_HEADDIM;
-    const int64_t nq = (int64_t)B * Hq * M * D;
-    const int64_t nk = (int64_t)B * Hkv * N * D;
+    const int64_t nq = elements({B, Hq, M, D});
+    const int64_t nk = elements({B, Hkv, N, D});
     if (nq > kI32Max || nk > kI32Max) return ATTN_ERR_OVERFLOW;
     if ((nq > 0 && (!q || !o)) || (nk > 0 && (!k || !v))) return ATTN_ERR_NULL;
     if ((q && !aligned16(q)) || (k && !aligned16(k)) || (v && !aligned16(v)) || (o && !aligned16(o)))

@@ -41,9 +41,9 @@ int validate_paged(const void* q, const void* kp, const void* vp, const int* tab
     if (Hq > 0 && Hq % Hkv != 0) return ATTN_ERR_GQA;
     if (D != 16 && D != 32 && D != 64 && D != 128) return ATTN_ERR_HEADDIM;
     const int G = Hkv > 0 ? Hq / Hkv : 1;
-    const int64_t nq = (int64_t)B * Hq * M * D;
-    const int64_t npool = (int64_t)num_pages * Hkv * page_size * D;
-    const int64_t ntab = (int64_t)B * max_pages;
+    const int64_t nq = elements({B, Hq, M, D});
+    const int64_t npool = elements({num_pages, Hkv, page_size, D});
+    const int64_t ntab = elements({B, max_pages});
     if (nq > kI32Max || npool > kI32Max || ntab > kI32Max || (int64_t)B * Hkv > 65535) return ATTN_ERR_OVERFLOW;
     if ((nq > 0 && (!q || !o)) || (npool > 0 && (!kp || !vp)) || (ntab > 0 && !table) || (B > 0 && !lens))
         return ATTN_ERR_NULL;

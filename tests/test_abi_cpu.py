@@ -189,6 +189,17 @@ def test_paged_validation_status(L, kw, status):
     assert paged(L, **kw) == status
 
 
+@pytest.mark.parametrize("call,kw", [
+    (fwd, dict(B_=1 << 15, Hq=1 << 15, Hkv=1 << 15, M=1 << 27, N=1, D=128)),   # 2^64 elements
+    (fwd, dict(B_=1 << 15, Hq=1 << 15, Hkv=1 << 15, M=1, N=1 << 27, D=128)),
+    (fwd, dict(B_=1 << 15, Hq=1 << 15, Hkv=1 << 15, M=1 << 27, N=1 << 27, D=128, q=None, k=None, v=None, o=None)),
+    (paged, dict(num_pages=1 << 30, Hq=1 << 11, Hkv=1 << 11, page_size=1 << 16)),
+    (paged, dict(B_=1, Hq=1 << 30, Hkv=1, M=1 << 27)),
+])
+def test_sizes_whose_product_passes_64_bits(L, call, kw):
+    assert call(L, **kw) == -6
+
+
 def test_paged_workspace_bytes(L):
     # the decode workload as pages of 16 keys: rows x splits x (2 + D) floats, 256-byte aligned parts
     nb = sa.attn_decode_paged_workspace_bytes(8, 32, 8, 1, 128, 16, 512, 8192, True, 4096)
