@@ -467,6 +467,91 @@ def test_decode_rising_and_constant_logits():
     check_decode(o, q, host, table, [L], L)
 
 
+def faint_tail(L, mass, mag, vd, D, dtype, seed):
+    """A first key that takes `mass` of the probability and has hardly a value, and a tail of L - 1 keys that share the
+    rest: what an attention sink in front of a long context looks like. (q [1, 1, 1, D], pools, host, o, bound).
+    The bound counts the output's rounding, both of a probability's (relative to A = sum w |v|), the logits (as
+    kv4_reference does), what is lost where probabilities and their products with a scale are FP16's small numbers (at
+    most 2^-25 each, times a code of at most 8, the factor and a scale, over a row sum of at least 2^3; one product
+    more with FP16 outputs), and the sums of at most 256 blocks of 16 keys to a warp and 64 joins."""
+    rng = np.random.default_rng(seed)
+    x = np.zeros((L, 1, D))
+    x[1:, 0, 0] = rng.normal(size=L - 1) * 1.5
+    x[0, 0, 1] = 7
+    v = rng.normal(size=(L, 1, D)) * mag + mag / 2
+    v[0] *= 0.01
+    host = []
+    for y, which, d in ((x, "k", 1.0), (v, "v", vd)):
+        codes, byte, val = ref.quantize(y, d)
+        host += [ref.pack(codes, which), byte, val[:, 0]]
+    k, val, unit = host[2], host[5], ref.units(host[4], vd)[:, 0]
+    tail = np.log(np.exp(k[1:, 0]).sum())
+    q = torch.zeros(1, 1, 1, D)
+    q[..., 0], q[..., 1] = 1, (tail + np.log(mass / (1 - mass))) / k[0, 1]
+    q = q.to(dtype)
+    logit = k @ ref.f64(q)[0, 0, 0]
+    w = np.exp(logit - logit.max())
+    w /= w.sum()
+    o, A, U = w @ val, w @ np.abs(val), 23 * (w @ unit)
+    ku, qa = ref.units(host[1], 1.0)[:, 0], np.abs(ref.f64(q)[0, 0, 0])
+    off = ((D + 8) * 2.0 ** -23 * 23 * (ku @ qa) + 2.0 ** -25 * qa.max() * np.abs(k).sum(1)
+           + 4 * 2.0 ** -24 * (np.abs(logit) + logit.max())).max()
+    small = L * 2.0 ** -25 * 8 * vd * (1 + unit.max() / vd) / 2.0 ** 3 * (1 if dtype == BF16 else 1.5)
+    p = 2.0 ** -10 if dtype == BF16 else 2.0 ** -11 + 2.0 ** -21
+    bound = (torch.finfo(dtype).eps / 2 * np.abs(o) + A * (p + 2 * off) + small
+             + 320 * 2.0 ** -23 * U + (2.0 ** -25 if dtype == FP16 else 0))
+    return q, host, o, bound
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("L,copies,mass,mag,vd,D", [
+    (65536, 1, 0.9, 0.5, 0.125, 128), (8192, 1, 0.99, 4.0, 1.0, 64), (4096, 512, 0.99, 0.5, 0.125, 128),
+    (4096, 600, 0.99, 4.0, 1.0, 32), (1000, 1, 0.995, 0.5, 0.125, 128), (1000, 300, 0.995, 0.5, 0.0625, 64)])
+def test_decode_a_faint_tail_behind_a_sink(L, copies, mass, mag, vd, D, dtype):
+    """Scales of the values between 1 and 448. One query row, and a batch of the same sequence (single-warp teams)."""
+    q, host, want, bound = faint_tail(L, mass, mag, vd, D, dtype, 40)
+    ps = 64
+    n = -(-L // ps)
+    dev = sa.kv4_cache(n, 1, ps, D)
+    for pool, x in zip(dev, (host[0], host[1], host[3], host[4])):
+        pool.view(torch.uint8).flatten(0, 2)[:L] = torch.from_numpy(x[:, 0]).to(DEV)
+    table = np.tile(np.arange(n, dtype=np.int32), (copies, 1))
+    o = run_decode(q.to(DEV).expand(copies, 1, 1, D).contiguous(), dev, table, [L] * copies, L, scale=1.0, vd=vd)
+    err = np.abs(ref.f64(o)[:, 0, 0] - want)
+    assert (err <= bound).all(), (err / bound).max()
+    assert np.linalg.norm(bound) < 0.1 * np.linalg.norm(want)  # the bound says something
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("lens,Hkv", [([900], 1), ([5000, 40], 1), ([3000] * 40, 2)])
+def test_decode_scales_that_rise(lens, Hkv, D, dtype):
+    """Values whose scales run from the smallest to the largest along a sequence, up and down and with single peaks: what
+    the probabilities were kept larger by is given back on the way."""
+    rng = np.random.default_rng(41)
+    ps, L = 32, max(lens)
+    for way in ("up", "down", "peaks"):
+        pages = -(-L // ps)
+        j = np.arange(pages * ps)
+        size = {"up": -9 + 17.5 * j / L, "down": 8.5 - 17.5 * j / L, "peaks": np.where(j % 501 == 77, 8.5, -9 + j % 7)}[way]
+        k = model_rows(rng, (pages * ps, Hkv, D), "k") * 0.5
+        v = rng.uniform(-7.5, 7.5, (pages * ps, Hkv, D)) * np.exp2(np.clip(size, -9, 8.5))[:, None, None]
+        v[..., ::32] = 7.5 * np.exp2(np.clip(size, -9, 8.5))[:, None, None]
+        dev, host = [], []
+        for x, which in ((k, "k"), (v, "v")):
+            codes, byte, _ = ref.quantize(x, 1.0)
+            for y in (ref.pack(codes, which), byte):
+                y = np.ascontiguousarray(y.reshape(pages, ps, Hkv, -1).transpose(0, 2, 1, 3))
+                host.append(y)
+                dev.append(torch.from_numpy(y).to(DEV))
+        dev[1], dev[3] = (x.view(torch.float8_e4m3fn) for x in (dev[1], dev[3]))
+        table = np.tile(np.arange(pages, dtype=np.int32), (len(lens), 1))
+        q = torch.from_numpy(rng.normal(size=(len(lens), 2 * Hkv, 1, D))).to(dtype).to(DEV)
+        o = run_decode(q, dev, table, lens, L, vd=1.0)
+        some = [0, len(lens) - 1]
+        check_decode(o[some], q[some], host, table[some], [lens[b] for b in some], L, vd=1.0)
+
+
 def test_decode_cap_empty_problems_and_no_pages():
     lens = [640, 640]
     q, dev, host, table = case(17, lens, 4, 1, 2, 64, 32, BF16)
