@@ -403,8 +403,10 @@ ATTN_API int attn_decode_paged_fp8(const void* q, const void* k_pages, const voi
  * exact in FP16 and BF16 times descale. k_descale and v_descale are one factor
  * for a whole cache, powers of two 2^-64 .. 2^64 (else ATTN_ERR_SCALE), to be given
  * with the same value to every call; they move the range of the scales
- * (2^-9 .. 448) to that of the data (1 suits magnitudes from 0.1 to a few
- * hundred). Codes lie in a row in units of consecutive elements, 8 in a key row
+ * (2^-9 .. 448) to that of the data. Scales below 2^-6 have fewer bits: 1 suits
+ * keys whose groups reach 0.12 to 3000. Values are better put higher, at scales of
+ * 1 to 400, so groups that reach 7.5 to 3000 times v_descale (1/8 suits 1 to 375):
+ * see attn_decode_paged_kv4 for what smaller scales lose. Codes lie in a row in units of consecutive elements, 8 in a key row
  * (one little-endian 32-bit word) and 4 in a value row (16 bits), the lowest
  * element in the lowest bits; unit u of group i is unit u * (D / 32) + i of the
  * row. A zeroed pool holds zeros.
@@ -477,11 +479,22 @@ ATTN_API int attn_kv4_gather(const void* k_codes, const void* k_scales, const vo
  *   j < sinks. <= 0: none; without a window it changes nothing.
  * The values of the cache enter the products exactly; the query is rounded to
  * FP16 relative to its row's largest element and the probabilities to FP16 before
- * and after their product with a scale (for FP16 outputs at most after it), all sums are
- * FP32. Pages need not be clean: what a query row does not see (behind a
- * sequence's end, in front of its window and no sinks, or a later row's key) may
- * hold anything. A table entry outside [0, num_pages) reads a page of zeros. NaN in
- * a key that a row sees makes that row NaN, in a value the elements of its group.
+ * and after their product with a scale; all sums are FP32. FP16 outputs lose
+ * less: few short sequences, which are left whole (wherever the workspace's size
+ * is 0), carry what both roundings left and are as exact as the output's own
+ * rounding; others carry the first one's (1.4 times that error).
+ * A key whose probability is below 2^-17 / s of the largest one in its part of
+ * the sequence, s the scale of its value, enters with fewer than 11 bits, and one
+ * below 2^-28 / s not at all. At scales from 1 on, what a key with 99 % of a row
+ * leaves to 2^17 others in one part is right to 2^-10; at scales of 1/30 it is off
+ * by a quarter.
+ * Pages need not be clean: what a query row does not see (behind a sequence's
+ * end, in front of its window and no sinks, or a later row's key) may hold
+ * anything. A table entry outside [0, num_pages) reads a page of zeros. NaN in a
+ * key that a row sees makes that row NaN, in a value the elements of its group.
+ * Which of the paged caches: with 8 KV heads and D = 128 this one is faster than
+ * attn_decode_paged_fp8 where a step would read more than about 15 MB of E4M3
+ * cache with one sequence and 130 MB with 8 or 16, and with 64 at any length.
  * D is 32, 64 or 128 (else ATTN_ERR_HEADDIM); B * Hkv <= 65535 and at most
  * 8 * 65535 grouped rows (Hq/Hkv) * M per KV head (else ATTN_ERR_OVERFLOW). Up
  * to 8 grouped rows read the cache once, more in blocks of 8 rows; for many

@@ -36,10 +36,12 @@
 // instructions per 16 keys.) The scales are applied where there are fewer numbers than
 // elements: a key's to the sum of a group's 32 products, a value's to the
 // probabilities, once per group.
-// What bounds it: the expansion, about 310 instructions of a warp per 16 keys of D = 128
-// on pipes that the 21 matrix instructions among them share, issued in 55 of 100 cycles:
-// each waits for the one before. 64 sequences of up to 16384 keys, 8192 on average, 8 KV
-// heads (580 MB): 111 us, 5.2 TB/s, 77 % of the measured copy bandwidth. (Without its
+// What bounds it: instructions that depend on each other. Of about 300 of a warp per 16
+// keys of D = 128, 88 expand codes and 21 are matrix instructions, the rest loads, scales,
+// softmax and sums; the three warps of a scheduler issue in 55 of 100 cycles, as each mostly
+// waits for the instruction before (1.5 warps an issue) or for a busy pipe (0.8), hardly for
+// memory (0.2). 64 sequences of up to 16384 keys, 8192 on average, 8 KV
+// heads (580 MB): 112 us, 5.2 TB/s, 76 % of the measured copy bandwidth. (Without its
 // copies a kernel of 122 us took 115.) 12 warps of 168 registers beat 16 of 128 (139 us
 // where 12 took 122), 20 of 96 and 24 of 80: fewer registers leave the compiler less to
 // overlap in a warp. 16 query rows to a team, for more than
@@ -52,7 +54,9 @@
 // probabilities to FP16, kept 8 to 128 times too large to stay clear of its small
 // numbers (the row sum adds them unrounded), and their products with the values' scales
 // (2^-9 .. 448, so between 2^-6 and 57344 at the largest score) to FP16; with FP16
-// outputs less is lost (kFine).
+// outputs less is lost (kFine). A product is one of FP16's small numbers where the
+// probability is below 2^-17 / scale of the largest one, and zero below 2^-28 / scale:
+// the factor of the values says how much of that range a cache has.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -277,8 +281,8 @@ struct Shares {
 // only before and after a part's tiles takes no registers while they run through them.
 // Every segment counts kPartCost more than its tiles when the tiles are shared out, in front of its first one: that is
 // what a team spends on starting its copies, its query and its sums. 256 ragged sequences of up to 1000 keys, 4 KV
-// heads, D = 64: 22.8 us at a cost of 4, 22.0 at 5, 21.2 at 6, 21.0 at 8; 64 of up to 16384, 8 KV heads, D = 128:
-// 112.3, 111.6, 110.9, 111.3.
+// heads, D = 64: 22.5 us at a cost of 4, 21.7 at 5, 20.8 at 6, 20.9 at 8; 64 of up to 16384, 8 KV heads, D = 128:
+// 113.0, 112.3, 112.1, 112.4.
 struct Part {
     long long u, rem;      // before the part: of all, and of its sequence
     int b, L, hz, t0, t1;  // t0 == t1: no part
@@ -508,9 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
     constexpr int NG = D / kKv4Group;
     // An output in FP16 shows the two roundings of a probability (1.7 times the error of the output's own rounding), one
     // in BF16 does not. For FP16 the first one's remainder is carried into the second (1.4 times, and 1 % of the time).
-    // Whole segments, whose time is mostly latency, multiply the second one's remainder too (1.0 times: 300 keys 5.6 us
-    // for 5.3, 8 sequences of up to 1000 keys, D = 128, 11.9 for 10.6); for 16 sequences of 8192 keys with 16 rows each
-    // that would be 46.6 us for 39.5.
+    // Whole segments, whose time is mostly latency, multiply the second one's remainder too (1.0 times: 300 keys 5.4 us
+    // for 5.2, 8 sequences of up to 1000 keys, D = 128, 11.8 for 10.6); for 16 sequences of up to 8192 keys with 16 rows
+    // each that would be 48.8 us for 40.2.
     constexpr bool kFine = is_half<T>, kFinest = kFine && kWhole;
     extern __shared__ __align__(16) uint8_t smem_of_block[];
     constexpr int kTile = tile_of(W);
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_decode_kernel(const __grid_co
 
         // One step: N blocks of 16 keys, the first at j0, from the stages at st. `edge`: some row does not see some of
         // them. Two blocks at a time wherever both are seen by every row: their products do not depend on each other, and
-        // one test of the maximum serves both (64 ragged sequences of up to 16384 keys: 111 us, 116 one at a time).
+        // one test of the maximum serves both (64 ragged sequences of up to 16384 keys: 112 us, 123 one at a time).
         const auto step = [&](uint32_t st, auto n_tag, int j0, auto edge_tag) {
             constexpr bool edge = decltype(edge_tag)::value;
             constexpr int N = decltype(n_tag)::value;
@@ -1075,13 +1079,14 @@ int sm_count() {
 int row_blocks(const Problem& p) { return (int)(((long long)p.G * p.M + ROWS - 1) / ROWS); }
 
 // Few short segments are left whole, one to a team of four warps: no sums of costs, no second kernel. Microseconds whole
-// and cut, 2 KV heads of one sequence, D = 64: 300 keys (5 tiles) 5.1 and 7.7, 1000 (16 tiles) 8.4 and 8.0, 2000 12.7 and
-// 8.1; 64 KV heads (8 sequences), D = 128: 6.9 and 10.5, 11.0 and 11.2, 16.6 and 13.2; 456 of 900 keys 17.2 and 23.0.
+// and cut, 2 KV heads of one sequence, D = 64, FP16: 300 keys (5 tiles) 5.4 and 7.8, 1000 (16 tiles) 8.9 and 8.1, 2000
+// 13.9 and 8.2; 64 KV heads (8 sequences), D = 128: 6.8 and 10.5, 11.0 and 11.3, 16.6 and 13.2; 456 of 900 keys 17.1 and
+// 23.0.
 // Otherwise a team is one warp where a segment is cut into kManyParts parts or less on average, and four warps (a
-// quarter of the parts) where there are fewer segments. With one and with four, D = 128: 8 segments of 131072 keys 38.6
-// and 35.6; 16 of 4096 11.3 and 11.1; 32 of 32768 35.4 and 36.7; 64 of 2048 11.4 and 12.9; 128 of up to 8192 24.2 and
-// 24.6; 512 of up to 16384 110.9 and 115.4; at D = 64 30.1 and 26.5 (8), 26.9 and 26.5 (32), 10.1 and 10.3 (64 of 2048),
-// 18.8 and 18.6 (128), 21.2 and 25.1 (1024 of up to 1000).
+// quarter of the parts) where there are fewer segments. With one and with four, D = 128: 8 segments of 131072 keys 38.7
+// and 35.0; 16 of 4096 11.3 and 11.0; 32 of 32768 35.5 and 36.0; 64 of 2048 13.5 and 14.0; 128 of up to 8192 24.3
+// and 24.2; 512 of up to 16384 112.2 and 114.3; at D = 64 30.4 and 26.3 (8), 27.2 and 26.4 (32), 11.5 and 11.1 (64), 18.9
+// and 18.6 (128), 20.9 and 24.8 (1024 of up to 1000).
 struct Plan {
     int blocks, warps;  // warps of a team
     bool whole;

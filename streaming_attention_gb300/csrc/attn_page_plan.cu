@@ -274,9 +274,10 @@ int attn_page_plan(const int* cached_lens, const int* new_lens, const int* free_
     }
     const PlanArgs a{cached_lens, new_lens, free_pages, block_table, seq_lens, row_starts, slot_map, stats,
                      B, page_size, max_pages, num_free, num_rows, (uint32_t)((kI32Max - (page_size - 1)) / page_size)};
-    // one row per thread, on at most one block per SM, one of them the block that counts. Few requests take smaller blocks, whose sums are quicker; many
-    // take larger ones, and so fewer chunks one after the other: 64 requests 3.0 us in blocks of 256 threads and 4.8 in
-    // blocks of 1024, 256 3.1 and 5.0, 512 5.1 and 5.5, 2000 18.0 and 7.4.
+    // one row per thread, on at most one block per SM, and the block that counts. Few requests take smaller blocks, whose
+    // sums are quicker; many take larger ones, and so fewer chunks one after the other: 64 requests 2.7 us in blocks of 256
+    // threads and 4.2 in blocks of 1024, 256 3.0 and 4.4, 512 (two chunks) 4.8 and 4.8, 513 5.9 and 4.8, 2000 of 97 new
+    // keys each 16.8 and 6.5.
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
     const int threads = B <= 512 ? 256 : 1024;
